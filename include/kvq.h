@@ -324,6 +324,178 @@ kvq_status kvq_destroy(kvq_handle* h);
 
 const char* kvq_status_string(kvq_status s);
 
+/* ------------------------------------------------------------------ pages
+ *
+ * A paged cache: the rows of every sequence live in pages of page_size tokens
+ * that a table names, so that sequences of any lengths share one pool, join
+ * and leave a running batch, and share full pages of a common prefix.  Every
+ * layer has its own (k_bits, v_bits): 16 keeps rows in the cache's type;
+ * 8, 4 and 2 quantize every row when it is appended, keys and values per token
+ * over their head_dim channels (the per-token-asym mode of KVQ_KEY_PER_TOKEN:
+ * KVTuner sections A3-A4), with no FP16 window.
+ *
+ * Shared by the paged entry points:
+ *   - Lengths, tables and rows are read on the device: nothing of a call but
+ *     pointers, strides and counts is fixed on the host, so a captured call
+ *     follows the tensors it was captured with.
+ *   - The handle is not changed by any call after kvq_paged_create(): calls on
+ *     it may come from several threads and streams.  The caller orders calls
+ *     that append to a page with those that read or append to the same page.
+ *   - The current device must be the one of kvq_paged_create() (KVQ_ERR_ARG).
+ *   - What only the device can see (a page number outside the pool, a length
+ *     past the table's width, a position past the rotation's table, fewer
+ *     tokens in a sequence than it has new rows) is never followed:
+ *     kvq_paged_device_error() reports it, an append or a read leaves the row
+ *     out, and what attention returns for that sequence has no meaning. */
+
+#define KVQ_FP16 0
+#define KVQ_BF16 1
+
+/* k_bits, v_bits: both 16, or both in {2, 4, 8} (KVQ_ERR_UNSUPPORTED for a
+ * 16 beside a smaller width, KVQ_ERR_BITS for any other). */
+typedef struct {
+  uint8_t k_bits;
+  uint8_t v_bits;
+} kvq_paged_layer_cfg;
+
+/* num_q_heads % num_kv_heads == 0 and num_q_heads / num_kv_heads <= 8;
+ * head_dim in {64, 128}; page_size in {16, 32, 64, 128};
+ * dtype: KVQ_FP16 or KVQ_BF16, the type of q, K, V, out and of 16-bit rows. */
+typedef struct {
+  int32_t num_layers;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;   /* pages of each layer */
+  int32_t dtype;
+  const kvq_paged_layer_cfg* layers;
+} kvq_paged_config;
+
+typedef struct kvq_paged kvq_paged;
+
+/* Device layout of one layer: page p's part of kv head h starts at
+ * pages + p * page_stride + h * head_stride and holds page_size / 16 tiles of
+ * tile_bytes, 16 consecutive tokens each.  The tile of tokens i = 0 .. 15:
+ *   16-bit rows: [K: 16 rows][V: 16 rows] of head_dim values; the 16-byte chunk
+ *     c of token i is stored at chunk c ^ (i & 7) of row i.
+ *   quantized:   [K codes: 16 rows][V codes: 16 rows][16 x (K scale, K zero,
+ *     V scale, V zero) fp16], code rows of head_dim * bits / 8 bytes, least
+ *     significant field first.  The key row and the scales of token i sit at
+ *     row r(i) = 2 (i & 3) + (i >> 2 & 1) + (i & 8), its value row at row i.
+ *     128-byte key rows: on odd r the 64-byte halves are exchanged.  Value
+ *     rows keep their 32-byte block b at b ^ (i & 3) (128-byte rows) or at
+ *     b ^ (i >> 1 & 1) (64-byte rows). */
+typedef struct {
+  int32_t k_bits, v_bits, page_size, head_dim;
+  int64_t tile_bytes, head_stride, page_stride;
+  void* pages;
+} kvq_paged_view;
+
+/* The sequences that a call works on.  All pointers are device memory.
+ *   page_table: [num_seqs] rows of max_pages page numbers, table_stride
+ *     elements apart; entry k of a row holds positions k * page_size .. .
+ *     Entries past a sequence's last page are not read.
+ *   seq_lens: [num_seqs] tokens of each sequence, the new ones included.
+ *   cu_tokens: [num_seqs + 1] ascending, or NULL.  Rows cu_tokens[s] ..
+ *     cu_tokens[s + 1] - 1 of a call's row tensors are the newest tokens of
+ *     sequence s, oldest first; NULL: row s is the newest token of sequence s
+ *     (none where seq_lens[s] is 0).  Rows that belong to no sequence, such as
+ *     padding behind the last one, are neither read nor written. */
+typedef struct {
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  const int32_t* cu_tokens;
+  int32_t num_seqs;
+  int32_t max_pages;
+} kvq_paged_batch;
+
+/* Rotation of queries and keys by their position.
+ *   table: device fp32 [rows][dim]: dim / 2 cosines, then dim / 2 sines, of
+ *     each position's angles; 16-byte aligned.
+ *   positions: device [n_tokens], each row's position, or NULL: its place in
+ *     its sequence.
+ *   dim: channels that turn, the first `dim` of a row, a multiple of 16;
+ *     interleaved 0 pairs channel i with i + dim / 2, 1 pairs 2i with 2i + 1.
+ * (a, b) becomes (a cos - b sin, b cos + a sin) in fp32, rounded once. */
+typedef struct {
+  const float* table;
+  const int32_t* positions;
+  int32_t rows;
+  int32_t dim;
+  int32_t interleaved;
+} kvq_rotation;
+
+/* A tensor of rows: row i's head h starts at data + (i * token_stride + h *
+ * head_stride) elements; its head_dim values are contiguous. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} kvq_rows;
+
+/* Bytes of the caller's device buffer (0 if cfg is invalid): every layer's
+ * pages, layer 0 first, each layer 256-byte aligned, then 256 bytes of the
+ * library's own. */
+size_t kvq_paged_bytes(const kvq_paged_config* cfg);
+
+/* Validates `cfg` and writes a handle on the pages in `dev_buf` (256-byte
+ * aligned, caller-owned) to *out.  What the pages hold stays: a page's slots
+ * mean nothing until they are appended to, whatever they hold.  Clears the
+ * error word (synchronizes once). */
+kvq_status kvq_paged_create(const kvq_paged_config* cfg, void* dev_buf, size_t bytes, kvq_paged** out);
+
+/* Appends the new rows of every sequence of `batch` to `layer`: keys turned by
+ * `rotation` (NULL: as they are), rounded to the cache's type or quantized,
+ * and written to their slots with the values; queries turned alike into q_out.
+ *   K, V: [n_tokens][num_kv_heads] rows.  q, q_out: [n_tokens][num_q_heads]
+ *     rows, or both NULL; q_out may be q itself, and overlaps nothing else.
+ *   n_tokens: rows of the tensors; without cu_tokens, equal to num_seqs.
+ * Rows need only their type's alignment; 16-byte aligned rows are faster.
+ * Quantized rows are taken in fp16 (clamped to +-65504): zero = min,
+ * scale = fp16((max - min) / (2^b - 1)), code = clamp(rint((x - zero) /
+ * scale), 0, 2^b - 1), as kvq_append does per token; a row with a NaN gets
+ * NaN scales.  Two rows of one call with the same slot (one page in the tables
+ * of two sequences that both append to it) leave one of them or a mixture
+ * there. */
+kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K,
+                            const kvq_rows* V, const kvq_rows* q, const kvq_rows* q_out,
+                            const kvq_rotation* rotation, int n_tokens, void* stream);
+
+/* Attention of one query token per sequence, the newest one, over its pages:
+ * positions max(0, len - window) .. len - 1 (window 0: all of them).
+ *   q: [num_seqs][num_q_heads] rows (cu_tokens is not looked at).
+ *   out: [num_seqs][num_q_heads][head_dim] contiguous, 16-byte aligned, the
+ *     cache's type; lse: fp32 [num_seqs][num_q_heads] or NULL: the natural
+ *     logarithm of the sum of exp(scale * q.k).  A sequence with no token gets
+ *     0, and -infinity.
+ *   scale: multiplies the scores; 0 means 1 / sqrt(head_dim).
+ *   workspace: device scratch of kvq_paged_workspace_bytes(h, num_seqs) bytes,
+ *     256-byte aligned, whatever it holds; not shared with a call in flight. */
+kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* q, void* out,
+                                 float* lse, float scale, int window, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Bytes of the workspace above (0 if h is null or num_seqs < 1). */
+size_t kvq_paged_workspace_bytes(const kvq_paged* h, int num_seqs);
+
+/* Reads the newest rows of every sequence (cu_tokens as for an append) back as
+ * the cache holds them: code * scale + zero in fp32, rounded once to the
+ * cache's type.  K, V: [n_tokens][num_kv_heads] rows; either may be NULL.
+ * Rows with a bad page are left as they were. */
+kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K, const kvq_rows* V,
+                          int n_tokens, void* stream);
+
+kvq_status kvq_paged_view_get(const kvq_paged* h, int layer, kvq_paged_view* v);
+
+/* Reads and clears the error word, synchronizing `stream`: 0, or 1 a device
+ * wait gave up, 2 a length or a row count that the batch's tensors cannot
+ * mean, 4 a bad page number, 5 a position outside the rotation's table. */
+kvq_status kvq_paged_device_error(kvq_paged* h, int32_t* code, void* stream);
+
+kvq_status kvq_paged_destroy(kvq_paged* h);
+
 #ifdef __cplusplus
 }
 #endif

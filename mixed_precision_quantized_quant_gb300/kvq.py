@@ -28,6 +28,8 @@ EXPORTS = (
     "kvq_destroy", "kvq_status_string", "kvq_decode_attn_noalloc", "kvq_chunk_attn",
     "kvq_selftest_bounded_wait", "kvq_chunk_workspace_bytes", "kvq_state_bytes", "kvq_state_save",
     "kvq_state_restore",
+    "kvq_paged_bytes", "kvq_paged_create", "kvq_paged_append", "kvq_paged_decode_attn", "kvq_paged_workspace_bytes",
+    "kvq_paged_read", "kvq_paged_view_get", "kvq_paged_device_error", "kvq_paged_destroy",
 )
 
 
@@ -62,6 +64,39 @@ class LayerView(ctypes.Structure):
                 ("records", ctypes.c_void_p), ("residual_k", ctypes.c_void_p),
                 ("residual_v", ctypes.c_void_p), ("window_bound", ctypes.c_int32),
                 ("rpc_percent", ctypes.c_int32)]
+
+
+KVQ_FP16, KVQ_BF16 = 0, 1
+
+
+class PagedLayerCfg(ctypes.Structure):
+    _fields_ = [("k_bits", ctypes.c_uint8), ("v_bits", ctypes.c_uint8)]
+
+
+class PagedConfig(ctypes.Structure):
+    _fields_ = [("num_layers", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("layers", ctypes.POINTER(PagedLayerCfg))]
+
+
+class PagedView(ctypes.Structure):
+    _fields_ = [("k_bits", ctypes.c_int32), ("v_bits", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("tile_bytes", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("pages", ctypes.c_void_p)]
+
+
+class PagedBatchArgs(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
+                ("cu_tokens", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class RotationArgs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -113,6 +148,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.kvq_destroy.restype = ctypes.c_int
     L.kvq_status_string.argtypes = [ctypes.c_int]
     L.kvq_status_string.restype = ctypes.c_char_p
+    batch, rows = ctypes.POINTER(PagedBatchArgs), ctypes.POINTER(Rows)
+    L.kvq_paged_bytes.argtypes = [ctypes.POINTER(PagedConfig)]
+    L.kvq_paged_bytes.restype = ctypes.c_size_t
+    L.kvq_paged_create.argtypes = [ctypes.POINTER(PagedConfig), vp, ctypes.c_size_t, ctypes.POINTER(vp)]
+    L.kvq_paged_create.restype = ctypes.c_int
+    L.kvq_paged_append.argtypes = [vp, ctypes.c_int, batch, rows, rows, rows, rows, ctypes.POINTER(RotationArgs),
+                                   ctypes.c_int, vp]
+    L.kvq_paged_append.restype = ctypes.c_int
+    L.kvq_paged_decode_attn.argtypes = [vp, ctypes.c_int, batch, rows, vp, vp, ctypes.c_float, ctypes.c_int, vp,
+                                        ctypes.c_size_t, vp]
+    L.kvq_paged_decode_attn.restype = ctypes.c_int
+    L.kvq_paged_workspace_bytes.argtypes = [vp, ctypes.c_int]
+    L.kvq_paged_workspace_bytes.restype = ctypes.c_size_t
+    L.kvq_paged_read.argtypes = [vp, ctypes.c_int, batch, rows, rows, ctypes.c_int, vp]
+    L.kvq_paged_read.restype = ctypes.c_int
+    L.kvq_paged_view_get.argtypes = [vp, ctypes.c_int, ctypes.POINTER(PagedView)]
+    L.kvq_paged_view_get.restype = ctypes.c_int
+    L.kvq_paged_device_error.argtypes = [vp, ctypes.POINTER(i32), vp]
+    L.kvq_paged_device_error.restype = ctypes.c_int
+    L.kvq_paged_destroy.argtypes = [vp]
+    L.kvq_paged_destroy.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -217,6 +273,65 @@ def kvq_state_restore(h: int, src: int, stream: int) -> None:
 
 def kvq_destroy(h: int) -> None:
     _check(load().kvq_destroy(h), "kvq_destroy")
+
+
+def make_paged_config(layers: Sequence[Tuple[int, int]], num_q_heads: int, num_kv_heads: int, head_dim: int,
+                      page_size: int, num_pages: int, dtype: int = KVQ_FP16):
+    """layers: (k_bits, v_bits) per layer; dtype: KVQ_FP16 or KVQ_BF16."""
+    arr = (PagedLayerCfg * len(layers))()
+    for i, (kb, vb) in enumerate(layers):
+        arr[i].k_bits, arr[i].v_bits = kb, vb
+    cfg = PagedConfig(len(layers), num_q_heads, num_kv_heads, head_dim, page_size, num_pages, dtype,
+                      ctypes.cast(arr, ctypes.POINTER(PagedLayerCfg)))
+    cfg._keep = arr
+    return cfg
+
+
+def kvq_paged_bytes(cfg: PagedConfig) -> int:
+    return int(load().kvq_paged_bytes(ctypes.byref(cfg)))
+
+
+def kvq_paged_create(cfg: PagedConfig, dev_buf: int, nbytes: int) -> int:
+    h = ctypes.c_void_p()
+    _check(load().kvq_paged_create(ctypes.byref(cfg), ctypes.c_void_p(dev_buf), nbytes, ctypes.byref(h)),
+           "kvq_paged_create")
+    return h.value
+
+
+def kvq_paged_append(h: int, layer: int, batch: PagedBatchArgs, K: Rows, V: Rows, q: Optional[Rows],
+                     q_out: Optional[Rows], rotation: Optional[RotationArgs], n_tokens: int, stream: int) -> None:
+    _check(load().kvq_paged_append(h, layer, batch, K, V, q, q_out, rotation, n_tokens, stream), "kvq_paged_append")
+
+
+def kvq_paged_decode_attn(h: int, layer: int, batch: PagedBatchArgs, q: Rows, out: int, lse: Optional[int],
+                          scale: float, window: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(load().kvq_paged_decode_attn(h, layer, batch, q, out, lse, scale, window, workspace, workspace_bytes,
+                                        stream), "kvq_paged_decode_attn")
+
+
+def kvq_paged_workspace_bytes(h: int, num_seqs: int) -> int:
+    return int(load().kvq_paged_workspace_bytes(h, num_seqs))
+
+
+def kvq_paged_read(h: int, layer: int, batch: PagedBatchArgs, K: Optional[Rows], V: Optional[Rows], n_tokens: int,
+                   stream: int) -> None:
+    _check(load().kvq_paged_read(h, layer, batch, K, V, n_tokens, stream), "kvq_paged_read")
+
+
+def kvq_paged_view_get(h: int, layer: int) -> dict:
+    v = PagedView()
+    _check(load().kvq_paged_view_get(h, layer, ctypes.byref(v)), "kvq_paged_view_get")
+    return {name: getattr(v, name) for name, _ in PagedView._fields_}
+
+
+def kvq_paged_device_error(h: int, stream: int) -> int:
+    code = ctypes.c_int32(0)
+    _check(load().kvq_paged_device_error(h, ctypes.byref(code), stream), "kvq_paged_device_error")
+    return code.value
+
+
+def kvq_paged_destroy(h: int) -> None:
+    _check(load().kvq_paged_destroy(h), "kvq_paged_destroy")
 
 
 def kvq_status_string(s: int) -> str:
@@ -334,6 +449,242 @@ class KVQCache:
     def close(self) -> None:
         if getattr(self, "h", None):
             kvq_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _device_tensor(t, name: str, dtype, device, ndim: int) -> None:
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+
+
+class PagedBatch:
+    """The sequences that calls of a ``KVQPagedCache`` work on: int32 CUDA
+    tensors, read on the device at every call (one batch serves every layer,
+    and a captured step follows what is copied into them later).
+
+    page_table [S, max_pages]: page of every page_size positions;
+    seq_lens [S]: tokens of each sequence, the new ones included;
+    cu_tokens [S + 1] or None: rows cu_tokens[s] .. cu_tokens[s+1] - 1 of an
+    append's or a read's tensors are the newest of sequence s (None: row s)."""
+
+    def __init__(self, page_table, seq_lens, cu_tokens=None):
+        import torch
+        dev = page_table.device
+        if dev.type != "cuda":
+            raise ValueError("page_table must be a CUDA tensor")
+        _device_tensor(page_table, "page_table", torch.int32, dev, 2)
+        _device_tensor(seq_lens, "seq_lens", torch.int32, dev, 1)
+        S, width = page_table.shape
+        if S < 1 or width < 1:
+            raise ValueError(f"page_table has shape {tuple(page_table.shape)}: at least one sequence and one page")
+        if width > 1 and page_table.stride(1) != 1:
+            raise ValueError("page_table rows must be contiguous")
+        stride = page_table.stride(0) if S > 1 else width
+        if stride < width:
+            raise ValueError("page_table rows must not overlap")
+        if tuple(seq_lens.shape) != (S,) or not seq_lens.is_contiguous():
+            raise ValueError(f"seq_lens must be contiguous of shape {(S,)}")
+        if cu_tokens is not None:
+            _device_tensor(cu_tokens, "cu_tokens", torch.int32, dev, 1)
+            if tuple(cu_tokens.shape) != (S + 1,) or not cu_tokens.is_contiguous():
+                raise ValueError(f"cu_tokens must be contiguous of shape {(S + 1,)}")
+        self.device, self.num_seqs = dev, S
+        self._keep = (page_table, seq_lens, cu_tokens)
+        self.args = PagedBatchArgs(page_table.data_ptr(), stride, seq_lens.data_ptr(),
+                                   None if cu_tokens is None else cu_tokens.data_ptr(), S, width)
+
+
+class Rotation:
+    """The position rotation of an append: table fp32 [rows, dim] on the GPU,
+    dim / 2 cosines then dim / 2 sines of each position's angles (see
+    ``rotation_table``); positions int32 [n_tokens] or None (each row's place
+    in its sequence); interleaved pairs channels (2i, 2i+1) instead of
+    (i, i + dim/2)."""
+
+    def __init__(self, table, interleaved: bool = False, positions=None):
+        import torch
+        if table.device.type != "cuda":
+            raise ValueError("table must be a CUDA tensor")
+        _device_tensor(table, "table", torch.float32, table.device, 2)
+        rows, dim = table.shape
+        if not table.is_contiguous() or rows < 1:
+            raise ValueError("table must be contiguous with at least one row")
+        if dim < 16 or dim % 16:
+            raise ValueError(f"table has {dim} columns: a multiple of 16 is needed")
+        self.positions = None
+        if positions is not None:
+            _device_tensor(positions, "positions", torch.int32, table.device, 1)
+            if not positions.is_contiguous():
+                raise ValueError("positions must be contiguous")
+            self.positions = positions
+        self.table, self.dim = table, dim
+        self.args = RotationArgs(table.data_ptr(), None if positions is None else positions.data_ptr(), rows, dim,
+                                 int(bool(interleaved)))
+
+
+def rotation_table(rows: int, dim: int, base: float = 10000.0, device="cuda"):
+    """Cosines and sines of p * base^(-2i/dim) for positions p < rows, in the
+    form ``Rotation`` takes; the angles are formed in 64 bits (far positions
+    lose theirs in 32)."""
+    import torch
+    inv = base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    ang = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+
+
+class KVQPagedCache:
+    """A paged cache of ``num_pages`` pages of ``page_size`` tokens per layer,
+    each layer at its own (k_bits, v_bits): (16, 16) keeps rows in ``dtype``,
+    smaller pairs from {2, 4, 8} quantize them per token (see include/kvq.h).
+    ``buffer``: uint8 CUDA tensor of ``nbytes`` bytes to use, else one is made.
+    Which pages belong to which sequence is the caller's: a call takes a
+    ``PagedBatch``.  Tensors of rows are [n, heads, head_dim] with contiguous
+    head_dim, such as slices of a projection's output."""
+
+    def __init__(self, layers: Sequence[Tuple[int, int]], num_q_heads: int, num_kv_heads: int, head_dim: int,
+                 page_size: int, num_pages: int, dtype=None, device="cuda", buffer=None):
+        import torch
+        self.h = None
+        dtype = torch.float16 if dtype is None else dtype
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+        self.layers = [tuple(x) for x in layers]
+        self.Hq, self.Hkv, self.D, self.P = num_q_heads, num_kv_heads, head_dim, page_size
+        self.num_pages, self.dtype = num_pages, dtype
+        self.cfg = make_paged_config(self.layers, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                                     KVQ_FP16 if dtype == torch.float16 else KVQ_BF16)
+        self.nbytes = kvq_paged_bytes(self.cfg)
+        if self.nbytes == 0:
+            raise KVQError(1, "kvq_paged_bytes")
+        if buffer is None:
+            buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        elif not buffer.is_cuda or buffer.dtype != torch.uint8 or buffer.dim() != 1 or not buffer.is_contiguous():
+            raise ValueError("buffer must be a contiguous one-dimensional uint8 CUDA tensor")
+        self.buf, self.device = buffer, buffer.device
+        with torch.cuda.device(self.device):
+            # the library writes its own bytes with the device idle behind it
+            torch.cuda.current_stream().synchronize()
+            self.h = kvq_paged_create(self.cfg, int(buffer.data_ptr()), buffer.numel())
+        self._ws = {}  # num_seqs -> workspace bytes
+
+    def _rows(self, t, name: str, n: int, heads: int) -> Rows:
+        if t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"{name} must be {self.dtype} on {self.device}, got {t.dtype} on {t.device}")
+        if tuple(t.shape) != (n, heads, self.D):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, self.D)}")
+        a, b, c = t.stride()
+        if c != 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+        return Rows(t.data_ptr(), a, b)
+
+    def _new(self, stream, shape, dtype=None):
+        """An output or scratch tensor that the allocator ties to the call's stream."""
+        import torch
+        if stream is None:
+            return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
+
+    def _batch(self, batch: PagedBatch) -> PagedBatchArgs:
+        if batch.device != self.device:
+            raise ValueError(f"batch must be on {self.device}, got {batch.device}")
+        return batch.args
+
+    def _call(self, stream, fn) -> None:
+        """fn(stream pointer) with the cache's device current."""
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            return fn((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        with torch.cuda.device(self.device):
+            return fn((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+
+    def append(self, layer: int, batch: PagedBatch, K, V, q=None, rotation: Optional[Rotation] = None, q_out=None,
+               stream=None):
+        """Appends the newest rows of every sequence: K, V [n, Hkv, d]; returns
+        q [n, Hq, d] turned by ``rotation`` (into ``q_out``, which may be q), or
+        None without q.  Rows of q_out that belong to no sequence are not
+        written."""
+        n = K.shape[0]
+        k, v = self._rows(K, "K", n, self.Hkv), self._rows(V, "V", n, self.Hkv)
+        b = self._batch(batch)
+        if b.cu_tokens is None and n != batch.num_seqs:
+            raise ValueError(f"K has {n} rows, expected one for each of {batch.num_seqs} sequences")
+        r = None
+        if rotation is not None:
+            if rotation.table.device != self.device or rotation.dim > self.D:
+                raise ValueError(f"rotation must be on {self.device} and turn at most {self.D} channels")
+            if rotation.positions is not None and rotation.positions.numel() < n:
+                raise ValueError(f"rotation has {rotation.positions.numel()} positions, expected {n}")
+            r = rotation.args
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+            self._call(stream, lambda s: kvq_paged_append(self.h, layer, b, k, v, None, None, r, n, s))
+            return None
+        qr = self._rows(q, "q", n, self.Hq)
+        if q_out is None:
+            q_out = self._new(stream, (n, self.Hq, self.D))
+        qo = self._rows(q_out, "q_out", n, self.Hq)
+        self._call(stream, lambda s: kvq_paged_append(self.h, layer, b, k, v, qr, qo, r, n, s))
+        return q_out
+
+    def decode_attn(self, layer: int, batch: PagedBatch, q, out=None, scale: float = 0.0, window: int = 0,
+                    return_lse: bool = False, stream=None):
+        """Attention of one query per sequence over its newest ``window``
+        tokens (0: all): q [S, Hq, d] -> [S, Hq, d] in the cache's dtype, and
+        with return_lse (out, fp32 [S, Hq] log-sum-exp of the scaled scores)."""
+        import torch
+        S = batch.num_seqs
+        b = self._batch(batch)
+        qr = self._rows(q, "q", S, self.Hq)
+        nws = self._ws.get(S)
+        if nws is None:
+            nws = self._ws[S] = kvq_paged_workspace_bytes(self.h, S)
+        # every call has a workspace of its own, so that calls on several
+        # streams, or of several captured graphs, never share one
+        ws = self._new(stream, (nws,), torch.uint8)
+        lse = self._new(stream, (S, self.Hq), torch.float32) if return_lse else None
+        if out is None:
+            out = self._new(stream, (S, self.Hq, self.D))
+        elif out.dtype != self.dtype or out.device != self.device or tuple(out.shape) != (S, self.Hq, self.D) or \
+                not out.is_contiguous():
+            raise ValueError(f"out must be contiguous {self.dtype} of shape {(S, self.Hq, self.D)} on {self.device}")
+        self._call(stream, lambda s: kvq_paged_decode_attn(
+            self.h, layer, b, qr, out.data_ptr(), lse.data_ptr() if return_lse else None, scale, window,
+            ws.data_ptr(), nws, s))
+        return (out, lse) if return_lse else out
+
+    def read(self, layer: int, batch: PagedBatch, n: int, K=None, V=None, stream=None):
+        """The newest rows of every sequence as the cache holds them: (K, V),
+        [n, Hkv, d] in the cache's dtype; rows that belong to no sequence are
+        not written."""
+        b = self._batch(batch)
+        if b.cu_tokens is None and n != batch.num_seqs:
+            raise ValueError(f"n is {n}, expected one row for each of {batch.num_seqs} sequences")
+        K, V = (self._new(stream, (n, self.Hkv, self.D)) if t is None else t for t in (K, V))
+        k, v = self._rows(K, "K", n, self.Hkv), self._rows(V, "V", n, self.Hkv)
+        self._call(stream, lambda s: kvq_paged_read(self.h, layer, b, k, v, n, s))
+        return K, V
+
+    def view(self, layer: int) -> dict:
+        return kvq_paged_view_get(self.h, layer)
+
+    def device_error(self, stream=None) -> int:
+        return self._call(stream, lambda s: kvq_paged_device_error(self.h, s))
+
+    def close(self) -> None:
+        if getattr(self, "h", None):
+            kvq_paged_destroy(self.h)
             self.h = None
 
     def __del__(self):
