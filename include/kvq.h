@@ -395,7 +395,9 @@ typedef struct {
 /* The sequences that a call works on.  All pointers are device memory.
  *   page_table: [num_seqs] rows of max_pages page numbers, table_stride
  *     elements apart; entry k of a row holds positions k * page_size .. .
- *     Entries past a sequence's last page are not read.
+ *     Entries past a sequence's last page, and in attention those of pages
+ *     wholly before its window, are not read.  max_pages * page_size is at
+ *     most 2^30.
  *   seq_lens: [num_seqs] tokens of each sequence, the new ones included.
  *   cu_tokens: [num_seqs + 1] ascending, or NULL.  Rows cu_tokens[s] ..
  *     cu_tokens[s + 1] - 1 of a call's row tensors are the newest tokens of

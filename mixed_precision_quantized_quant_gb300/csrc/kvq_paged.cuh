@@ -71,7 +71,8 @@ struct PagedAttnParams {
   float alpha;            // scale * log2(e)
   int window;             // 0: all
   int hkv, gqa;
-  uint8_t* ws;
+  uint8_t* ws;             // what the join needs of every unit, then partial results
+  int64_t ws_partials;    // where those start
 };
 
 // ---------------------------------------------------------------- tile layout
@@ -118,7 +119,9 @@ struct Num<__nv_bfloat16> {
 
 cudaError_t paged_append_launch(const PagedAppendParams& p, int D, int dtype, cudaStream_t s);
 cudaError_t paged_read_launch(const PagedReadParams& p, int D, int dtype, cudaStream_t s);
-cudaError_t paged_attn_launch(const PagedAttnParams& p, int D, int dtype, int sms, cudaStream_t s);
-size_t paged_attn_workspace(int D, int gqa, int hkv, int seqs, int sms);
+// Makes a layer's attention kernel ready on the current device; once, at creation.
+cudaError_t paged_attn_prepare(int kb, int vb, int D, int dtype);
+cudaError_t paged_attn_launch(PagedAttnParams p, int D, int dtype, int sms, cudaStream_t s);
+size_t paged_attn_workspace(int D, int hkv, int seqs, int sms);
 
 }  // namespace kvq

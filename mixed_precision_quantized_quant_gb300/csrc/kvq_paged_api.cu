@@ -90,8 +90,10 @@ kvq_status open_call(const kvq_paged* h, int layer, const kvq_paged_batch* b, kv
   if (!h || layer < 0 || layer >= h->cfg.num_layers || !b) return KVQ_ERR_ARG;
   if (b->num_seqs < 1 || b->max_pages < 1 || b->table_stride < b->max_pages || !b->page_table || !b->seq_lens)
     return KVQ_ERR_ARG;
-  // positions are held in 32 bits
-  if (static_cast<int64_t>(b->max_pages) * h->cfg.page_size > INT_MAX) return KVQ_ERR_ARG;
+  // positions, with room to round them up to a chunk, and units are held in 32 bits
+  if (static_cast<int64_t>(b->max_pages) * h->cfg.page_size > INT_MAX / 2 ||
+      static_cast<int64_t>(b->num_seqs) * h->cfg.num_kv_heads > INT_MAX)
+    return KVQ_ERR_ARG;
   int cur = -1;
   if (cudaGetDevice(&cur) != cudaSuccess) return KVQ_ERR_CUDA;
   if (cur != h->device) return KVQ_ERR_ARG;
@@ -157,7 +159,13 @@ kvq_status kvq_paged_create(const kvq_paged_config* cfg, void* dev_buf, size_t b
   h->cfg.layers = nullptr;
   h->base = static_cast<uint8_t*>(dev_buf);
   int64_t off = 0;
-  for (int l = 0; l < cfg->num_layers; ++l) layer_plan(cfg, l, off, &h->layers[l], &off);
+  for (int l = 0; l < cfg->num_layers; ++l) {
+    layer_plan(cfg, l, off, &h->layers[l], &off);
+    if (kvq::paged_attn_prepare(h->layers[l].kb, h->layers[l].vb, cfg->head_dim, cfg->dtype) != cudaSuccess) {
+      delete h;
+      return KVQ_ERR_CUDA;
+    }
+  }
   h->err = reinterpret_cast<int32_t*>(h->base + off);
   if (cudaGetDevice(&h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
@@ -202,7 +210,7 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
 
 size_t kvq_paged_workspace_bytes(const kvq_paged* h, int num_seqs) {
   if (!h || num_seqs < 1) return 0;
-  return kvq::paged_attn_workspace(h->cfg.head_dim, h->cfg.num_q_heads / h->cfg.num_kv_heads, h->cfg.num_kv_heads,
+  return kvq::paged_attn_workspace(h->cfg.head_dim, h->cfg.num_kv_heads,
                                    num_seqs, h->sms);
 }
 

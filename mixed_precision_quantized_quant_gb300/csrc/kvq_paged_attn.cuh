@@ -1,0 +1,814 @@
+// Paged cache: attention of one query token per sequence, split over the
+// cache's length and joined.
+//
+// Mathematics.  For the up to 8 query heads of a kv head, with t = scale
+// log2(e) q.k, running maximum m and l = sum 2^(t - m), o = sum 2^(t - m) v.
+// A key k = s c + z (c its codes) gives q.k = s (q.c) + z sum(q); a value row
+// gives p v = (p s) c + p z, whose second part is the same for every channel:
+// the codes go into the tensor cores as they are and the scales and zeros are
+// one multiply-add per (token, head).
+//
+// Bound.  Every cached byte is read once; 2 * 8 heads * D products per token
+// and kv head are far below the tensor rate, so the floor is the copy rate,
+// and what competes with it is the issue rate (unpacking, softmax).
+//
+// Work split.  A chunk is S tiles of 16 tokens of one (sequence, kv head).  The
+// chunks of all units in a row are cut into equal ranges, one per CTA of one
+// wave, so that neither many short sequences nor one long one leaves CTAs idle.
+// The four warps of a CTA take its chunks in turn, each with a ring of NST
+// stages in shared memory that one bulk copy a page fills, and meet only at
+// the end of a unit to merge.  A unit that lies in one range is written by its
+// CTA; one that several share leaves partial results, which a second kernel
+// (a programmatic dependent, resident when the first drains) joins in a fixed
+// order.  Nothing is counted across CTAs, so the workspace needs no clearing.
+//
+// Layout.  Products are taken transposed: keys are the 16 rows of an MMA and
+// query heads its 8 columns, so that 8 heads fill it.  The score fragment,
+// packed to 16 bits and transposed by movmatrix, is the P fragment of the
+// second product, whose rows are channels.  The channel order inside each
+// product is free: a thread takes the channels that its own bytes hold, and q
+// is loaded in the same order.  Codes are taken as fp16 subnormals (code *
+// 2^-24 * 2^field), exact, with no conversion; the field's power of two is
+// taken out of q (keys) or of the result (values).
+#pragma once
+
+#include <type_traits>
+
+#include "kvq_paged.cuh"
+
+namespace kvq {
+namespace paged {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLazy = 8.0f;  // the maximum follows the scores only past 2^8: rescaling is rare, and P stays below 256
+
+template <int KB, int VB, int D>
+struct Shape {
+  static constexpr bool quant = KB != 16;
+  static constexpr int TB = paged_tile_bytes(D, KB, VB);
+  // tiles of a chunk: about 4 KB a stage
+  static constexpr int S = TB > 2304 ? 1 : (TB > 1152 ? 2 : 4);
+  static constexpr int stage = S * TB;
+  static constexpr int CPS = TB > 4224 ? 2 : 4;  // CTAs per SM
+  static constexpr int merge = 2 * 32 * D;       // two warps' results (D/4 fp32 a lane)
+  static constexpr int extra = 1024;             // barriers, maxima and sums, the search's sums
+  static constexpr int ring = ((CPS == 2 ? 113 : 56) * 1024 - merge - extra) / kWarps;
+  static constexpr int NST = ring / stage > 4 ? 4 : ring / stage;
+  static constexpr int smem = extra + merge + kWarps * NST * stage;
+  static_assert(NST >= 2, "ring");
+};
+
+// One partial result in the workspace: {m, l} of 8 heads, then the result in
+// fragment order (register, lane).
+__host__ __device__ constexpr int partial_floats(int D) { return 16 + 8 * D; }
+
+struct Meta {     // start of the workspace: what the join needs of unit u
+  int32_t first;  // first CTA of the unit
+  int32_t count;  // CTAs that share it, 0: written already
+  int32_t second; // 1: the first CTA's part is its second slot
+  int32_t pad;
+};
+
+struct Seg {   // chunks of one unit in a CTA's range
+  int b, h;
+  int len, first;  // tokens attended: [first, len)
+  int cbase;       // chunk of the range's i-th chunk: cbase + i
+  int i0, i1;      // the range's chunks [i0, i1)
+  int n;           // chunks of the unit
+};
+
+__device__ __forceinline__ int seq_len(const PagedAttnParams& p, int b) {
+  const int room = p.batch.max_pages << p.pool.page_shift;
+  const int len = __ldg(p.batch.lens + b);
+  return len < 0 ? 0 : (len > room ? room : len);
+}
+__device__ __forceinline__ int seq_first(const PagedAttnParams& p, int len) {
+  return p.window > 0 && len > p.window ? len - p.window : 0;
+}
+template <int S>
+__device__ __forceinline__ int chunk_count(const PagedAttnParams& p, int len) {
+  return (len + 16 * S - 1) / (16 * S) - seq_first(p, len) / (16 * S);  // (len + 16 S: below 2^31, see open_call)
+}
+
+template <int S>
+__device__ __forceinline__ void seg_at(const PagedAttnParams& p, Seg& s, int i0, int skip, int range) {
+  s.len = seq_len(p, s.b);
+  s.first = seq_first(p, s.len);
+  s.n = chunk_count<S>(p, s.len);
+  s.i0 = i0;
+  s.cbase = s.first / (16 * S) + skip - i0;
+  const int left = s.n - skip;
+  s.i1 = left < range - i0 ? i0 + left : range;
+}
+// The unit after s; there is one while s.i1 < range.
+template <int S>
+__device__ __forceinline__ void seg_next(const PagedAttnParams& p, Seg& s, int range) {
+  const int i0 = s.i1;
+  if (++s.h == p.hkv) {
+    s.h = 0;
+    do {
+      ++s.b;
+    } while (s.b < p.batch.seqs - 1 && seq_len(p, s.b) == 0);
+  }
+  seg_at<S>(p, s, i0, 0, range);
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_t(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value) {
+    mma_16816(d, a0, a1, a2, a3, b0, b1);
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) return h2_as_u32(__floats2half2_rn(lo, hi));
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---------------------------------------------------------------- codes
+
+// Register r (two fp16 halves) of the key fragments of thread column t: the
+// channels of its halves, and log2 of the power of two its field carries.
+template <int KB, int D>
+__host__ __device__ constexpr int key_chan(int t, int r, int hi) {
+  return KB == 16  ? 16 * (r / 2) + 8 * (r % 2) + 2 * t + hi
+         : KB == 8 ? (D == 128 ? 16 * (t + 4 * (r / 8)) : 16 * t) + 2 * (r % 8) + hi
+         : KB == 4 ? D / 4 * t + 8 * (r / 4) + r % 4 + 4 * hi
+                   : D / 4 * t + 16 * (r / 8) + r % 8 + 8 * hi;
+}
+template <int B>
+__host__ __device__ constexpr int field_shift(int r) {
+  return B == 4 ? 4 * (r % 2) : B == 2 ? 2 * (r % 8 < 5 ? r % 8 : r % 8 - 5) : 0;
+}
+
+// Words of code rows -> registers of two fp16 subnormals each.
+template <int B>
+__device__ __forceinline__ void key_regs(uint32_t w, uint32_t* r) {
+  if (B == 8) {
+    r[0] = prmt(w, 0, 0x4140);
+    r[1] = prmt(w, 0, 0x4342);
+  } else if (B == 4) {
+    const uint32_t u = w >> 8;
+    r[0] = w & 0x000f000fu;
+    r[1] = w & 0x00f000f0u;
+    r[2] = u & 0x000f000fu;
+    r[3] = u & 0x00f000f0u;
+  } else {
+    const uint32_t u = w >> 10;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) r[i] = w & (0x00030003u << (2 * i));
+#pragma unroll
+    for (int i = 0; i < 3; ++i) r[5 + i] = u & (0x00030003u << (2 * i));
+  }
+}
+// x: two tokens' 16 bits of codes (low half one token, high half the other).
+template <int B>
+__device__ __forceinline__ void val_regs(uint32_t x, uint32_t* r) {
+  if (B == 8) {
+    r[0] = prmt(x, 0, 0x4240);
+    r[1] = prmt(x, 0, 0x4341);
+  } else {
+    key_regs<B>(x, r);
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <typename T, int KB, int VB, int D>
+__global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(PagedAttnParams p) {
+  using C = Shape<KB, VB, D>;
+  constexpr int S = C::S;
+  constexpr int NR = D / 8;   // key fragment registers of a thread, per row
+  constexpr int MT = D / 16;  // m-tiles of 16 channels
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);           // [warps][NST]
+  float* ml = reinterpret_cast<float*>(smem + 128);             // [warps][m 8, l 8]
+  int64_t* sums = reinterpret_cast<int64_t*>(smem + 512);       // [warps] of the search
+  int* found = reinterpret_cast<int*>(smem + 576);              // where the range starts: sequence, head, chunk
+  float* mergebuf = reinterpret_cast<float*>(smem + C::extra);  // [2][MT * 4][32]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + C::extra + C::merge + warp * C::NST * C::stage;
+  uint64_t* bar = bars + warp * C::NST;
+
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < C::NST; ++i) mbar_init(bar + i, 1);
+    fence_mbar_init();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // ---- the CTA's range of chunks, and the unit it starts in
+  const int B = p.batch.seqs;
+  int64_t total = 0;
+  for (int b = threadIdx.x; b < B; b += kThreads) {
+    const int len = __ldg(p.batch.lens + b);
+    const int used = seq_len(p, b);
+    if (blockIdx.x == 0 && len != used) atomicExch(p.pool.err, kErrBadState);
+    total += chunk_count<S>(p, used);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) sums[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += sums[w];
+  total *= p.hkv;
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kWarps) per = kWarps;
+  const int64_t r0 = per * blockIdx.x;
+  if (r0 >= total) return;  // the same for every thread
+  const int range = static_cast<int>(total - r0 < per ? total - r0 : per);
+  // the sequence that holds r0: prefix sums, 128 sequences at a time
+  {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int64_t mine = b < B ? static_cast<int64_t>(chunk_count<S>(p, seq_len(p, b))) * p.hkv : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      __syncthreads();  // sums of the round before have been read
+      if (lane == 31) sums[warp] = incl;
+      __syncthreads();
+      int64_t at = before + incl - mine;
+      for (int w = 0; w < warp; ++w) at += sums[w];
+      if (r0 >= at && r0 < at + mine) {
+        found[0] = b;
+        const int64_t off = r0 - at;
+        const int n = static_cast<int>(mine / p.hkv);
+        found[1] = static_cast<int>(off / n);
+        found[2] = static_cast<int>(off % n);
+      }
+      for (int w = 0; w < kWarps; ++w) before += sums[w];
+      if (r0 < before) break;
+    }
+    __syncthreads();
+  }
+  Seg cs;
+  cs.b = found[0];
+  cs.h = found[1];
+  seg_at<S>(p, cs, 0, found[2], range);
+  bool whole_start = found[2] == 0;  // the segment begins its unit
+
+  // ---- the producer's side of the ring: chunk `ip` is the next to copy, its
+  // page numbers loaded one step ahead of the copy that needs them
+  Seg ps = cs;
+  int ip = warp, page = 0, ntiles = 0, tok0 = 0, pieces = 0;
+  const int tiles_page = 1 << (p.pool.page_shift - 4);
+  auto prepare = [&]() {
+    if (ip >= range) return;
+    while (ip >= ps.i1) seg_next<S>(p, ps, range);
+    tok0 = (ps.cbase + ip) * (16 * S);
+    const int left = (ps.len - tok0 + 15) >> 4;
+    ntiles = left < S ? left : S;
+    pieces = tiles_page >= S ? 1 : (ntiles + tiles_page - 1) / tiles_page;
+    if (lane < pieces) {
+      const int idx = (tok0 >> p.pool.page_shift) + lane;
+      // a page wholly before the window is masked and its entry may be gone
+      page = ((idx + 1) << p.pool.page_shift) <= ps.first
+                 ? 0
+                 : __ldg(p.batch.table + ps.b * p.batch.table_stride + idx);
+    }
+  };
+  auto issue = [&](int st) {
+    if (ip >= range) return;
+    if (lane == 0) mbar_arrive_expect_tx(bar + st, static_cast<uint32_t>(ntiles * C::TB));
+    __syncwarp();
+    if (lane < pieces) {
+      if (page < 0 || page >= p.pool.num_pages) {
+        atomicExch(p.pool.err, kErrBadPage);
+        page = 0;
+      }
+      const int at = pieces == 1 ? (tok0 >> 4) & (tiles_page - 1) : 0;
+      const int d = lane * tiles_page;
+      const int n = pieces == 1 ? ntiles : (ntiles - d < tiles_page ? ntiles - d : tiles_page);
+      bulk_g2s(ring + st * C::stage + d * C::TB,
+               p.pool.pages + page * p.pool.page_stride + ps.h * p.pool.head_stride + at * C::TB,
+               static_cast<uint32_t>(n * C::TB), bar + st);
+    }
+    ip += kWarps;
+    prepare();
+  };
+  __syncwarp();
+  prepare();
+  for (int st = 0; st < C::NST; ++st) issue(st);
+
+  int ic = warp, st = 0;
+  uint32_t phase = 0;
+  bool dead = false;  // a wait gave up: nothing more is copied or computed
+  int flying = 0;     // copies that were then under way
+
+  for (;;) {
+    // ---- q of the unit, in the order of the key fragments
+    uint32_t qf[NR];
+    float fac[2], qs[2];  // of heads 2t, 2t + 1: score = fac s acc + qs z (quantized), fac acc (16 bits)
+    {
+      const bool has = g < p.gqa;
+      const T* q = reinterpret_cast<const T*>(p.q.data) + cs.b * p.q.token_stride +
+                   (cs.h * p.gqa + (has ? g : 0)) * p.q.head_stride;
+      if (!C::quant) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(q);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          qf[r] = has ? h[key_chan<KB, D>(t, r, 0)] | static_cast<uint32_t>(h[key_chan<KB, D>(t, r, 1)]) << 16 : 0u;
+        fac[0] = fac[1] = p.alpha;
+        qs[0] = qs[1] = 0.0f;
+      } else {
+        // A power of two takes the row's largest |q| to [2^13, 2^14): fields'
+        // powers come off without reaching fp16's subnormals (2^-8 at most),
+        // and a bf16 q fits fp16 exactly down to 2^-30 of the row's largest.
+        float x[NR][2], mx = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            x[r][i] = has ? Num<T>::to(q[key_chan<KB, D>(t, r, i)]) : 0.0f;
+            mx = fmaxf(mx, fabsf(x[r][i]));
+            sum += x[r][i];
+          }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // mx in [2^e, 2^(e+1))
+        e = mx < 1e-30f ? 13 : (e > 100 ? 100 : e);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float f = up * (1.0f / (1 << field_shift<KB>(r)));
+          qf[r] = h2_as_u32(__floats2half2_rn(x[r][0] * f, x[r][1] * f));
+        }
+        const float a = p.alpha * down * 16777216.0f, c = p.alpha * sum;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          fac[i] = __shfl_sync(0xffffffffu, a, (2 * t + i) * 4);
+          qs[i] = __shfl_sync(0xffffffffu, c, (2 * t + i) * 4);
+        }
+      }
+    }
+    float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, zs[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+
+    for (; ic < cs.i1; ic += kWarps) {
+      if (dead) continue;
+      dead = __any_sync(0xffffffffu, !mbar_wait(bar + st, phase, p.pool.err));
+      if (dead) {
+        flying = (ip - ic) / kWarps;
+        continue;
+      }
+      uint8_t* buf = ring + st * C::stage;
+      const int base = (cs.cbase + ic) * (16 * S);
+      const bool edge = base < cs.first || base + 16 * S > cs.len;
+      float sc[S][4];  // scores of (row g, heads 2t, 2t+1), (row g + 8, the same)
+
+      if constexpr (!C::quant) {
+        const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          float acc[2][4] = {};
+          const uint8_t* row = buf + s * C::TB + r * 2 * D;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            uint32_t a[4];
+            ldsm_x4(a, row + 16 * tile_chunk16(2 * j + c, r));
+            mma_t<T>(acc[j & 1], a[0], a[1], a[2], a[3], qf[2 * j], qf[2 * j + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[s][i] = (acc[0][i] + acc[1][i]) * p.alpha;
+        }
+        if (edge) {
+          // rows outside [first, len) may hold anything: no score, and values set to 0
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = base + 16 * s + g + 8 * (i >> 1);
+              if (tok < cs.first || tok >= cs.len) sc[s][i] = -INFINITY;
+            }
+            for (int x = lane; x < 16 * (D / 8); x += 32) {
+              const int tok = base + 16 * s + x / (D / 8);
+              if (tok < cs.first || tok >= cs.len)
+                *reinterpret_cast<uint4*>(buf + s * C::TB + 32 * D + 16 * x) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          __syncwarp();
+          fence_proxy_async_smem();  // the next copy into this stage comes after these stores
+        }
+      } else {
+        constexpr int rk = D * KB / 8;
+        constexpr int off_sz = 2 * D * (KB + VB);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const uint8_t* tile = buf + s * C::TB;
+          uint32_t k0[NR], k1[NR];  // rows g and g + 8
+          if constexpr (rk / 4 >= 16) {
+#pragma unroll
+            for (int i = 0; i < rk / 64; ++i) {
+              const int at = (16 * t + 64 * i) ^ tile_key_xor(rk, g);  // (rows g and g + 8 alike)
+              const uint4 a = *reinterpret_cast<const uint4*>(tile + g * rk + at);
+              const uint4 b = *reinterpret_cast<const uint4*>(tile + (g + 8) * rk + at);
+              constexpr int R = 16 / KB;  // registers of a word
+              key_regs<KB>(a.x, k0 + (4 * i) * R), key_regs<KB>(b.x, k1 + (4 * i) * R);
+              key_regs<KB>(a.y, k0 + (4 * i + 1) * R), key_regs<KB>(b.y, k1 + (4 * i + 1) * R);
+              key_regs<KB>(a.z, k0 + (4 * i + 2) * R), key_regs<KB>(b.z, k1 + (4 * i + 2) * R);
+              key_regs<KB>(a.w, k0 + (4 * i + 3) * R), key_regs<KB>(b.w, k1 + (4 * i + 3) * R);
+            }
+          } else if constexpr (rk / 4 == 8) {
+            const uint2 a = *reinterpret_cast<const uint2*>(tile + g * rk + 8 * t);
+            const uint2 b = *reinterpret_cast<const uint2*>(tile + (g + 8) * rk + 8 * t);
+            key_regs<KB>(a.x, k0), key_regs<KB>(b.x, k1);
+            key_regs<KB>(a.y, k0 + NR / 2), key_regs<KB>(b.y, k1 + NR / 2);
+          } else {
+            key_regs<KB>(*reinterpret_cast<const uint32_t*>(tile + g * rk + 4 * t), k0);
+            key_regs<KB>(*reinterpret_cast<const uint32_t*>(tile + (g + 8) * rk + 4 * t), k1);
+          }
+          float acc[2][4] = {};
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            mma_16816(acc[j & 1], k0[2 * j], k1[2 * j], k0[2 * j + 1], k1[2 * j + 1], qf[2 * j], qf[2 * j + 1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 sz = *reinterpret_cast<const __half2*>(tile + off_sz + 8 * (g + 8 * i));
+            const float ks = __low2float(sz), kz = __high2float(sz);
+#pragma unroll
+            for (int hd = 0; hd < 2; ++hd)
+              sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[0][2 * i + hd] + acc[1][2 * i + hd], kz * qs[hd]);
+            if (edge) {
+              const int tok = base + 16 * s + tile_row_token(g) + 8 * i;
+              if (tok < cs.first || tok >= cs.len) sc[s][2 * i] = sc[s][2 * i + 1] = -INFINITY;
+            }
+          }
+        }
+      }
+
+      // ---- running maximum.  For codes it is that of t + log2(s): what P holds
+      // is 2^(t - m) s, which then stays in fp16's range whatever the scales are
+      float vs[S][2], vz[S][2];
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float lv = 0.0f;
+          if constexpr (C::quant) {
+            const __half2 sz =
+                *reinterpret_cast<const __half2*>(buf + s * C::TB + 2 * D * (KB + VB) + 8 * (g + 8 * i) + 4);
+            vs[s][i] = __low2float(sz), vz[s][i] = __high2float(sz);
+            if (edge && sc[s][2 * i] == -INFINITY) {
+              const int tok = base + 16 * s + tile_row_token(g) + 8 * i;
+              if (tok < cs.first || tok >= cs.len) vs[s][i] = vz[s][i] = 0.0f;
+            }
+            lv = lg2(fmaxf(vs[s][i], 5.9604645e-8f));  // a scale of 0 counts as fp16's smallest
+          }
+          mx[0] = fmaxf(mx[0], sc[s][2 * i] + lv);
+          mx[1] = fmaxf(mx[1], sc[s][2 * i + 1] + lv);
+        }
+      if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
+#pragma unroll
+        for (int hd = 0; hd < 2; ++hd) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx[hd] = fmaxf(mx[hd], __shfl_xor_sync(0xffffffffu, mx[hd], x));
+          const float mn = fmaxf(m[hd], mx[hd]);
+          const float f = m[hd] == mn ? 1.0f : ex2(m[hd] - mn);
+          m[hd] = mn;
+          l[hd] *= f;
+          zs[hd] *= f;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            o[j][hd] *= f;
+            o[j][2 + hd] *= f;
+          }
+        }
+      }
+
+      // ---- probabilities and the second product
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        uint32_t pb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p0 = ex2(sc[s][2 * i] - m[0]), p1 = ex2(sc[s][2 * i + 1] - m[1]);
+          l[0] += p0;
+          l[1] += p1;
+          if constexpr (C::quant) {
+            zs[0] = fmaf(p0, vz[s][i], zs[0]);
+            zs[1] = fmaf(p1, vz[s][i], zs[1]);
+            // one rounding to fp16: at most 2^-11 of the weight
+            pb[i] = transpose8(h2_as_u32(__floats2half2_rn(p0 * vs[s][i], p1 * vs[s][i])));
+          } else {
+            pb[i] = transpose8(pack2<T>(p0, p1));  // one rounding of the weight to the cache's type
+          }
+        }
+        const uint8_t* tile = buf + s * C::TB;
+        if constexpr (!C::quant) {
+          const int r = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
+          const uint8_t* row = tile + 32 * D + r * 2 * D;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            uint32_t a[4];
+            ldsm_x4_t(a, row + 16 * tile_chunk16(2 * j + c, r));
+            mma_t<T>(o[j], a[0], a[1], a[2], a[3], pb[0], pb[1]);
+          }
+        } else {
+          constexpr int rv = D * VB / 8;
+          constexpr int CB = rv / 8;  // bytes of a thread's D/8 channels
+          const uint8_t* vals = tile + 2 * D * KB;
+          // [pair (t, t+4) or (t+8, t+12)][channel of the thread]
+          uint32_t v[2][NR];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int ta = t + 8 * h;  // tokens ta and ta + 4
+            const uint8_t* ra = vals + ta * rv + ((CB * g) ^ tile_val_xor(rv, ta));
+            const uint8_t* rb = vals + (ta + 4) * rv + ((CB * g) ^ tile_val_xor(rv, ta + 4));
+            if constexpr (CB >= 4) {
+              uint32_t wa[CB / 4], wb[CB / 4];
+              if constexpr (CB == 16) {
+                *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(ra);
+                *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(rb);
+              } else if constexpr (CB == 8) {
+                *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(ra);
+                *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(rb);
+              } else {
+                wa[0] = *reinterpret_cast<const uint32_t*>(ra);
+                wb[0] = *reinterpret_cast<const uint32_t*>(rb);
+              }
+              constexpr int R = 16 / VB;  // channels of 16 bits
+#pragma unroll
+              for (int w = 0; w < CB / 4; ++w) {
+                val_regs<VB>(prmt(wa[w], wb[w], 0x5410), v[h] + 2 * w * R);
+                val_regs<VB>(prmt(wa[w], wb[w], 0x7632), v[h] + (2 * w + 1) * R);
+              }
+            } else {
+              const uint32_t x = *reinterpret_cast<const uint16_t*>(ra) |
+                                 static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(rb)) << 16;
+              val_regs<VB>(x, v[h]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            mma_16816(o[j], v[0][2 * j], v[0][2 * j + 1], v[1][2 * j], v[1][2 * j + 1], pb[0], pb[1]);
+        }
+      }
+      __syncwarp();
+      issue(st);
+      if (++st == C::NST) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+
+    // ---- the unit's end: merge the four warps, in a fixed order
+#pragma unroll
+    for (int hd = 0; hd < 2; ++hd)
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[hd] += __shfl_xor_sync(0xffffffffu, l[hd], x);
+        zs[hd] += __shfl_xor_sync(0xffffffffu, zs[hd], x);
+      }
+    if (g == 0) {
+#pragma unroll
+      for (int hd = 0; hd < 2; ++hd) {
+        ml[warp * 16 + 2 * t + hd] = m[hd];
+        ml[warp * 16 + 8 + 2 * t + hd] = l[hd];
+      }
+    }
+    __syncthreads();
+    float top[2], sum[2];
+#pragma unroll
+    for (int hd = 0; hd < 2; ++hd) {
+      top[hd] = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top[hd] = fmaxf(top[hd], ml[w * 16 + 2 * t + hd]);
+      sum[hd] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = ml[w * 16 + 2 * t + hd], lw = ml[w * 16 + 8 + 2 * t + hd];
+        sum[hd] += lw == 0.0f ? 0.0f : lw * ex2(mw - top[hd]);
+      }
+      const float f = l[hd] == 0.0f ? 0.0f : ex2(m[hd] - top[hd]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x = o[j][2 * half + hd];
+          if (C::quant) x = fmaf(x, 16777216.0f / (1 << field_shift<VB>(2 * j + half)), zs[hd]);
+          o[j][2 * half + hd] = x * f;
+        }
+    }
+    float* mb = mergebuf + (warp & 1) * MT * 128 + lane;
+    if (warp >= 2) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mb[(4 * j + i) * 32] = o[j][i];
+    }
+    __syncthreads();
+    if (warp < 2) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[j][i] += mb[(4 * j + i) * 32];
+          if (warp == 1) mb[(4 * j + i) * 32] = o[j][i];
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      mb += MT * 128;
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] += mb[(4 * j + i) * 32];
+      const int64_t unit = static_cast<int64_t>(cs.b) * p.hkv + cs.h;
+      const bool ends = cs.cbase + cs.i1 == cs.first / (16 * S) + cs.n;
+      if (whole_start && lane == 0) {
+        const int64_t last = (r0 + cs.i0 + cs.n - 1) / per;
+        Meta meta = {static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(ends ? 0 : last - blockIdx.x + 1),
+                     cs.i0 > 0 ? 1 : 0, 0};
+        *reinterpret_cast<int4*>(p.ws + unit * sizeof(Meta)) = *reinterpret_cast<int4*>(&meta);
+      }
+      if (whole_start && ends) {
+#pragma unroll
+        for (int hd = 0; hd < 2; ++hd) {
+          const int head = 2 * t + hd;
+          if (head < p.gqa) {
+            const int64_t row = unit * p.gqa + head;
+            const float inv = 1.0f / sum[hd];
+            T* out = reinterpret_cast<T*>(p.out) + row * D;
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int c = C::quant ? NR * g + 2 * j + half : 16 * j + 8 * half + g;
+                out[c] = Num<T>::from(o[j][2 * half + hd] * inv);
+              }
+            if (p.lse && g == 0) p.lse[row] = (top[hd] + log2f(sum[hd])) * 0.693147180559945f;
+          }
+        }
+      } else {
+        float* part = reinterpret_cast<float*>(p.ws + p.ws_partials) +
+                      (2 * static_cast<int64_t>(blockIdx.x) + (cs.i0 > 0 ? 1 : 0)) * partial_floats(D);
+        if (g == 0) {
+#pragma unroll
+          for (int hd = 0; hd < 2; ++hd) {
+            part[2 * t + hd] = top[hd];
+            part[8 + 2 * t + hd] = sum[hd];
+          }
+        }
+        // [m-tile][lane][4]
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          *reinterpret_cast<float4*>(part + 16 + (j * 32 + lane) * 4) = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      }
+    }
+    if (cs.i1 >= range) break;
+    seg_next<S>(p, cs, range);
+    whole_start = true;
+  }
+  if (dead) {  // copies under way must not outlive the CTA's shared memory
+    for (int i = 0; i < flying; ++i) {
+      mbar_wait(bar + st, phase, p.pool.err);
+      if (++st == C::NST) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+// Joins the parts of units that several CTAs shared, and writes the rows of
+// sequences with no token.  One CTA per unit, a thread per four results.
+template <typename T, bool QUANT, int D>
+__global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t unit = blockIdx.x;
+  const int b = static_cast<int>(unit / p.hkv);
+  const int j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int4 raw = *reinterpret_cast<const int4*>(p.ws + unit * sizeof(Meta));
+  if (seq_len(p, b) == 0) {
+    for (int x = threadIdx.x; x < p.gqa * D; x += 2 * D)
+      reinterpret_cast<T*>(p.out)[unit * p.gqa * D + x] = Num<T>::from(0.0f);
+    if (p.lse && threadIdx.x < p.gqa) p.lse[unit * p.gqa + threadIdx.x] = -INFINITY;
+    return;
+  }
+  const int first = raw.x, count = raw.y, second = raw.z;
+  if (count == 0) return;
+  const float* base = reinterpret_cast<const float*>(p.ws + p.ws_partials);
+  auto part = [&](int i) {
+    return base + (2 * (static_cast<int64_t>(first) + i) + (i == 0 ? second : 0)) * partial_floats(D);
+  };
+  float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f}, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const float2 mi = *reinterpret_cast<const float2*>(part(i) + 2 * t);
+    top[0] = fmaxf(top[0], mi.x);
+    top[1] = fmaxf(top[1], mi.y);
+  }
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const float* x = part(i);
+    const float2 mi = *reinterpret_cast<const float2*>(x + 2 * t);
+    const float2 li = *reinterpret_cast<const float2*>(x + 8 + 2 * t);
+    const float4 v = *reinterpret_cast<const float4*>(x + 16 + (j * 32 + lane) * 4);
+    const float f0 = li.x == 0.0f ? 0.0f : ex2(mi.x - top[0]), f1 = li.y == 0.0f ? 0.0f : ex2(mi.y - top[1]);
+    sum[0] = fmaf(li.x, f0, sum[0]);
+    sum[1] = fmaf(li.y, f1, sum[1]);
+    o[0] = fmaf(v.x, f0, o[0]);
+    o[1] = fmaf(v.y, f1, o[1]);
+    o[2] = fmaf(v.z, f0, o[2]);
+    o[3] = fmaf(v.w, f1, o[3]);
+  }
+#pragma unroll
+  for (int hd = 0; hd < 2; ++hd) {
+    const int head = 2 * t + hd;
+    if (head >= p.gqa) continue;
+    const int64_t row = unit * p.gqa + head;
+    const float inv = 1.0f / sum[hd];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int c = QUANT ? D / 8 * g + 2 * j + half : 16 * j + 8 * half + g;
+      reinterpret_cast<T*>(p.out)[row * D + c] = Num<T>::from(o[2 * half + hd] * inv);
+    }
+    if (p.lse && g == 0 && j == 0) p.lse[row] = (top[hd] + log2f(sum[hd])) * 0.693147180559945f;
+  }
+}
+
+// ---------------------------------------------------------------- launch
+
+// Without parameters: makes the kernel ready on the current device.
+template <typename T, int KB, int VB, int D>
+cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
+  using C = Shape<KB, VB, D>;
+  if (!pp)
+    return cudaFuncSetAttribute(attn_kernel<T, KB, VB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  const PagedAttnParams& p = *pp;
+  // no more CTAs than the longest sequences that fit the tables can fill
+  const int64_t chunks = (static_cast<int64_t>(p.batch.max_pages) << p.pool.page_shift) / (16 * C::S) + 1;
+  const int64_t most = (chunks * p.hkv * p.batch.seqs + kWarps - 1) / kWarps;
+  const int64_t wave = static_cast<int64_t>(sms) * C::CPS;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(static_cast<unsigned>(most < wave ? most : wave));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::smem;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kernel<T, KB, VB, D>, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.hkv * p.batch.seqs));
+  cfg.blockDim = dim3(2 * D);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, C::quant, D>, p);
+}
+
+template <int KB, int VB>
+cudaError_t attn_quant(const PagedAttnParams* p, int D, int dtype, int sms, cudaStream_t s) {
+  if (dtype == 0) return D == 64 ? attn_as<__half, KB, VB, 64>(p, sms, s) : attn_as<__half, KB, VB, 128>(p, sms, s);
+  return D == 64 ? attn_as<__nv_bfloat16, KB, VB, 64>(p, sms, s) : attn_as<__nv_bfloat16, KB, VB, 128>(p, sms, s);
+}
+
+}  // namespace paged
+
+cudaError_t paged_attn_k16(const PagedAttnParams* p, int D, int dtype, int sms, cudaStream_t s);
+cudaError_t paged_attn_k8(const PagedAttnParams* p, int vb, int D, int dtype, int sms, cudaStream_t s);
+cudaError_t paged_attn_k4(const PagedAttnParams* p, int vb, int D, int dtype, int sms, cudaStream_t s);
+cudaError_t paged_attn_k2(const PagedAttnParams* p, int vb, int D, int dtype, int sms, cudaStream_t s);
+
+}  // namespace kvq

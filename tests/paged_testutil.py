@@ -70,23 +70,23 @@ class Pages:
         tile[off:off + 4] = np.concatenate([s, mn]).astype(np.float16).view(np.uint8)
 
     def get(self, page, slot, head, is_value):
-        """([d] values, [d] code * scale part) in 64 bits."""
+        """([d] values, [d] code * scale part, the scale or 1) in 64 bits."""
         tile, i = self.data[page, head, slot // 16], slot % 16
         start, n, xor = self._row(is_value, i)
         raw = tile[start + (np.arange(n) ^ xor)]
         if self.kb == 16:
             v = torch.from_numpy(raw.copy()).view(self.dtype).double().numpy()
-            return v, v
+            return v, v, 1.0
         bits = self.vb if is_value else self.kb
         off = 16 * (self.rk + self.rv) + key_row(i) * 8 + (4 if is_value else 0)
         s, z = tile[off:off + 4].view(np.float16).astype(np.float64)
         c = unpack(raw, bits, self.d) * s
-        return c + z, c
+        return c + z, c, s
 
     def rows(self, table_row, lo, hi, head, is_value):
-        """Values (and code parts) of positions lo .. hi - 1, [n, d] each."""
+        """Values and code parts of positions lo .. hi - 1, [n, d] each, and scales [n]."""
         got = [self.get(table_row[p // self.P], p % self.P, head, is_value) for p in range(lo, hi)]
-        return np.stack([g[0] for g in got]), np.stack([g[1] for g in got])
+        return np.stack([g[0] for g in got]), np.stack([g[1] for g in got]), np.array([g[2] for g in got])
 
 
 def turn(x, pos, table, interleaved):
@@ -111,13 +111,15 @@ def attend(pages, table, lens, q, scale=0.0, window=0, dtype=torch.float16):
     with the values (fp16 for codes):
       * the output's own rounding, u_out |o|;
       * each weight's rounding, u sum_j p_j |w_j| with w_j what it multiplies
-        (the value, or scale * code: the zeros are summed in fp32), and where a
-        weight is below 2^-14 (fp16), at most 2^-25 |w_j| each;
+        (the value, or scale * code: the zeros are summed in fp32).  An fp16
+        weight of codes is p_j s_j over 2^m, m at most the largest log2(p s):
+        below 2^-14 it is off by at most 2^-25, so the codes' sum by 2^-25 *
+        max(p s) * sum_j c_j, and a 16-bit value's by 2^-25 * sum_j |v_j|;
       * the scores' fp32 sums over d channels, e = (d + 16) 2^-23 max_j |scale|
         sum_c |q_c| |k_jc| (both parts of a dequantized key counted), which
         moves every weight by at most a factor exp(2 e);
-      * fp32 sums over the tokens, 64 * 2^-24 of sum_j p_j |v_j|: partial sums
-        of every 16 tokens go through a tree of a few dozen additions.
+      * fp32 sums over n tokens, a thread's chain of n / 8 additions at the
+        most and the merges' of a few dozen: (n / 8 + 64) 2^-23 of sum_j p_j |v_j|.
     """
     B, hq, d = q.shape
     g = hq // pages.hkv
@@ -133,8 +135,9 @@ def attend(pages, table, lens, q, scale=0.0, window=0, dtype=torch.float16):
         if n == 0:
             continue
         for h in range(pages.hkv):
-            k, kc = pages.rows(table[b], lo, n, h, False)
-            v, vc = pages.rows(table[b], lo, n, h, True)
+            k, kc, _ = pages.rows(table[b], lo, n, h, False)
+            v, vc, vs = pages.rows(table[b], lo, n, h, True)
+            codes = np.abs(vc) / np.where(vs > 0, vs, 1.0)[:, None]
             for j in range(h * g, h * g + g):
                 qq = q[b, j].double().numpy()
                 t = k @ qq * sc
@@ -143,8 +146,9 @@ def attend(pages, table, lens, q, scale=0.0, window=0, dtype=torch.float16):
                 out[b, j] = p @ v / total
                 lse[b, j] = t.max() + np.log(total)
                 e = (d + 16) * 2.0 ** -23 * abs(sc) * ((np.abs(kc) + np.abs(k - kc)) @ np.abs(qq)).max() + 2.0 ** -20
-                tol[b, j] = (u_out * np.abs(out[b, j]) + (u * (p @ np.abs(vc)) + 2.0 ** -25 * np.abs(vc).sum(0)) / total
-                             + (2 * e + 64 * 2.0 ** -24) * (p @ (np.abs(v) + np.abs(v - vc))) / total
-                             + 2.0 ** -24)
-                ltol[b, j] = 2 * e + 2.0 ** -20 * (1 + abs(lse[b, j]))
+                f = ((n - lo) / 8 + 64) * 2.0 ** -23
+                tol[b, j] = (u_out * np.abs(out[b, j])
+                             + (u * (p @ np.abs(vc)) + 2.0 ** -25 * (p * vs).max() * codes.sum(0)) / total
+                             + (2 * e + f) * (p @ (np.abs(v) + np.abs(v - vc))) / total + 2.0 ** -24)
+                ltol[b, j] = 2 * e + f + 2.0 ** -20 * (1 + abs(lse[b, j]))
     return out, lse, tol, ltol

@@ -194,7 +194,7 @@ def test_read(kb, vb, d, dtype):
     for row, b, p in c.places():
         for h in range(2):
             for is_v in (0, 1):
-                x, _ = c.model.get(c.table[b, p // 16], p % 16, h, bool(is_v))
+                x, _, _ = c.model.get(c.table[b, p // 16], p % 16, h, bool(is_v))
                 # code * scale + zero, rounded to fp32 and then to the type, as documented
                 exp[is_v][row, h] = torch.from_numpy(x).float().to(c.dtype)
     assert torch.equal(k.cpu(), exp[0]) and torch.equal(v.cpu(), exp[1])
