@@ -147,6 +147,14 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// bulk_g2s with the destination as a shared-memory address
+__device__ __forceinline__ void bulk_g2s_at(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // ---------------------------------------------------------------- codes
 
 // Register r (two fp16 halves) of the key fragments of thread column t: the
@@ -278,47 +286,62 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
   seg_at<S>(p, cs, 0, found[2], range);
   bool whole_start = found[2] == 0;  // the segment begins its unit
 
-  // ---- the producer's side of the ring: chunk `ip` is the next to copy, its
-  // page numbers loaded one step ahead of the copy that needs them
+  // ---- the producer's side of the ring: the addresses of the warp's next
+  // copies are worked out one a lane, 32 / ppc chunks at a time (one alone
+  // costs as many instructions as all of them); chunk `ip` is the next to copy
   Seg ps = cs;
-  int ip = warp, page = 0, ntiles = 0, tok0 = 0, pieces = 0;
   const int tiles_page = 1 << (p.pool.page_shift - 4);
-  auto prepare = [&]() {
-    if (ip >= range) return;
-    while (ip >= ps.i1) seg_next<S>(p, ps, range);
-    tok0 = (ps.cbase + ip) * (16 * S);
-    const int left = (ps.len - tok0 + 15) >> 4;
-    ntiles = left < S ? left : S;
-    pieces = tiles_page >= S ? 1 : (ntiles + tiles_page - 1) / tiles_page;
-    if (lane < pieces) {
-      const int idx = (tok0 >> p.pool.page_shift) + lane;
-      // a page wholly before the window is masked and its entry may be gone
-      page = ((idx + 1) << p.pool.page_shift) <= ps.first
-                 ? 0
-                 : __ldg(p.batch.table + ps.b * p.batch.table_stride + idx);
+  const int ppc = S > tiles_page ? S / tiles_page : 1;  // pages of a chunk
+  const int nb = 32 / ppc, mine = lane / ppc, piece = lane % ppc;
+  int ip = warp, nxt = 0;
+  const uint8_t* src = nullptr;
+  uint32_t bytes = 0, chunk_bytes = 0;
+  uint32_t dst = smem_u32(ring) + piece * tiles_page * C::TB;
+  auto fill = [&]() {
+    nxt = 0;
+    bytes = 0;
+    const int idx = ip + mine * kWarps;
+    const int last = ip + (nb - 1) * kWarps < range ? ip + (nb - 1) * kWarps : range - 1;
+    for (;;) {
+      if (idx >= ps.i0 && idx < ps.i1) {
+        const int tok0 = (ps.cbase + idx) * (16 * S);
+        const int left = (ps.len - tok0 + 15) >> 4;
+        const int ntiles = left < S ? left : S;
+        const int skip = piece * tiles_page;  // tiles of the chunk before this piece
+        int n = ntiles - skip;
+        n = n < 0 ? 0 : (ppc > 1 && n > tiles_page ? tiles_page : n);
+        chunk_bytes = static_cast<uint32_t>(ntiles * C::TB);
+        bytes = static_cast<uint32_t>(n * C::TB);
+        if (n > 0) {
+          const int e = (tok0 >> p.pool.page_shift) + piece;
+          // a page wholly before the window is masked, and its entry may be gone
+          int page = ((e + 1) << p.pool.page_shift) <= ps.first
+                         ? 0
+                         : __ldg(p.batch.table + ps.b * p.batch.table_stride + e);
+          if (page < 0 || page >= p.pool.num_pages) {
+            atomicExch(p.pool.err, kErrBadPage);
+            page = 0;
+          }
+          src = p.pool.pages + page * p.pool.page_stride + ps.h * p.pool.head_stride +
+                (ppc > 1 ? 0 : ((tok0 >> 4) & (tiles_page - 1)) * C::TB);
+        }
+      }
+      if (last < ps.i1) break;
+      seg_next<S>(p, ps, range);
     }
   };
   auto issue = [&](int st) {
     if (ip >= range) return;
-    if (lane == 0) mbar_arrive_expect_tx(bar + st, static_cast<uint32_t>(ntiles * C::TB));
-    __syncwarp();
-    if (lane < pieces) {
-      if (page < 0 || page >= p.pool.num_pages) {
-        atomicExch(p.pool.err, kErrBadPage);
-        page = 0;
-      }
-      const int at = pieces == 1 ? (tok0 >> 4) & (tiles_page - 1) : 0;
-      const int d = lane * tiles_page;
-      const int n = pieces == 1 ? ntiles : (ntiles - d < tiles_page ? ntiles - d : tiles_page);
-      bulk_g2s(ring + st * C::stage + d * C::TB,
-               p.pool.pages + page * p.pool.page_stride + ps.h * p.pool.head_stride + at * C::TB,
-               static_cast<uint32_t>(n * C::TB), bar + st);
-    }
+    if (nxt == nb) fill();
+    const bool turn = mine == nxt;
+    if (turn && piece == 0) mbar_arrive_expect_tx(bar + st, chunk_bytes);
+    if (ppc > 1) __syncwarp();
+    if (turn && bytes) bulk_g2s_at(dst + st * C::stage, src, bytes, bar + st);
+    ++nxt;
     ip += kWarps;
-    prepare();
   };
   __syncwarp();
-  prepare();
+  if (ip < range) fill();
   for (int st = 0; st < C::NST; ++st) issue(st);
 
   int ic = warp, st = 0;
@@ -393,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
       const int base = (cs.cbase + ic) * (16 * S);
       const bool edge = base < cs.first || base + 16 * S > cs.len;
       float sc[S][4];  // scores of (row g, heads 2t, 2t+1), (row g + 8, the same)
+      float vs[S][2], vz[S][2];  // value scales and zeros of the two rows
 
       if constexpr (!C::quant) {
         const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
@@ -455,20 +479,24 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
             key_regs<KB>(*reinterpret_cast<const uint32_t*>(tile + g * rk + 4 * t), k0);
             key_regs<KB>(*reinterpret_cast<const uint32_t*>(tile + (g + 8) * rk + 4 * t), k1);
           }
-          float acc[2][4] = {};
+          float acc[4] = {};
 #pragma unroll
           for (int j = 0; j < MT; ++j)
-            mma_16816(acc[j & 1], k0[2 * j], k1[2 * j], k0[2 * j + 1], k1[2 * j + 1], qf[2 * j], qf[2 * j + 1]);
+            mma_16816(acc, k0[2 * j], k1[2 * j], k0[2 * j + 1], k1[2 * j + 1], qf[2 * j], qf[2 * j + 1]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const __half2 sz = *reinterpret_cast<const __half2*>(tile + off_sz + 8 * (g + 8 * i));
-            const float ks = __low2float(sz), kz = __high2float(sz);
+            const uint2 raw = *reinterpret_cast<const uint2*>(tile + off_sz + 8 * (g + 8 * i));
+            const float ks = __low2float(u32_as_h2(raw.x)), kz = __high2float(u32_as_h2(raw.x));
+            vs[s][i] = __low2float(u32_as_h2(raw.y)), vz[s][i] = __high2float(u32_as_h2(raw.y));
 #pragma unroll
             for (int hd = 0; hd < 2; ++hd)
-              sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[0][2 * i + hd] + acc[1][2 * i + hd], kz * qs[hd]);
+              sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[2 * i + hd], kz * qs[hd]);
             if (edge) {
               const int tok = base + 16 * s + tile_row_token(g) + 8 * i;
-              if (tok < cs.first || tok >= cs.len) sc[s][2 * i] = sc[s][2 * i + 1] = -INFINITY;
+              if (tok < cs.first || tok >= cs.len) {
+                sc[s][2 * i] = sc[s][2 * i + 1] = -INFINITY;
+                vs[s][i] = vz[s][i] = 0.0f;
+              }
             }
           }
         }
@@ -476,23 +504,13 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
 
       // ---- running maximum.  For codes it is that of t + log2(s): what P holds
       // is 2^(t - m) s, which then stays in fp16's range whatever the scales are
-      float vs[S][2], vz[S][2];
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float lv = 0.0f;
-          if constexpr (C::quant) {
-            const __half2 sz =
-                *reinterpret_cast<const __half2*>(buf + s * C::TB + 2 * D * (KB + VB) + 8 * (g + 8 * i) + 4);
-            vs[s][i] = __low2float(sz), vz[s][i] = __high2float(sz);
-            if (edge && sc[s][2 * i] == -INFINITY) {
-              const int tok = base + 16 * s + tile_row_token(g) + 8 * i;
-              if (tok < cs.first || tok >= cs.len) vs[s][i] = vz[s][i] = 0.0f;
-            }
-            lv = lg2(fmaxf(vs[s][i], 5.9604645e-8f));  // a scale of 0 counts as fp16's smallest
-          }
+          if constexpr (C::quant) lv = lg2(fmaxf(vs[s][i], 5.9604645e-8f));  // a scale of 0 counts as fp16's smallest
           mx[0] = fmaxf(mx[0], sc[s][2 * i] + lv);
           mx[1] = fmaxf(mx[1], sc[s][2 * i + 1] + lv);
         }
