@@ -71,6 +71,7 @@ struct PagedAttnParams {
   float alpha;            // scale * log2(e)
   int window;             // 0: all
   int hkv, gqa;
+  int q_vec;              // every row of q is 16-byte aligned
   uint8_t* ws;             // what the join needs of every unit, then partial results
   int64_t ws_partials;    // where those start
 };

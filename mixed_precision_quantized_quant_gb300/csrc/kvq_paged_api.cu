@@ -221,8 +221,8 @@ kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch*
   kvq::PagedAttnParams p = {};
   kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
   if (st != KVQ_OK) return st;
-  int vec = 1;
-  if ((st = take_rows(q, &p.q, &vec)) != KVQ_OK) return st;
+  p.q_vec = 1;
+  if ((st = take_rows(q, &p.q, &p.q_vec)) != KVQ_OK) return st;
   if (!out || !workspace || window < 0 || !std::isfinite(scale)) return KVQ_ERR_ARG;
   if (!aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
       (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))

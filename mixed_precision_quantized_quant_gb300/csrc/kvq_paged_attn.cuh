@@ -157,15 +157,16 @@ __device__ __forceinline__ void bulk_g2s_at(uint32_t dst, const void* src, uint3
 
 // ---------------------------------------------------------------- codes
 
-// Register r (two fp16 halves) of the key fragments of thread column t: the
-// channels of its halves, and log2 of the power of two its field carries.
-template <int KB, int D>
-__host__ __device__ constexpr int key_chan(int t, int r, int hi) {
-  return KB == 16  ? 16 * (r / 2) + 8 * (r % 2) + 2 * t + hi
-         : KB == 8 ? (D == 128 ? 16 * (t + 4 * (r / 8)) : 16 * t) + 2 * (r % 8) + hi
-         : KB == 4 ? D / 4 * t + 8 * (r / 4) + r % 4 + 4 * hi
-                   : D / 4 * t + 16 * (r / 8) + r % 8 + 8 * hi;
+// The thread column t of a key fragment owns D/4 channels: with 16-bit keys
+// the MMA's own (16 j + 8 i + 2t, + 1 for register 2j + i), with codes the
+// ones of its bytes, a run of D/4 (8 bits, D = 128: the runs of 16 channels at
+// 16t and 16t + 64).  Which of the run's channels are the two halves of
+// register r:
+template <int KB>
+__host__ __device__ constexpr int key_local(int r, int hi) {
+  return KB == 8 ? 2 * r + hi : KB == 4 ? 8 * (r / 4) + r % 4 + 4 * hi : 16 * (r / 8) + r % 8 + 8 * hi;
 }
+// log2 of the power of two that the field of register (or channel) r carries
 template <int B>
 __host__ __device__ constexpr int field_shift(int r) {
   return B == 4 ? 4 * (r % 2) : B == 2 ? 2 * (r % 8 < 5 ? r % 8 : r % 8 - 5) : 0;
@@ -213,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);           // [warps][NST]
   float* ml = reinterpret_cast<float*>(smem + 128);             // [warps][m 8, l 8]
-  int64_t* sums = reinterpret_cast<int64_t*>(smem + 512);       // [warps] of the search
-  int* found = reinterpret_cast<int*>(smem + 576);              // where the range starts: sequence, head, chunk
+  int64_t* sums = reinterpret_cast<int64_t*>(smem + 512);       // [2][warps] of the search
+  int* found = reinterpret_cast<int*>(smem + 640);              // where the range starts: sequence, head, chunk
   float* mergebuf = reinterpret_cast<float*>(smem + C::extra);  // [2][MT * 4][32]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -229,56 +230,70 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- the CTA's range of chunks, and the unit it starts in
+  // ---- the CTA's range of chunks, and the unit it starts in: prefix sums of
+  // the sequences' chunks, 128 sequences at a time
   const int B = p.batch.seqs;
+  auto chunks_of = [&](int b) {
+    if (b >= B) return static_cast<int64_t>(0);
+    const int raw = __ldg(p.batch.lens + b), len = seq_len(p, b);
+    if (blockIdx.x == 0 && raw != len) atomicExch(p.pool.err, kErrBadState);
+    return static_cast<int64_t>(chunk_count<S>(p, len)) * p.hkv;
+  };
   int64_t total = 0;
-  for (int b = threadIdx.x; b < B; b += kThreads) {
-    const int len = __ldg(p.batch.lens + b);
-    const int used = seq_len(p, b);
-    if (blockIdx.x == 0 && len != used) atomicExch(p.pool.err, kErrBadState);
-    total += chunk_count<S>(p, used);
-  }
+  for (int b0 = kThreads; b0 < B; b0 += kThreads) total += chunks_of(b0 + threadIdx.x);  // but the first 128
+  int64_t held = chunks_of(threadIdx.x), incl = held;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) sums[warp] = total;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (B > kThreads) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 31) {
+    sums[warp] = incl;
+    sums[kWarps + warp] = total;
+  }
   __syncthreads();
+  int64_t before = 0;  // chunks of the sequences looked at so far
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sums[w];
-  total *= p.hkv;
+  for (int w = 0; w < kWarps; ++w) {
+    total += sums[w] + sums[kWarps + w];
+    before += sums[w];
+    if (w < warp) incl += sums[w];
+  }
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
   if (per < kWarps) per = kWarps;
   const int64_t r0 = per * blockIdx.x;
   if (r0 >= total) return;  // the same for every thread
   const int range = static_cast<int>(total - r0 < per ? total - r0 : per);
-  // the sequence that holds r0: prefix sums, 128 sequences at a time
-  {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      const int64_t mine = b < B ? static_cast<int64_t>(chunk_count<S>(p, seq_len(p, b))) * p.hkv : 0;
-      int64_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      __syncthreads();  // sums of the round before have been read
-      if (lane == 31) sums[warp] = incl;
-      __syncthreads();
-      int64_t at = before + incl - mine;
-      for (int w = 0; w < warp; ++w) at += sums[w];
-      if (r0 >= at && r0 < at + mine) {
-        found[0] = b;
-        const int64_t off = r0 - at;
-        const int n = static_cast<int>(mine / p.hkv);
-        found[1] = static_cast<int>(off / n);
-        found[2] = static_cast<int>(off % n);
-      }
-      for (int w = 0; w < kWarps; ++w) before += sums[w];
-      if (r0 < before) break;
+  for (int b0 = 0;;) {
+    const int64_t at = incl - held;
+    if (r0 >= at && r0 < incl) {
+      const int n = static_cast<int>(held / p.hkv), off = static_cast<int>(r0 - at);
+      found[0] = b0 + threadIdx.x;
+      found[1] = off / n;
+      found[2] = off % n;
     }
     __syncthreads();
+    if (r0 < before) break;
+    b0 += kThreads;
+    held = incl = chunks_of(b0 + threadIdx.x);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    incl += before;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      before += sums[w];
+      if (w < warp) incl += sums[w];
+    }
   }
   Seg cs;
   cs.b = found[0];
@@ -344,6 +359,15 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
   if (ip < range) fill();
   for (int st = 0; st < C::NST; ++st) issue(st);
 
+  // ---- where the thread reads in a tile.  Quantized: key rows g and g + 8 (the
+  // second eight rows lie 8 rows on, with the same XOR), value tokens t, t + 4,
+  // t + 8, t + 12 (alike).  16 bits: its ldmatrix row and chunk.
+  constexpr int rk = D * KB / 8, rv = D * VB / 8, CB = rv / 8;
+  constexpr int off_v = 16 * rk, off_sz = 16 * (rk + rv);
+  const int koff = C::quant ? g * rk + ((rk / 4 >= 16 ? 16 * t : rk / 4 * t) ^ tile_key_xor(rk, g)) : 0;
+  const int voff = C::quant ? off_v + t * rv + ((CB * g) ^ tile_val_xor(rv, t)) : 0;
+  const int soff = off_sz + 8 * g;
+
   int ic = warp, st = 0;
   uint32_t phase = 0;
   bool dead = false;  // a wait gave up: nothing more is copied or computed
@@ -360,23 +384,38 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
       if (!C::quant) {
         const uint16_t* h = reinterpret_cast<const uint16_t*>(q);
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-          qf[r] = has ? h[key_chan<KB, D>(t, r, 0)] | static_cast<uint32_t>(h[key_chan<KB, D>(t, r, 1)]) << 16 : 0u;
+        for (int r = 0; r < NR; ++r) {
+          const uint16_t* c = h + 8 * r + 2 * t;
+          qf[r] = !has ? 0u : p.q_vec ? *reinterpret_cast<const uint32_t*>(c) : c[0] | static_cast<uint32_t>(c[1]) << 16;
+        }
         fac[0] = fac[1] = p.alpha;
         qs[0] = qs[1] = 0.0f;
       } else {
         // A power of two takes the row's largest |q| to [2^13, 2^14): fields'
         // powers come off without reaching fp16's subnormals (2^-8 at most),
         // and a bf16 q fits fp16 exactly down to 2^-30 of the row's largest.
-        float x[NR][2], mx = 0.0f, sum = 0.0f;
+        // The thread's D/4 channels are runs of 16 bytes of codes' worth
+        // (KB = 8: two of 16 channels), read 8 channels at a time.
+        float x[D / 4], mx = 0.0f, sum = 0.0f;
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
+        for (int c = 0; c < D / 4; c += 8) {
+          const T* y = q + (KB == 8 && D == 128 ? 16 * t + 64 * (c / 16) + c % 16 : D / 4 * t + c);
+          T v[8];
+          if (!has) {
+            *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0);
+          } else if (p.q_vec) {
+            *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(y);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            x[r][i] = has ? Num<T>::to(q[key_chan<KB, D>(t, r, i)]) : 0.0f;
-            mx = fmaxf(mx, fabsf(x[r][i]));
-            sum += x[r][i];
+            for (int i = 0; i < 8; ++i) v[i] = y[i];
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[c + i] = Num<T>::to(v[i]);
+            mx = fmaxf(mx, fabsf(x[c + i]));
+            sum += x[c + i];
+          }
+        }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -389,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float f = up * (1.0f / (1 << field_shift<KB>(r)));
-          qf[r] = h2_as_u32(__floats2half2_rn(x[r][0] * f, x[r][1] * f));
+          qf[r] = h2_as_u32(__floats2half2_rn(x[key_local<KB>(r, 0)] * f, x[key_local<KB>(r, 1)] * f));
         }
         const float a = p.alpha * down * 16777216.0f, c = p.alpha * sum;
 #pragma unroll
@@ -452,32 +491,30 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
           fence_proxy_async_smem();  // the next copy into this stage comes after these stores
         }
       } else {
-        constexpr int rk = D * KB / 8;
-        constexpr int off_sz = 2 * D * (KB + VB);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          const uint8_t* tile = buf + s * C::TB;
+          const uint8_t* kp = buf + s * C::TB + koff;
           uint32_t k0[NR], k1[NR];  // rows g and g + 8
           if constexpr (rk / 4 >= 16) {
+            constexpr int R = 16 / KB;  // registers of a word
 #pragma unroll
             for (int i = 0; i < rk / 64; ++i) {
-              const int at = (16 * t + 64 * i) ^ tile_key_xor(rk, g);  // (rows g and g + 8 alike)
-              const uint4 a = *reinterpret_cast<const uint4*>(tile + g * rk + at);
-              const uint4 b = *reinterpret_cast<const uint4*>(tile + (g + 8) * rk + at);
-              constexpr int R = 16 / KB;  // registers of a word
+              const uint8_t* x = i ? buf + s * C::TB + (koff ^ 64) : kp;
+              const uint4 a = *reinterpret_cast<const uint4*>(x);
+              const uint4 b = *reinterpret_cast<const uint4*>(x + 8 * rk);
               key_regs<KB>(a.x, k0 + (4 * i) * R), key_regs<KB>(b.x, k1 + (4 * i) * R);
               key_regs<KB>(a.y, k0 + (4 * i + 1) * R), key_regs<KB>(b.y, k1 + (4 * i + 1) * R);
               key_regs<KB>(a.z, k0 + (4 * i + 2) * R), key_regs<KB>(b.z, k1 + (4 * i + 2) * R);
               key_regs<KB>(a.w, k0 + (4 * i + 3) * R), key_regs<KB>(b.w, k1 + (4 * i + 3) * R);
             }
           } else if constexpr (rk / 4 == 8) {
-            const uint2 a = *reinterpret_cast<const uint2*>(tile + g * rk + 8 * t);
-            const uint2 b = *reinterpret_cast<const uint2*>(tile + (g + 8) * rk + 8 * t);
+            const uint2 a = *reinterpret_cast<const uint2*>(kp);
+            const uint2 b = *reinterpret_cast<const uint2*>(kp + 8 * rk);
             key_regs<KB>(a.x, k0), key_regs<KB>(b.x, k1);
             key_regs<KB>(a.y, k0 + NR / 2), key_regs<KB>(b.y, k1 + NR / 2);
           } else {
-            key_regs<KB>(*reinterpret_cast<const uint32_t*>(tile + g * rk + 4 * t), k0);
-            key_regs<KB>(*reinterpret_cast<const uint32_t*>(tile + (g + 8) * rk + 4 * t), k1);
+            key_regs<KB>(*reinterpret_cast<const uint32_t*>(kp), k0);
+            key_regs<KB>(*reinterpret_cast<const uint32_t*>(kp + 8 * rk), k1);
           }
           float acc[4] = {};
 #pragma unroll
@@ -485,20 +522,24 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
             mma_16816(acc, k0[2 * j], k1[2 * j], k0[2 * j + 1], k1[2 * j + 1], qf[2 * j], qf[2 * j + 1]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint2 raw = *reinterpret_cast<const uint2*>(tile + off_sz + 8 * (g + 8 * i));
+            const uint2 raw = *reinterpret_cast<const uint2*>(buf + s * C::TB + soff + 64 * i);
             const float ks = __low2float(u32_as_h2(raw.x)), kz = __high2float(u32_as_h2(raw.x));
             vs[s][i] = __low2float(u32_as_h2(raw.y)), vz[s][i] = __high2float(u32_as_h2(raw.y));
 #pragma unroll
             for (int hd = 0; hd < 2; ++hd)
               sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[2 * i + hd], kz * qs[hd]);
-            if (edge) {
-              const int tok = base + 16 * s + tile_row_token(g) + 8 * i;
-              if (tok < cs.first || tok >= cs.len) {
+          }
+        }
+        if (edge) {  // rows outside [first, len) may hold anything
+          const int lo = cs.first - base - tile_row_token(g), hi = cs.len - base - tile_row_token(g);
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (16 * s + 8 * i < lo || 16 * s + 8 * i >= hi) {
                 sc[s][2 * i] = sc[s][2 * i + 1] = -INFINITY;
                 vs[s][i] = vz[s][i] = 0.0f;
               }
-            }
-          }
         }
       }
 
@@ -561,16 +602,12 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
             mma_t<T>(o[j], a[0], a[1], a[2], a[3], pb[0], pb[1]);
           }
         } else {
-          constexpr int rv = D * VB / 8;
-          constexpr int CB = rv / 8;  // bytes of a thread's D/8 channels
-          const uint8_t* vals = tile + 2 * D * KB;
           // [pair (t, t+4) or (t+8, t+12)][channel of the thread]
           uint32_t v[2][NR];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int ta = t + 8 * h;  // tokens ta and ta + 4
-            const uint8_t* ra = vals + ta * rv + ((CB * g) ^ tile_val_xor(rv, ta));
-            const uint8_t* rb = vals + (ta + 4) * rv + ((CB * g) ^ tile_val_xor(rv, ta + 4));
+            const uint8_t* ra = tile + voff + 8 * h * rv;
+            const uint8_t* rb = ra + 4 * rv;
             if constexpr (CB >= 4) {
               uint32_t wa[CB / 4], wb[CB / 4];
               if constexpr (CB == 16) {
@@ -736,7 +773,7 @@ __global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
   const int64_t unit = blockIdx.x;
   const int b = static_cast<int>(unit / p.hkv);
   const int j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int4 raw = *reinterpret_cast<const int4*>(p.ws + unit * sizeof(Meta));
+  const int4 raw = *reinterpret_cast<const int4*>(p.ws + unit * sizeof(Meta));  // (garbage where there is no token)
   if (seq_len(p, b) == 0) {
     for (int x = threadIdx.x; x < p.gqa * D; x += 2 * D)
       reinterpret_cast<T*>(p.out)[unit * p.gqa * D + x] = Num<T>::from(0.0f);
@@ -749,26 +786,45 @@ __global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
   auto part = [&](int i) {
     return base + (2 * (static_cast<int64_t>(first) + i) + (i == 0 ? second : 0)) * partial_floats(D);
   };
+  // parts are read eight at a time, all their loads under way together
   float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f}, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int i = 0; i < count; ++i) {
-    const float2 mi = *reinterpret_cast<const float2*>(part(i) + 2 * t);
-    top[0] = fmaxf(top[0], mi.x);
-    top[1] = fmaxf(top[1], mi.y);
-  }
-#pragma unroll 4
-  for (int i = 0; i < count; ++i) {
-    const float* x = part(i);
-    const float2 mi = *reinterpret_cast<const float2*>(x + 2 * t);
-    const float2 li = *reinterpret_cast<const float2*>(x + 8 + 2 * t);
-    const float4 v = *reinterpret_cast<const float4*>(x + 16 + (j * 32 + lane) * 4);
-    const float f0 = li.x == 0.0f ? 0.0f : ex2(mi.x - top[0]), f1 = li.y == 0.0f ? 0.0f : ex2(mi.y - top[1]);
-    sum[0] = fmaf(li.x, f0, sum[0]);
-    sum[1] = fmaf(li.y, f1, sum[1]);
-    o[0] = fmaf(v.x, f0, o[0]);
-    o[1] = fmaf(v.y, f1, o[1]);
-    o[2] = fmaf(v.z, f0, o[2]);
-    o[3] = fmaf(v.w, f1, o[3]);
+  constexpr int U = 8;
+  for (int i0 = 0; i0 < count; i0 += U) {
+    float2 mi[U], li[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mi[u] = make_float2(-INFINITY, -INFINITY);
+      li[u] = make_float2(0.0f, 0.0f);
+      v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i0 + u < count) {
+        const float* x = part(i0 + u);
+        mi[u] = *reinterpret_cast<const float2*>(x + 2 * t);
+        li[u] = *reinterpret_cast<const float2*>(x + 8 + 2 * t);
+        v[u] = *reinterpret_cast<const float4*>(x + 16 + (j * 32 + lane) * 4);
+      }
+    }
+    float mn[2] = {top[0], top[1]};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mn[0] = fmaxf(mn[0], mi[u].x);
+      mn[1] = fmaxf(mn[1], mi[u].y);
+    }
+    const float g0 = sum[0] == 0.0f ? 0.0f : ex2(top[0] - mn[0]), g1 = sum[1] == 0.0f ? 0.0f : ex2(top[1] - mn[1]);
+    sum[0] *= g0, sum[1] *= g1;
+    o[0] *= g0, o[1] *= g1, o[2] *= g0, o[3] *= g1;
+    top[0] = mn[0], top[1] = mn[1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f0 = li[u].x == 0.0f ? 0.0f : ex2(mi[u].x - top[0]);
+      const float f1 = li[u].y == 0.0f ? 0.0f : ex2(mi[u].y - top[1]);
+      sum[0] = fmaf(li[u].x, f0, sum[0]);
+      sum[1] = fmaf(li[u].y, f1, sum[1]);
+      o[0] = fmaf(v[u].x, f0, o[0]);
+      o[1] = fmaf(v[u].y, f1, o[1]);
+      o[2] = fmaf(v[u].z, f0, o[2]);
+      o[3] = fmaf(v[u].w, f1, o[3]);
+    }
   }
 #pragma unroll
   for (int hd = 0; hd < 2; ++hd) {
