@@ -47,13 +47,17 @@ template <int KB, int VB, int D>
 struct Shape {
   static constexpr bool quant = KB != 16;
   static constexpr int TB = paged_tile_bytes(D, KB, VB);
-  // tiles of a chunk: about 4 KB a stage
-  static constexpr int S = TB > 2304 ? 1 : (TB > 1152 ? 2 : 4);
+  // Tiles of a chunk, and CTAs per SM.  Codes: a chunk costs about 50
+  // instructions beside its tiles (wait, maximum, next copy), so larger chunks
+  // on 12 warps an SM beat smaller ones on 16 (K4V2, 8 x 32K tokens: 4 tiles on
+  // 3 CTAs 41.5 us, 2 on 3 45.3, 2 on 4 47.3, 4 on 2 43.6).  16 bits: one tile,
+  // as many CTAs as leave a ring of three stages.
+  static constexpr int S = !quant ? 1 : (TB > 1664 ? 2 : 4);
   static constexpr int stage = S * TB;
-  static constexpr int CPS = TB > 4224 ? 2 : 4;  // CTAs per SM
+  static constexpr int CPS = quant ? 3 : (TB > 4096 ? 2 : 4);
   static constexpr int merge = 2 * 32 * D;       // two warps' results (D/4 fp32 a lane)
   static constexpr int extra = 1024;             // barriers, maxima and sums, the search's sums
-  static constexpr int ring = ((CPS == 2 ? 113 : 56) * 1024 - merge - extra) / kWarps;
+  static constexpr int ring = ((CPS == 2 ? 113 : CPS == 3 ? 75 : 56) * 1024 - merge - extra) / kWarps;
   static constexpr int NST = ring / stage > 4 ? 4 : ring / stage;
   static constexpr int smem = extra + merge + kWarps * NST * stage;
   static_assert(NST >= 2, "ring");
