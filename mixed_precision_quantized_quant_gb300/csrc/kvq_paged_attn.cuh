@@ -39,8 +39,6 @@
 namespace kvq {
 namespace paged {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr float kLazy = 8.0f;  // the maximum follows the scores only past 2^8: rescaling is rare, and P stays below 256
 
 template <int KB, int VB, int D>
@@ -52,14 +50,17 @@ struct Shape {
   // on 12 warps an SM beat smaller ones on 16 (K4V2, 8 x 32K tokens: 4 tiles on
   // 3 CTAs 41.5 us, 2 on 3 45.3, 2 on 4 47.3, 4 on 2 43.6).  16 bits: one tile,
   // as many CTAs as leave a ring of three stages.
-  static constexpr int S = !quant ? 1 : (TB > 1664 ? 2 : 4);
+  static constexpr int S = !quant ? 1 : (TB > 1664 ? 2 : 4);  // tiles of a chunk
+  static constexpr int Z = S;                                 // tiles of a step
   static constexpr int stage = S * TB;
+  static constexpr int W = 4;  // warps
+  static constexpr int threads = 32 * W;
   static constexpr int CPS = quant ? 3 : (TB > 4096 ? 2 : 4);
   static constexpr int merge = 2 * 32 * D;       // two warps' results (D/4 fp32 a lane)
   static constexpr int extra = 1024;             // barriers, maxima and sums, the search's sums
-  static constexpr int ring = ((CPS == 2 ? 113 : CPS == 3 ? 75 : 56) * 1024 - merge - extra) / kWarps;
+  static constexpr int ring = ((228 / CPS - 1) * 1024 - merge - extra) / W;
   static constexpr int NST = ring / stage > 4 ? 4 : ring / stage;
-  static constexpr int smem = extra + merge + kWarps * NST * stage;
+  static constexpr int smem = extra + merge + W * NST * stage;
   static_assert(NST >= 2, "ring");
 };
 
@@ -118,15 +119,16 @@ __device__ __forceinline__ void seg_next(const PagedAttnParams& p, Seg& s, int r
   seg_at<S>(p, s, i0, 0, range);
 }
 
+// D = A(16x16) B(16x8) + D.  Not volatile: the compiler may interleave chains.
 template <typename T>
 __device__ __forceinline__ void mma_t(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value) {
-    mma_16816(d, a0, a1, a2, a3, b0, b1);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   } else {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
@@ -157,6 +159,20 @@ __device__ __forceinline__ void bulk_g2s_at(uint32_t dst, const void* src, uint3
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+// N words (1, 2 or 4) from shared memory in one load.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // ---------------------------------------------------------------- codes
@@ -210,16 +226,16 @@ __device__ __forceinline__ void val_regs(uint32_t x, uint32_t* r) {
 // ---------------------------------------------------------------- the kernel
 
 template <typename T, int KB, int VB, int D>
-__global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(PagedAttnParams p) {
+__global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::CPS) attn_kernel(PagedAttnParams p) {
   using C = Shape<KB, VB, D>;
-  constexpr int S = C::S;
+  constexpr int S = C::S, Z = C::Z, kWarps = C::W, kThreads = C::threads;
   constexpr int NR = D / 8;   // key fragment registers of a thread, per row
   constexpr int MT = D / 16;  // m-tiles of 16 channels
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);           // [warps][NST]
-  float* ml = reinterpret_cast<float*>(smem + 128);             // [warps][m 8, l 8]
-  int64_t* sums = reinterpret_cast<int64_t*>(smem + 512);       // [2][warps] of the search
-  int* found = reinterpret_cast<int*>(smem + 640);              // where the range starts: sequence, head, chunk
+  float* ml = reinterpret_cast<float*>(smem + 256);             // [warps][m 8, l 8]
+  int64_t* sums = reinterpret_cast<int64_t*>(smem + 768);       // [2][warps] of the search
+  int* found = reinterpret_cast<int*>(smem + 896);              // where the range starts: sequence, head, chunk
   float* mergebuf = reinterpret_cast<float*>(smem + C::extra);  // [2][MT * 4][32]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -455,16 +471,19 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
         flying = (ip - ic) / kWarps;
         continue;
       }
-      uint8_t* buf = ring + st * C::stage;
-      const int base = (cs.cbase + ic) * (16 * S);
-      const bool edge = base < cs.first || base + 16 * S > cs.len;
-      float sc[S][4];  // scores of (row g, heads 2t, 2t+1), (row g + 8, the same)
-      float vs[S][2], vz[S][2];  // value scales and zeros of the two rows
+#pragma unroll 1
+      for (int z = 0; z < S; z += Z) {  // steps of Z tiles
+      uint8_t* buf = ring + st * C::stage + z * C::TB;
+      const int base = (cs.cbase + ic) * (16 * S) + 16 * z;
+      if (z > 0 && base >= cs.len) break;
+      const bool edge = base < cs.first || base + 16 * Z > cs.len;
+      float sc[Z][4];  // scores of (row g, heads 2t, 2t+1), (row g + 8, the same)
+      float vs[Z][2], vz[Z][2];  // value scales and zeros of the two rows
 
       if constexpr (!C::quant) {
         const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < Z; ++s) {
           float acc[2][4] = {};
           const uint8_t* row = buf + s * C::TB + r * 2 * D;
 #pragma unroll
@@ -479,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
         if (edge) {
           // rows outside [first, len) may hold anything: no score, and values set to 0
 #pragma unroll
-          for (int s = 0; s < S; ++s) {
+          for (int s = 0; s < Z; ++s) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int tok = base + 16 * s + g + 8 * (i >> 1);
@@ -495,35 +514,36 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
           fence_proxy_async_smem();  // the next copy into this stage comes after these stores
         }
       } else {
+        // the words of rows g and g + 8, then the products word by word with the
+        // tiles inside, so that their S chains of dependent MMAs interleave
+        constexpr int NW = rk / 16;  // words of a thread's part of a row
+        constexpr int R = 16 / KB;   // registers of a word
+        uint32_t wa[Z][NW], wb[Z][NW];
+        float acc[Z][4] = {};
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < Z; ++s) {
           const uint8_t* kp = buf + s * C::TB + koff;
-          uint32_t k0[NR], k1[NR];  // rows g and g + 8
-          if constexpr (rk / 4 >= 16) {
-            constexpr int R = 16 / KB;  // registers of a word
-#pragma unroll
-            for (int i = 0; i < rk / 64; ++i) {
-              const uint8_t* x = i ? buf + s * C::TB + (koff ^ 64) : kp;
-              const uint4 a = *reinterpret_cast<const uint4*>(x);
-              const uint4 b = *reinterpret_cast<const uint4*>(x + 8 * rk);
-              key_regs<KB>(a.x, k0 + (4 * i) * R), key_regs<KB>(b.x, k1 + (4 * i) * R);
-              key_regs<KB>(a.y, k0 + (4 * i + 1) * R), key_regs<KB>(b.y, k1 + (4 * i + 1) * R);
-              key_regs<KB>(a.z, k0 + (4 * i + 2) * R), key_regs<KB>(b.z, k1 + (4 * i + 2) * R);
-              key_regs<KB>(a.w, k0 + (4 * i + 3) * R), key_regs<KB>(b.w, k1 + (4 * i + 3) * R);
-            }
-          } else if constexpr (rk / 4 == 8) {
-            const uint2 a = *reinterpret_cast<const uint2*>(kp);
-            const uint2 b = *reinterpret_cast<const uint2*>(kp + 8 * rk);
-            key_regs<KB>(a.x, k0), key_regs<KB>(b.x, k1);
-            key_regs<KB>(a.y, k0 + NR / 2), key_regs<KB>(b.y, k1 + NR / 2);
-          } else {
-            key_regs<KB>(*reinterpret_cast<const uint32_t*>(kp), k0);
-            key_regs<KB>(*reinterpret_cast<const uint32_t*>(kp + 8 * rk), k1);
+          load_words<(NW < 4 ? NW : 4)>(kp, wa[s]);
+          load_words<(NW < 4 ? NW : 4)>(kp + 8 * rk, wb[s]);
+          if constexpr (NW == 8) {
+            const uint8_t* kq = buf + s * C::TB + (koff ^ 64);
+            load_words<4>(kq, wa[s] + 4);
+            load_words<4>(kq + 8 * rk, wb[s] + 4);
           }
-          float acc[4] = {};
+        }
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
-            mma_16816(acc, k0[2 * j], k1[2 * j], k0[2 * j + 1], k1[2 * j + 1], qf[2 * j], qf[2 * j + 1]);
+        for (int w = 0; w < NW; ++w)
+#pragma unroll
+          for (int s = 0; s < Z; ++s) {
+            uint32_t x[R], y[R];
+            key_regs<KB>(wa[s][w], x);
+            key_regs<KB>(wb[s][w], y);
+#pragma unroll
+            for (int j = 0; j < R; j += 2)
+              mma_t<__half>(acc[s], x[j], y[j], x[j + 1], y[j + 1], qf[w * R + j], qf[w * R + j + 1]);
+          }
+#pragma unroll
+        for (int s = 0; s < Z; ++s)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint2 raw = *reinterpret_cast<const uint2*>(buf + s * C::TB + soff + 64 * i);
@@ -531,13 +551,12 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
             vs[s][i] = __low2float(u32_as_h2(raw.y)), vz[s][i] = __high2float(u32_as_h2(raw.y));
 #pragma unroll
             for (int hd = 0; hd < 2; ++hd)
-              sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[2 * i + hd], kz * qs[hd]);
+              sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[s][2 * i + hd], kz * qs[hd]);
           }
-        }
         if (edge) {  // rows outside [first, len) may hold anything
           const int lo = cs.first - base - tile_row_token(g), hi = cs.len - base - tile_row_token(g);
 #pragma unroll
-          for (int s = 0; s < S; ++s)
+          for (int s = 0; s < Z; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               if (16 * s + 8 * i < lo || 16 * s + 8 * i >= hi) {
@@ -551,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
       // is 2^(t - m) s, which then stays in fp16's range whatever the scales are
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int s = 0; s < S; ++s)
+      for (int s = 0; s < Z; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float lv = 0.0f;
@@ -577,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
         }
       }
 
-      // ---- probabilities and the second product
+      // ---- probabilities, transposed into the second product's fragments
+      uint32_t pb[Z][2];
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        uint32_t pb[2];
+      for (int s = 0; s < Z; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float p0 = ex2(sc[s][2 * i] - m[0]), p1 = ex2(sc[s][2 * i + 1] - m[1]);
@@ -590,11 +609,15 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
             zs[0] = fmaf(p0, vz[s][i], zs[0]);
             zs[1] = fmaf(p1, vz[s][i], zs[1]);
             // one rounding to fp16: at most 2^-11 of the weight
-            pb[i] = transpose8(h2_as_u32(__floats2half2_rn(p0 * vs[s][i], p1 * vs[s][i])));
+            pb[s][i] = transpose8(h2_as_u32(__floats2half2_rn(p0 * vs[s][i], p1 * vs[s][i])));
           } else {
-            pb[i] = transpose8(pack2<T>(p0, p1));  // one rounding of the weight to the cache's type
+            pb[s][i] = transpose8(pack2<T>(p0, p1));  // one rounding of the weight to the cache's type
           }
         }
+
+      // ---- the second product
+#pragma unroll
+      for (int s = 0; s < Z; ++s) {
         const uint8_t* tile = buf + s * C::TB;
         if constexpr (!C::quant) {
           const int r = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
@@ -603,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
           for (int j = 0; j < MT; ++j) {
             uint32_t a[4];
             ldsm_x4_t(a, row + 16 * tile_chunk16(2 * j + c, r));
-            mma_t<T>(o[j], a[0], a[1], a[2], a[3], pb[0], pb[1]);
+            mma_t<T>(o[j], a[0], a[1], a[2], a[3], pb[s][0], pb[s][1]);
           }
         } else {
           // [pair (t, t+4) or (t+8, t+12)][channel of the thread]
@@ -613,22 +636,14 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
             const uint8_t* ra = tile + voff + 8 * h * rv;
             const uint8_t* rb = ra + 4 * rv;
             if constexpr (CB >= 4) {
-              uint32_t wa[CB / 4], wb[CB / 4];
-              if constexpr (CB == 16) {
-                *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(ra);
-                *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(rb);
-              } else if constexpr (CB == 8) {
-                *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(ra);
-                *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(rb);
-              } else {
-                wa[0] = *reinterpret_cast<const uint32_t*>(ra);
-                wb[0] = *reinterpret_cast<const uint32_t*>(rb);
-              }
+              uint32_t ua[CB / 4], ub[CB / 4];
+              load_words<CB / 4>(ra, ua);
+              load_words<CB / 4>(rb, ub);
               constexpr int R = 16 / VB;  // channels of 16 bits
 #pragma unroll
               for (int w = 0; w < CB / 4; ++w) {
-                val_regs<VB>(prmt(wa[w], wb[w], 0x5410), v[h] + 2 * w * R);
-                val_regs<VB>(prmt(wa[w], wb[w], 0x7632), v[h] + (2 * w + 1) * R);
+                val_regs<VB>(prmt(ua[w], ub[w], 0x5410), v[h] + 2 * w * R);
+                val_regs<VB>(prmt(ua[w], ub[w], 0x7632), v[h] + (2 * w + 1) * R);
               }
             } else {
               const uint32_t x = *reinterpret_cast<const uint16_t*>(ra) |
@@ -638,8 +653,9 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
           }
 #pragma unroll
           for (int j = 0; j < MT; ++j)
-            mma_16816(o[j], v[0][2 * j], v[0][2 * j + 1], v[1][2 * j], v[1][2 * j + 1], pb[0], pb[1]);
+            mma_t<__half>(o[j], v[0][2 * j], v[0][2 * j + 1], v[1][2 * j], v[1][2 * j + 1], pb[s][0], pb[s][1]);
         }
+      }
       }
       __syncwarp();
       issue(st);
@@ -687,22 +703,30 @@ __global__ void __launch_bounds__(kThreads, Shape<KB, VB, D>::CPS) attn_kernel(P
           o[j][2 * half + hd] = x * f;
         }
     }
+    // pairs of warps add theirs to warps 0 and 1 in turn, then 1 to 0
     float* mb = mergebuf + (warp & 1) * MT * 128 + lane;
-    if (warp >= 2) {
+#pragma unroll
+    for (int w = 2; w < kWarps; w += 2) {
+      if ((warp & ~1) == w) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mb[(4 * j + i) * 32] = o[j][i];
+      }
+      __syncthreads();
+      if (warp < 2) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] += mb[(4 * j + i) * 32];
+      }
+      if (w + 2 < kWarps) __syncthreads();
+    }
+    if (warp == 1) {
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mb[(4 * j + i) * 32] = o[j][i];
-    }
-    __syncthreads();
-    if (warp < 2) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[j][i] += mb[(4 * j + i) * 32];
-          if (warp == 1) mb[(4 * j + i) * 32] = o[j][i];
-        }
     }
     __syncthreads();
     if (warp == 0) {
@@ -856,7 +880,7 @@ cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
   const PagedAttnParams& p = *pp;
   // no more CTAs than the longest sequences that fit the tables can fill
   const int64_t chunks = (static_cast<int64_t>(p.batch.max_pages) << p.pool.page_shift) / (16 * C::S) + 1;
-  const int64_t most = (chunks * p.hkv * p.batch.seqs + kWarps - 1) / kWarps;
+  const int64_t most = (chunks * p.hkv * p.batch.seqs + C::W - 1) / C::W;
   const int64_t wave = static_cast<int64_t>(sms) * C::CPS;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -866,7 +890,7 @@ cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
   cfg.numAttrs = 1;
   cfg.stream = s;
   cfg.gridDim = dim3(static_cast<unsigned>(most < wave ? most : wave));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::threads);
   cfg.dynamicSmemBytes = C::smem;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kernel<T, KB, VB, D>, p);
   if (e != cudaSuccess) return e;
