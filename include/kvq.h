@@ -403,7 +403,7 @@ typedef struct {
  *     cu_tokens[s + 1] - 1 of a call's row tensors are the newest tokens of
  *     sequence s, oldest first; NULL: row s is the newest token of sequence s
  *     (none where seq_lens[s] is 0).  Rows that belong to no sequence, such as
- *     padding behind the last one, are neither read nor written. */
+ *     padding behind the last one, are not written, whatever they hold. */
 typedef struct {
   const int32_t* page_table;
   int64_t table_stride;

@@ -52,6 +52,7 @@ struct PagedAppendParams {
   int rope_rows, rope_dim, interleaved;
   int n, hq, hkv;         // hq = 0: no queries
   int vec;                // every row is 16-byte aligned
+  int tokens;             // log2 of the tokens of a CTA (set at launch)
 };
 
 struct PagedReadParams {
@@ -60,6 +61,7 @@ struct PagedReadParams {
   PagedRows k, v;
   int n, hkv;
   int vec;
+  int tokens;
 };
 
 struct PagedAttnParams {
@@ -118,8 +120,8 @@ struct Num<__nv_bfloat16> {
 
 // ---------------------------------------------------------------- host entry points
 
-cudaError_t paged_append_launch(const PagedAppendParams& p, int D, int dtype, cudaStream_t s);
-cudaError_t paged_read_launch(const PagedReadParams& p, int D, int dtype, cudaStream_t s);
+cudaError_t paged_append_launch(const PagedAppendParams& p, int D, int dtype, int sms, cudaStream_t s);
+cudaError_t paged_read_launch(const PagedReadParams& p, int D, int dtype, int sms, cudaStream_t s);
 // Makes a layer's attention kernel ready on the current device; once, at creation.
 cudaError_t paged_attn_prepare(int kb, int vb, int D, int dtype);
 cudaError_t paged_attn_launch(PagedAttnParams p, int D, int dtype, int sms, cudaStream_t s);

@@ -184,7 +184,7 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
   kvq::PagedAppendParams p = {};
   kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
   if (st != KVQ_OK) return st;
-  if (n_tokens < 0 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!q != !q_out)) return KVQ_ERR_ARG;
+  if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!q != !q_out)) return KVQ_ERR_ARG;
   if (n_tokens == 0) return KVQ_OK;
   p.vec = 1;
   if ((st = take_rows(K, &p.k, &p.vec)) != KVQ_OK || (st = take_rows(V, &p.v, &p.vec)) != KVQ_OK) return st;
@@ -203,7 +203,7 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
   p.n = n_tokens;
   p.hq = q ? h->cfg.num_q_heads : 0;
   p.hkv = h->cfg.num_kv_heads;
-  return kvq::paged_append_launch(p, h->cfg.head_dim, h->cfg.dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return kvq::paged_append_launch(p, h->cfg.head_dim, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }
@@ -248,14 +248,14 @@ kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch,
   kvq::PagedReadParams p = {};
   kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
   if (st != KVQ_OK) return st;
-  if (n_tokens < 0 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!K && !V)) return KVQ_ERR_ARG;
+  if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!K && !V)) return KVQ_ERR_ARG;
   if (n_tokens == 0) return KVQ_OK;
   p.vec = 1;
   if (K && (st = take_rows(K, &p.k, &p.vec)) != KVQ_OK) return st;
   if (V && (st = take_rows(V, &p.v, &p.vec)) != KVQ_OK) return st;
   p.n = n_tokens;
   p.hkv = h->cfg.num_kv_heads;
-  return kvq::paged_read_launch(p, h->cfg.head_dim, h->cfg.dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return kvq::paged_read_launch(p, h->cfg.head_dim, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }

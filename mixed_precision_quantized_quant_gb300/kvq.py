@@ -527,7 +527,7 @@ class Rotation:
             if not positions.is_contiguous():
                 raise ValueError("positions must be contiguous")
             self.positions = positions
-        self.table, self.dim = table, dim
+        self.table, self.dim, self.device = table, dim, table.device
         self.args = RotationArgs(table.data_ptr(), None if positions is None else positions.data_ptr(), rows, dim,
                                  int(bool(interleaved)))
 
@@ -576,37 +576,47 @@ class KVQPagedCache:
             torch.cuda.current_stream().synchronize()
             self.h = kvq_paged_create(self.cfg, int(buffer.data_ptr()), buffer.numel())
         self._ws = {}  # num_seqs -> workspace bytes
+        # a decode step makes two of these calls for every layer, so what a
+        # call looks up is kept here
+        lib = load()
+        self._c_append, self._c_attn, self._c_read = lib.kvq_paged_append, lib.kvq_paged_decode_attn, lib.kvq_paged_read
+        self._empty, self._f32, self._u8 = torch.empty, torch.float32, torch.uint8
+        self._raw_stream, self._index = torch._C._cuda_getCurrentRawStream, self.device.index
+        self._current_device, self._device_guard = torch.cuda.current_device, torch.cuda.device
+        self._stream_guard = torch.cuda.stream
 
     def _rows(self, t, name: str, n: int, heads: int) -> Rows:
-        if t.dtype != self.dtype or t.device != self.device:
-            raise ValueError(f"{name} must be {self.dtype} on {self.device}, got {t.dtype} on {t.device}")
+        if t.dtype is self.dtype and t.shape == (n, heads, self.D) and t.device == self.device:
+            a, b, c = t.stride()
+            if c == 1:
+                return Rows(t.data_ptr(), a, b)
+            raise ValueError(f"{name}'s last dimension must be contiguous")
         if tuple(t.shape) != (n, heads, self.D):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, self.D)}")
-        a, b, c = t.stride()
-        if c != 1:
-            raise ValueError(f"{name}'s last dimension must be contiguous")
-        return Rows(t.data_ptr(), a, b)
+        raise ValueError(f"{name} must be {self.dtype} on {self.device}, got {t.dtype} on {t.device}")
 
-    def _new(self, stream, shape, dtype=None):
+    def _new(self, stream, shape, dtype):
         """An output or scratch tensor that the allocator ties to the call's stream."""
-        import torch
         if stream is None:
-            return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
+            return self._empty(shape, dtype=dtype, device=self.device)
+        with self._stream_guard(stream):
+            return self._empty(shape, dtype=dtype, device=self.device)
 
     def _batch(self, batch: PagedBatch) -> PagedBatchArgs:
         if batch.device != self.device:
             raise ValueError(f"batch must be on {self.device}, got {batch.device}")
         return batch.args
 
-    def _call(self, stream, fn) -> None:
-        """fn(stream pointer) with the cache's device current."""
-        import torch
-        if torch.cuda.current_device() == self.device.index:
-            return fn((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
-        with torch.cuda.device(self.device):
-            return fn((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    def _call(self, where: str, fn, stream, *args) -> None:
+        """fn(*args, stream) with the cache's device current."""
+        s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
+        if self._current_device() == self._index:
+            st = fn(*args, s)
+        else:
+            with self._device_guard(self.device):
+                st = fn(*args, s)
+        if st:
+            raise KVQError(st, where)
 
     def append(self, layer: int, batch: PagedBatch, K, V, q=None, rotation: Optional[Rotation] = None, q_out=None,
                stream=None):
@@ -619,23 +629,21 @@ class KVQPagedCache:
         b = self._batch(batch)
         if b.cu_tokens is None and n != batch.num_seqs:
             raise ValueError(f"K has {n} rows, expected one for each of {batch.num_seqs} sequences")
-        r = None
+        r = qr = qo = None
         if rotation is not None:
-            if rotation.table.device != self.device or rotation.dim > self.D:
+            if rotation.device != self.device or rotation.dim > self.D:
                 raise ValueError(f"rotation must be on {self.device} and turn at most {self.D} channels")
             if rotation.positions is not None and rotation.positions.numel() < n:
                 raise ValueError(f"rotation has {rotation.positions.numel()} positions, expected {n}")
             r = rotation.args
-        if q is None:
-            if q_out is not None:
-                raise ValueError("q_out without q")
-            self._call(stream, lambda s: kvq_paged_append(self.h, layer, b, k, v, None, None, r, n, s))
-            return None
-        qr = self._rows(q, "q", n, self.Hq)
-        if q_out is None:
-            q_out = self._new(stream, (n, self.Hq, self.D))
-        qo = self._rows(q_out, "q_out", n, self.Hq)
-        self._call(stream, lambda s: kvq_paged_append(self.h, layer, b, k, v, qr, qo, r, n, s))
+        if q is not None:
+            qr = self._rows(q, "q", n, self.Hq)
+            if q_out is None:
+                q_out = self._new(stream, (n, self.Hq, self.D), self.dtype)
+            qo = self._rows(q_out, "q_out", n, self.Hq)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        self._call("kvq_paged_append", self._c_append, stream, self.h, layer, b, k, v, qr, qo, r, n)
         return q_out
 
     def decode_attn(self, layer: int, batch: PagedBatch, q, out=None, scale: float = 0.0, window: int = 0,
@@ -643,25 +651,23 @@ class KVQPagedCache:
         """Attention of one query per sequence over its newest ``window``
         tokens (0: all): q [S, Hq, d] -> [S, Hq, d] in the cache's dtype, and
         with return_lse (out, fp32 [S, Hq] log-sum-exp of the scaled scores)."""
-        import torch
         S = batch.num_seqs
         b = self._batch(batch)
         qr = self._rows(q, "q", S, self.Hq)
+        if out is None:
+            out = self._new(stream, (S, self.Hq, self.D), self.dtype)
+        elif out.dtype != self.dtype or out.device != self.device or tuple(out.shape) != (S, self.Hq, self.D) or \
+                not out.is_contiguous():
+            raise ValueError(f"out must be contiguous {self.dtype} of shape {(S, self.Hq, self.D)} on {self.device}")
+        lse = self._new(stream, (S, self.Hq), self._f32) if return_lse else None
         nws = self._ws.get(S)
         if nws is None:
             nws = self._ws[S] = kvq_paged_workspace_bytes(self.h, S)
         # every call has a workspace of its own, so that calls on several
         # streams, or of several captured graphs, never share one
-        ws = self._new(stream, (nws,), torch.uint8)
-        lse = self._new(stream, (S, self.Hq), torch.float32) if return_lse else None
-        if out is None:
-            out = self._new(stream, (S, self.Hq, self.D))
-        elif out.dtype != self.dtype or out.device != self.device or tuple(out.shape) != (S, self.Hq, self.D) or \
-                not out.is_contiguous():
-            raise ValueError(f"out must be contiguous {self.dtype} of shape {(S, self.Hq, self.D)} on {self.device}")
-        self._call(stream, lambda s: kvq_paged_decode_attn(
-            self.h, layer, b, qr, out.data_ptr(), lse.data_ptr() if return_lse else None, scale, window,
-            ws.data_ptr(), nws, s))
+        ws = self._new(stream, nws, self._u8)
+        self._call("kvq_paged_decode_attn", self._c_attn, stream, self.h, layer, b, qr, out.data_ptr(),
+                   lse.data_ptr() if return_lse else None, scale, window, ws.data_ptr(), nws)
         return (out, lse) if return_lse else out
 
     def read(self, layer: int, batch: PagedBatch, n: int, K=None, V=None, stream=None):
@@ -671,16 +677,20 @@ class KVQPagedCache:
         b = self._batch(batch)
         if b.cu_tokens is None and n != batch.num_seqs:
             raise ValueError(f"n is {n}, expected one row for each of {batch.num_seqs} sequences")
-        K, V = (self._new(stream, (n, self.Hkv, self.D)) if t is None else t for t in (K, V))
+        if K is None:
+            K = self._new(stream, (n, self.Hkv, self.D), self.dtype)
+        if V is None:
+            V = self._new(stream, (n, self.Hkv, self.D), self.dtype)
         k, v = self._rows(K, "K", n, self.Hkv), self._rows(V, "V", n, self.Hkv)
-        self._call(stream, lambda s: kvq_paged_read(self.h, layer, b, k, v, n, s))
+        self._call("kvq_paged_read", self._c_read, stream, self.h, layer, b, k, v, n)
         return K, V
 
     def view(self, layer: int) -> dict:
         return kvq_paged_view_get(self.h, layer)
 
     def device_error(self, stream=None) -> int:
-        return self._call(stream, lambda s: kvq_paged_device_error(self.h, s))
+        with self._device_guard(self.device):
+            return kvq_paged_device_error(self.h, _stream_ptr(stream))
 
     def close(self) -> None:
         if getattr(self, "h", None):
