@@ -52,7 +52,7 @@ struct PagedAppendParams {
   int rope_rows, rope_dim, interleaved;
   int n, hq, hkv;         // hq = 0: no queries
   int vec;                // every row is 16-byte aligned
-  int tokens;             // log2 of the tokens of a CTA (set at launch)
+  int tokens;             // tokens of a CTA (set at launch)
 };
 
 struct PagedReadParams {
