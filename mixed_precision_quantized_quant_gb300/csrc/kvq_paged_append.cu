@@ -5,12 +5,10 @@
 //
 // A row (one token, one head, D channels) is handled by D/16 neighbouring
 // lanes with two 16-byte chunks each, so a warp holds a group of 4 or 8 rows.
-// The two chunks lie D/2 channels apart (in an append: as far apart as the
-// channels that turn together, so that no lane needs another's), and one store
-// of a row's lanes covers whole 32-byte sectors.  A CTA takes up to 32
-// tokens: its first warp finds their places, a lane each (three dependent loads, so
-// they are paid once a CTA); then each of its eight warps takes a run of the
-// (token, group) pairs of the queries, of the keys and of the values.
+// The two chunks are as far apart as the channels that turn together, so that
+// no lane needs another's, and one store of a row's lanes covers whole 32-byte
+// sectors.  Finding a token's place takes three dependent loads, which two
+// forms of the kernel hide in two ways (see them below).
 #include "kvq_paged_rows.cuh"
 
 namespace kvq {
@@ -22,16 +20,41 @@ constexpr int kAppendPerSm = 3;  // CTAs of an SM
 
 // ---------------------------------------------------------------- append
 
-enum { kQueries, kKeys, kValues };
+enum { kQueries, kKeys, kValues, kKinds };
 
+constexpr int kDepth = 2;  // groups a warp has under way beside the one it works on
+
+// cp.async of 16 bytes
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+struct AppendSmem {
+  RowPlace places[kRowTokens];
+  uint4 ring[kRowThreads / 32][kDepth][2][32];  // each lane's two chunks of the groups under way
+  float angles[kRowTokens][128];                // the tokens' cosines and sines
+};
+
+// What is done with a row once its two chunks are in registers.
 template <typename T, int D, bool QUANT>
-struct Appender {
+struct RowWork {
   static constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes of a row, rows of a group
   const PagedAppendParams& p;
-  const RowPlace* places;
-  int row0, count, lane, j, sub, c0, c1;
+  int j, sub, c0, c1;  // lane of the row, row of the group, the lane's chunks
   bool turns;
 
+  __device__ __forceinline__ RowWork(const PagedAppendParams& p_, int lane) : p(p_), j(lane % LPR), sub(lane / LPR) {
+    // a pair of chunks that turns together, or two that pass
+    const int pairs = p.rope ? p.rope_dim / 16 : 0;
+    turns = j < pairs;
+    c0 = turns ? j : pairs + j;
+    c1 = turns ? j + pairs : c0 + LPR - pairs;
+  }
   template <int KIND>
   __device__ __forceinline__ const PagedRows& rows() const {
     return KIND == kQueries ? p.q : KIND == kKeys ? p.k : p.v;
@@ -41,56 +64,13 @@ struct Appender {
     return KIND == kQueries ? p.hq : p.hkv;
   }
   template <int KIND>
-  __device__ __forceinline__ Run run(int warp) const {
-    return Run(count, (heads<KIND>() + RPW - 1) / RPW, KIND == kValues ? (warp + 4) & 7 : warp);
-  }
-  // the lane's chunks of the pair's row
-  template <int KIND>
-  __device__ __forceinline__ void load(const Run& r, uint4& a, uint4& b) const {
-    const int head = r.g * RPW + sub;
-    if (r.left <= 0 || head >= heads<KIND>()) return;
-    const T* x = reinterpret_cast<const T*>(rows<KIND>().data) + (row0 + r.tk) * rows<KIND>().token_stride +
-                 head * rows<KIND>().head_stride;
-    load8(x + 8 * c0, p.vec, a);
-    load8(x + 8 * c1, p.vec, b);
-  }
-
-  // a, b: the first pair's chunks, loaded already
-  template <int KIND>
-  __device__ __forceinline__ void work(Run r, uint4 a, uint4 b) const {
-    int tk = -1;
-    RowPlace pl;
-    pl.ok = 0;
-    f2 cs[4], sn[4];  // of the half-split pairs, or of the lane's two chunks
-#pragma unroll 1
-    while (r.left > 0) {
-      Run n = r;
-      n.next();
-      uint4 na = make_uint4(0, 0, 0, 0), nb = na;
-      load<KIND>(n, na, nb);  // under way while this pair is worked on
-      if (r.tk != tk) {
-        tk = r.tk;
-        pl = places[tk];
-        if (KIND != kValues && turns && pl.ok) {
-          const float* t = p.rope + static_cast<int64_t>(pl.rope) * p.rope_dim;
-          const float* u = t + p.rope_dim / 2;
-          const int o0 = p.interleaved ? 4 * c0 : 8 * j, o1 = p.interleaved ? 4 * c1 : 8 * j + 4;
-          float4 x = __ldg(reinterpret_cast<const float4*>(t + o0)), y = __ldg(reinterpret_cast<const float4*>(t + o1));
-          cs[0] = f2_of(x.x, x.y), cs[1] = f2_of(x.z, x.w), cs[2] = f2_of(y.x, y.y), cs[3] = f2_of(y.z, y.w);
-          x = __ldg(reinterpret_cast<const float4*>(u + o0)), y = __ldg(reinterpret_cast<const float4*>(u + o1));
-          sn[0] = f2_of(x.x, x.y), sn[1] = f2_of(x.z, x.w), sn[2] = f2_of(y.x, y.y), sn[3] = f2_of(y.z, y.w);
-        }
-      }
-      if (pl.ok) one<KIND>(r.tk, r.g * RPW + sub, pl, cs, sn, a, b);
-      a = na;
-      b = nb;
-      r = n;
-    }
+  __device__ __forceinline__ const T* row_of(int row, int head) const {
+    return reinterpret_cast<const T*>(rows<KIND>().data) + row * rows<KIND>().token_stride +
+           head * rows<KIND>().head_stride;
   }
 
   template <int KIND>
-  __device__ __forceinline__ void one(int tk, int head, const RowPlace& pl, const f2 (&cs)[4], const f2 (&sn)[4],
-                                      uint4 a, uint4 b) const {
+  __device__ __forceinline__ void one(int row, int head, const RowPlace& pl, const float* angles, uint4 a, uint4 b) const {
     f2 f[2][4];
     const bool turned = KIND != kValues && turns;
     if (turned || (QUANT && KIND != kQueries)) {
@@ -98,6 +78,13 @@ struct Appender {
       unpack8<T>(b, f[1]);
     }
     if (turned) {
+      // angles of the half-split pairs, or of the lane's two chunks
+      const float *t = angles, *u = t + p.rope_dim / 2;
+      const int o0 = p.interleaved ? 4 * c0 : 8 * j, o1 = p.interleaved ? 4 * c1 : 8 * j + 4;
+      float4 x = *reinterpret_cast<const float4*>(t + o0), y = *reinterpret_cast<const float4*>(t + o1);
+      const f2 cs[4] = {f2_of(x.x, x.y), f2_of(x.z, x.w), f2_of(y.x, y.y), f2_of(y.z, y.w)};
+      x = *reinterpret_cast<const float4*>(u + o0), y = *reinterpret_cast<const float4*>(u + o1);
+      const f2 sn[4] = {f2_of(x.x, x.y), f2_of(x.z, x.w), f2_of(y.x, y.y), f2_of(y.z, y.w)};
       if (!p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) turn2(f[0][i], f[1][i], cs[i], sn[i]);
@@ -120,7 +107,7 @@ struct Appender {
     const bool live = head < heads<KIND>();
     if constexpr (KIND == kQueries) {
       if (live) {
-        T* y = reinterpret_cast<T*>(p.qo.data) + (row0 + tk) * p.qo.token_stride + head * p.qo.head_stride;
+        T* y = reinterpret_cast<T*>(p.qo.data) + row * p.qo.token_stride + head * p.qo.head_stride;
         store8(y + 8 * c0, p.vec, a);
         store8(y + 8 * c1, p.vec, b);
       }
@@ -184,41 +171,150 @@ struct Appender {
   }
 };
 
+// Streams a warp's pairs: their rows are fetched kDepth pairs ahead.
+template <typename T, int D, bool QUANT>
+struct Appender {
+  using W = RowWork<T, D, QUANT>;
+  const W& w;
+  AppendSmem& sm;
+  int row0, count, lane, warp;
+  // the next pair to fetch
+  int kind;
+  Run ahead;
+
+  __device__ __forceinline__ Run run(int k) const {
+    const int h = k == kQueries ? w.p.hq : w.p.hkv;
+    return h ? Run(count, (h + W::RPW - 1) / W::RPW, k == kValues ? (warp + 4) & 7 : warp) : Run(0, 1, 0);
+  }
+  // starts the copy of the lane's chunks of the pair's row into `slot`
+  template <int KIND>
+  __device__ __forceinline__ void load(int slot) const {
+    const int head = ahead.g * W::RPW + w.sub;
+    if (head >= w.template heads<KIND>()) return;
+    const T* x = w.template row_of<KIND>(row0 + ahead.tk, head);
+    uint4* y = &sm.ring[warp][slot][0][lane];
+    if (w.p.vec) {
+      copy16(y, x + 8 * w.c0);
+      copy16(y + 32, x + 8 * w.c1);
+    } else {
+      load8(x + 8 * w.c0, 0, y[0]);
+      load8(x + 8 * w.c1, 0, y[32]);
+    }
+  }
+  __device__ __forceinline__ void fetch(int slot) {
+    while (kind < kKinds && ahead.left <= 0) {
+      ++kind;
+      if (kind < kKinds) ahead = run(kind);
+    }
+    if (kind == kQueries) load<kQueries>(slot);
+    if (kind == kKeys) load<kKeys>(slot);
+    if (kind == kValues) load<kValues>(slot);
+    if (kind < kKinds) ahead.next();
+    copy_commit();
+  }
+
+  // The warp's pairs of one kind, in the order they are fetched in.
+  template <int KIND>
+  __device__ __forceinline__ void work(int& slot) {
+    Run r = run(KIND);
+#pragma unroll 1
+    for (; r.left > 0; r.next()) {
+      copy_wait<kDepth - 1>();
+      const uint4 a = sm.ring[warp][slot][0][lane], b = sm.ring[warp][slot][1][lane];
+      fetch(slot);
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
+      const RowPlace pl = sm.places[r.tk];
+      if (pl.ok) w.template one<KIND>(row0 + r.tk, r.g * W::RPW + w.sub, pl, sm.angles[r.tk], a, b);
+    }
+  }
+};
+
+// Many tokens: a CTA takes up to 32.
 template <typename T, int D, bool QUANT>
 __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
-  using A = Appender<T, D, QUANT>;
-  __shared__ RowPlace places[kRowTokens];
+  __shared__ __align__(16) AppendSmem sm;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = lane % A::LPR;
-  const int pairs = p.rope ? p.rope_dim / 16 : 0;
-  const bool turns = j < pairs;
-  // the lane's chunks: a pair that turns together, or two that pass
-  const int c0 = turns ? j : pairs + j, c1 = turns ? j + pairs : c0 + A::LPR - pairs;
   const int row0 = blockIdx.x * p.tokens;  // (n is at most INT_MAX - 31)
   const int count = p.n - row0 < p.tokens ? p.n - row0 : p.tokens;
-  const A w = {p, places, row0, count, lane, j, lane / A::LPR, c0, c1, turns};
-  uint4 a[3], b[3];  // first rows of each kind, on their way while the places are found
-  const Run rk = w.template run<kKeys>(warp), rv = w.template run<kValues>(warp);
-  const Run rq = p.hq ? w.template run<kQueries>(warp) : Run(0, 1, 0);
-  w.template load<kQueries>(rq, a[0], b[0]);
-  w.template load<kKeys>(rk, a[1], b[1]);
-  w.template load<kValues>(rv, a[2], b[2]);
+  const RowWork<T, D, QUANT> work(p, lane);
+  Appender<T, D, QUANT> ap = {work, sm, row0, count, lane, warp, kQueries, Run(0, 1, 0)};
+  ap.ahead = ap.run(kQueries);
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) ap.fetch(i);  // under way while the places are found
   if (warp == 0) {
     const RowPlace r = find_places(p.batch, p.pool, row0, count, p.rope, p.positions, p.rope_rows, lane);
-    if (lane < count) places[lane] = r;
+    if (lane < count) sm.places[lane] = r;
   }
   __syncthreads();
-  w.template work<kQueries>(rq, a[0], b[0]);
-  w.template work<kKeys>(rk, a[1], b[1]);
-  w.template work<kValues>(rv, a[2], b[2]);
+  if (p.rope) {  // every token's angles once, for all its rows
+    const int quads = p.rope_dim / 4;
+    for (int tk = warp; tk < count; tk += kRowThreads / 32)
+      if (sm.places[tk].ok && lane < quads)
+        *reinterpret_cast<float4*>(&sm.angles[tk][4 * lane]) =
+            __ldg(reinterpret_cast<const float4*>(p.rope + static_cast<int64_t>(sm.places[tk].rope) * p.rope_dim) + lane);
+    __syncthreads();
+  }
+  int slot = 0;
+  ap.template work<kQueries>(slot);
+  ap.template work<kKeys>(slot);
+  ap.template work<kValues>(slot);
+}
+
+// Few tokens, where latency counts: a CTA takes one, a warp one group of its
+// rows (more where there are over 32), each finding the token's place by
+// itself while its row is on its way; no shared memory and no barrier.
+template <typename T, int D, bool QUANT>
+__global__ void __launch_bounds__(1024) paged_append_few_kernel(const __grid_constant__ PagedAppendParams p) {
+  using W = RowWork<T, D, QUANT>;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, row = blockIdx.x;
+  const W w(p, lane);
+  const int gq = (p.hq + W::RPW - 1) / W::RPW, gk = (p.hkv + W::RPW - 1) / W::RPW;
+  RowPlace pl;
+  bool found = false;
+  for (int g = threadIdx.x >> 5; g < gq + 2 * gk; g += blockDim.x >> 5) {
+    const bool q = g < gq, k = g < gq + gk;
+    const int head = (q ? g : k ? g - gq : g - gq - gk) * W::RPW + w.sub;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (head < (q ? p.hq : p.hkv)) {
+      const T* x = q ? w.template row_of<kQueries>(row, head)
+                     : k ? w.template row_of<kKeys>(row, head) : w.template row_of<kValues>(row, head);
+      load8(x + 8 * w.c0, p.vec, a);
+      load8(x + 8 * w.c1, p.vec, b);
+    }
+    if (!found) {
+      pl = find_places(p.batch, p.pool, row, 1, p.rope, p.positions, p.rope_rows, lane);
+      pl.tile = __shfl_sync(0xffffffffu, pl.tile, 0);
+      pl.tok = __shfl_sync(0xffffffffu, pl.tok, 0);
+      pl.rope = __shfl_sync(0xffffffffu, pl.rope, 0);
+      pl.ok = __shfl_sync(0xffffffffu, pl.ok, 0);
+      found = true;
+    }
+    if (!pl.ok) return;
+    const float* angles = p.rope ? p.rope + static_cast<int64_t>(pl.rope) * p.rope_dim : nullptr;
+    if (q)
+      w.template one<kQueries>(row, head, pl, angles, a, b);
+    else if (k)
+      w.template one<kKeys>(row, head, pl, angles, a, b);
+    else
+      w.template one<kValues>(row, head, pl, angles, a, b);
+  }
 }
 
 template <typename T, int D>
 cudaError_t append_as(PagedAppendParams p, int sms, cudaStream_t s) {
   p.tokens = cta_tokens(p.n, sms, kAppendPerSm);
   const dim3 grid(static_cast<unsigned>((p.n - 1) / p.tokens + 1));
+  if (p.tokens == 1) {
+    constexpr int RPW = 32 / (D / 16);
+    const int groups = (p.hq + RPW - 1) / RPW + 2 * ((p.hkv + RPW - 1) / RPW);
+    const int threads = groups < 32 ? 32 * groups : 1024;
+    return p.pool.kb == 16 ? launch_pdl(paged_append_few_kernel<T, D, false>, p, grid, threads, s)
+                           : launch_pdl(paged_append_few_kernel<T, D, true>, p, grid, threads, s);
+  }
   return p.pool.kb == 16 ? launch_pdl(paged_append_kernel<T, D, false>, p, grid, kRowThreads, s)
                          : launch_pdl(paged_append_kernel<T, D, true>, p, grid, kRowThreads, s);
 }
