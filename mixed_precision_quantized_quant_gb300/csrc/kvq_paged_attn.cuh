@@ -56,11 +56,13 @@ struct Shape {
   static constexpr int W = 4;  // warps
   static constexpr int threads = 32 * W;
   static constexpr int CPS = quant ? 3 : (TB > 4096 ? 2 : 4);
-  static constexpr int merge = 2 * 32 * D;       // two warps' results (D/4 fp32 a lane)
+  static constexpr int merge = 32 * D;           // one warp's results (D/4 fp32 a lane)
+  static constexpr int queries = 2 * 16 * D;     // the rows of 8 heads, of this unit and the next
   static constexpr int extra = 1024;             // barriers, maxima and sums, the search's sums
-  static constexpr int ring = ((228 / CPS - 1) * 1024 - merge - extra) / W;
+  static constexpr int head = extra + merge + queries;
+  static constexpr int ring = ((228 / CPS - 1) * 1024 - head) / W;
   static constexpr int NST = ring / stage > 4 ? 4 : ring / stage;
-  static constexpr int smem = extra + merge + W * NST * stage;
+  static constexpr int smem = head + W * NST * stage;
   static_assert(NST >= 2, "ring");
 };
 
@@ -236,10 +238,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   float* ml = reinterpret_cast<float*>(smem + 256);             // [warps][m 8, l 8]
   int64_t* sums = reinterpret_cast<int64_t*>(smem + 768);       // [2][warps] of the search
   int* found = reinterpret_cast<int*>(smem + 896);              // where the range starts: sequence, head, chunk
-  float* mergebuf = reinterpret_cast<float*>(smem + C::extra);  // [2][MT * 4][32]
+  float* mergebuf = reinterpret_cast<float*>(smem + C::extra);  // [MT * 4][32]
+  T* qbuf = reinterpret_cast<T*>(smem + C::extra + C::merge);   // [2][8][D]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + C::extra + C::merge + warp * C::NST * C::stage;
+  uint8_t* ring = smem + C::head + warp * C::NST * C::stage;
   uint64_t* bar = bars + warp * C::NST;
 
   if (lane == 0) {
@@ -253,6 +256,13 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   // ---- the CTA's range of chunks, and the unit it starts in: prefix sums of
   // the sequences' chunks, 128 sequences at a time
   const int B = p.batch.seqs;
+  // the page table on its way into L2 while the lengths are: a small one whole
+  {
+    const int64_t lines = (static_cast<int64_t>(B - 1) * p.batch.table_stride + p.batch.max_pages + 31) / 32;
+    const int line = blockIdx.x * kThreads + threadIdx.x;
+    if (lines <= 2048 && line < lines)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.batch.table + 32 * line));
+  }
   auto chunks_of = [&](int b) {
     if (b >= B) return static_cast<int64_t>(0);
     const int raw = __ldg(p.batch.lens + b), len = seq_len(p, b);
@@ -284,7 +294,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     before += sums[w];
     if (w < warp) incl += sums[w];
   }
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  int64_t per = total + gridDim.x - 1;
+  per = per >> 32 ? per / gridDim.x : static_cast<uint32_t>(per) / gridDim.x;  // (64 bits cost over 100 instructions)
   if (per < kWarps) per = kWarps;
   const int64_t r0 = per * blockIdx.x;
   if (r0 >= total) return;  // the same for every thread
@@ -320,6 +331,25 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   cs.h = found[1];
   seg_at<S>(p, cs, 0, found[2], range);
   bool whole_start = found[2] == 0;  // the segment begins its unit
+
+  // ---- q rows of a unit into shared memory: asked for ahead of the copies of
+  // its chunks (behind them, the first came 3 us late), of the next unit while
+  // this one is worked on
+  constexpr int RC = D / 8;  // 16-byte chunks of a row
+  auto fetch_q = [&](const Seg& u, int which) {
+    for (int x = threadIdx.x; x < p.gqa * RC; x += kThreads) {
+      const T* src = reinterpret_cast<const T*>(p.q.data) + u.b * p.q.token_stride +
+                     (u.h * p.gqa + x / RC) * p.q.head_stride + x % RC * 8;
+      T* dst = qbuf + which * 8 * D + x * 8;
+      if (p.q_vec) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = src[i];
+      }
+    }
+  };
+  fetch_q(cs, 0);
 
   // ---- the producer's side of the ring: the addresses of the warp's next
   // copies are worked out one a lane, 32 / ppc chunks at a time (one alone
@@ -388,26 +418,29 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   const int voff = C::quant ? off_v + t * rv + ((CB * g) ^ tile_val_xor(rv, t)) : 0;
   const int soff = off_sz + 8 * g;
 
-  int ic = warp, st = 0;
+  int ic = warp, st = 0, which = 0;
   uint32_t phase = 0;
   bool dead = false;  // a wait gave up: nothing more is copied or computed
   int flying = 0;     // copies that were then under way
 
   for (;;) {
     // ---- q of the unit, in the order of the key fragments
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    Seg ns = cs;  // the next unit
+    if (cs.i1 < range) {
+      seg_next<S>(p, ns, range);
+      fetch_q(ns, which ^ 1);
+    }
     uint32_t qf[NR];
     float fac[2], qs[2];  // of heads 2t, 2t + 1: score = fac s acc + qs z (quantized), fac acc (16 bits)
     {
       const bool has = g < p.gqa;
-      const T* q = reinterpret_cast<const T*>(p.q.data) + cs.b * p.q.token_stride +
-                   (cs.h * p.gqa + (has ? g : 0)) * p.q.head_stride;
+      const T* q = qbuf + (which * 8 + g) * D;
+      which ^= 1;
       if (!C::quant) {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(q);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const uint16_t* c = h + 8 * r + 2 * t;
-          qf[r] = !has ? 0u : p.q_vec ? *reinterpret_cast<const uint32_t*>(c) : c[0] | static_cast<uint32_t>(c[1]) << 16;
-        }
+        for (int r = 0; r < NR; ++r) qf[r] = has ? *reinterpret_cast<const uint32_t*>(q + 8 * r + 2 * t) : 0u;
         fac[0] = fac[1] = p.alpha;
         qs[0] = qs[1] = 0.0f;
       } else {
@@ -420,15 +453,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 #pragma unroll
         for (int c = 0; c < D / 4; c += 8) {
           const T* y = q + (KB == 8 && D == 128 ? 16 * t + 64 * (c / 16) + c % 16 : D / 4 * t + c);
-          T v[8];
-          if (!has) {
-            *reinterpret_cast<uint4*>(v) = make_uint4(0, 0, 0, 0);
-          } else if (p.q_vec) {
-            *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(y);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = y[i];
-          }
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          if (has) raw = *reinterpret_cast<const uint4*>(y);
+          const T* v = reinterpret_cast<const T*>(&raw);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             x[c + i] = Num<T>::to(v[i]);
@@ -703,38 +730,26 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
           o[j][2 * half + hd] = x * f;
         }
     }
-    // pairs of warps add theirs to warps 0 and 1 in turn, then 1 to 0
-    float* mb = mergebuf + (warp & 1) * MT * 128 + lane;
+    // warps 1, 2, ... hand theirs to warp 0 in turn
+    float* mb = mergebuf + lane;
 #pragma unroll
-    for (int w = 2; w < kWarps; w += 2) {
-      if ((warp & ~1) == w) {
+    for (int w = 1; w < kWarps; ++w) {
+      if (warp == w) {
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) mb[(4 * j + i) * 32] = o[j][i];
       }
       __syncthreads();
-      if (warp < 2) {
+      if (warp == 0) {
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][i] += mb[(4 * j + i) * 32];
       }
-      if (w + 2 < kWarps) __syncthreads();
+      if (w + 1 < kWarps) __syncthreads();
     }
-    if (warp == 1) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mb[(4 * j + i) * 32] = o[j][i];
-    }
-    __syncthreads();
     if (warp == 0) {
-      mb += MT * 128;
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][i] += mb[(4 * j + i) * 32];
       const int64_t unit = static_cast<int64_t>(cs.b) * p.hkv + cs.h;
       const bool ends = cs.cbase + cs.i1 == cs.first / (16 * S) + cs.n;
       if (whole_start && lane == 0) {
@@ -778,7 +793,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       }
     }
     if (cs.i1 >= range) break;
-    seg_next<S>(p, cs, range);
+    cs = ns;
     whole_start = true;
   }
   if (dead) {  // copies under way must not outlive the CTA's shared memory
