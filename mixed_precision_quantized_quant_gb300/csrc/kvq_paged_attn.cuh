@@ -50,15 +50,15 @@ struct Shape {
   // on 12 warps an SM beat smaller ones on 16 (K4V2, 8 x 32K tokens: 4 tiles on
   // 3 CTAs 41.5 us, 2 on 3 45.3, 2 on 4 47.3, 4 on 2 43.6).  16 bits: one tile,
   // as many CTAs as leave a ring of three stages.
-  static constexpr int S = !quant ? 1 : (TB > 1664 ? 2 : 4);  // tiles of a chunk
+  static constexpr int S = !quant || TB > 3200 ? 1 : (TB > 1664 ? 2 : 4);  // tiles of a chunk
   static constexpr int Z = S;                                 // tiles of a step
   static constexpr int stage = S * TB;
   static constexpr int W = 4;  // warps
   static constexpr int threads = 32 * W;
   static constexpr int CPS = quant ? 3 : (TB > 4096 ? 2 : 4);
-  static constexpr int merge = 32 * D;           // one warp's results (D/4 fp32 a lane)
-  static constexpr int queries = 2 * 16 * D;     // the rows of 8 heads, of this unit and the next
-  static constexpr int extra = 1024;             // barriers, maxima and sums, the search's sums
+  static constexpr int merge = (W - 1) * 32 * D;            // what each warp hands the others (D/4 fp32 a lane)
+  static constexpr int queries = (quant ? 3 : 2) * 16 * D;  // rows of 8 heads (see fetch_q)
+  static constexpr int extra = 1024;             // barriers, maxima and sums, q's factors, the search's sums
   static constexpr int head = extra + merge + queries;
   static constexpr int ring = ((228 / CPS - 1) * 1024 - head) / W;
   static constexpr int NST = ring / stage > 4 ? 4 : ring / stage;
@@ -233,13 +233,18 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   constexpr int S = C::S, Z = C::Z, kWarps = C::W, kThreads = C::threads;
   constexpr int NR = D / 8;   // key fragment registers of a thread, per row
   constexpr int MT = D / 16;  // m-tiles of 16 channels
+  constexpr int QT = MT / C::W;  // of which a warp finishes
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);           // [warps][NST]
   float* ml = reinterpret_cast<float*>(smem + 256);             // [warps][m 8, l 8]
   int64_t* sums = reinterpret_cast<int64_t*>(smem + 768);       // [2][warps] of the search
   int* found = reinterpret_cast<int*>(smem + 896);              // where the range starts: sequence, head, chunk
-  float* mergebuf = reinterpret_cast<float*>(smem + C::extra);  // [MT * 4][32]
-  T* qbuf = reinterpret_cast<T*>(smem + C::extra + C::merge);   // [2][8][D]
+  float2* qstat = reinterpret_cast<float2*>(smem + 512);        // [2][8 heads]
+  float4* mergebuf = reinterpret_cast<float4*>(smem + C::extra);  // [warps][warps - 1][QT][32]
+  // 16 bits: q rows [2][8][D].  Codes: rows as they come [8][D], then their
+  // fragments [2][NR / 4][32 lanes][4 registers]
+  uint8_t* const qbuf = smem + C::extra + C::merge;
+  uint32_t* const qfrag = reinterpret_cast<uint32_t*>(qbuf + 16 * D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + C::head + warp * C::NST * C::stage;
@@ -249,6 +254,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 #pragma unroll
     for (int i = 0; i < C::NST; ++i) mbar_init(bar + i, 1);
     fence_mbar_init();
+  }
+  if constexpr (C::quant) {  // fragments of the heads that there are not stay 0
+    for (int x = threadIdx.x; x < 8 * D; x += kThreads) qfrag[x] = 0;
+    if (threadIdx.x < 16) qstat[threadIdx.x] = make_float2(0.0f, 0.0f);
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -334,20 +343,73 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 
   // ---- q rows of a unit into shared memory: asked for ahead of the copies of
   // its chunks (behind them, the first came 3 us late), of the next unit while
-  // this one is worked on
+  // this one is worked on.  A thread takes 16 bytes, 8 channels of a head.
   constexpr int RC = D / 8;  // 16-byte chunks of a row
+  static_assert(8 * RC <= kThreads, "one chunk a thread");
+  const int qhead = threadIdx.x / RC, qchunk = threadIdx.x % RC;
+  uint8_t* const qraw = qbuf + threadIdx.x * 16;
   auto fetch_q = [&](const Seg& u, int which) {
-    for (int x = threadIdx.x; x < p.gqa * RC; x += kThreads) {
-      const T* src = reinterpret_cast<const T*>(p.q.data) + u.b * p.q.token_stride +
-                     (u.h * p.gqa + x / RC) * p.q.head_stride + x % RC * 8;
-      T* dst = qbuf + which * 8 * D + x * 8;
-      if (p.q_vec) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-      } else {
+    if (qhead >= p.gqa) return;
+    const T* src = reinterpret_cast<const T*>(p.q.data) + u.b * p.q.token_stride +
+                   (u.h * p.gqa + qhead) * p.q.head_stride + qchunk * 8;
+    uint8_t* dst = qraw + (C::quant ? 0 : which * 16 * D);
+    if (p.q_vec) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    } else {
+      T v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = src[i];
-      }
+      for (int i = 0; i < 8; ++i) v[i] = src[i];
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(v);
     }
+  };
+  // Codes: the thread's 8 channels, which it fetched itself, into the order of
+  // the key fragments.  A power of two takes the row's largest |q| to
+  // [2^13, 2^14): the fields' powers come off without reaching fp16's
+  // subnormals (2^-8 at most), and a bf16 q fits fp16 exactly down to 2^-30 of
+  // the row's largest.
+  auto make_frags = [&](int which) {
+    float x[8], mx = 0.0f, sum = 0.0f;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (qhead < p.gqa) raw = *reinterpret_cast<const uint4*>(qraw);
+    const T* v = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = Num<T>::to(v[i]);
+      mx = fmaxf(mx, fabsf(x[i]));
+      sum += x[i];
+    }
+#pragma unroll
+    for (int o = 1; o < RC; o <<= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (qhead >= p.gqa) return;
+    int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // mx in [2^e, 2^(e+1))
+    e = mx < 1e-30f ? 13 : (e > 100 ? 100 : e);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+    // channel 8 qchunk + i: thread column, register and half (see key_local)
+    constexpr bool two_runs = KB == 8 && D == 128;
+    const int col = two_runs ? qchunk / 2 % 4 : qchunk / (RC / 4);
+    const int in_run = two_runs ? 16 * (qchunk / 8) + 8 * (qchunk % 2) : 8 * (qchunk % (RC / 4));
+    uint32_t* const f = qfrag + which * 4 * D + (qhead * 4 + col) * 4;  // register r at f[r / 4 * 128 + r % 4]
+    if constexpr (KB == 2) {  // registers 0 .. 7 of 16 channels, one half each
+      __half* h = reinterpret_cast<__half*>(f + in_run / 16 * 256) + in_run / 8 % 2;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        h[i / 4 * 256 + i % 4 * 2] = __float2half_rn(x[i] * (up * (1.0f / (1 << field_shift<KB>(i)))));
+    } else {
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = x[KB == 8 ? 2 * i : i], b = x[KB == 8 ? 2 * i + 1 : i + 4];
+        const float u = up * (1.0f / (1 << field_shift<KB>(i)));
+        r[i] = h2_as_u32(__floats2half2_rn(a * u, b * u));
+      }
+      *reinterpret_cast<uint4*>(f + in_run / 8 * 128) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    // score = fac s acc + qs z
+    if (qchunk == 0) qstat[which * 8 + qhead] = make_float2(p.alpha * down * 16777216.0f, p.alpha * sum);
   };
   fetch_q(cs, 0);
 
@@ -408,6 +470,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   __syncwarp();
   if (ip < range) fill();
   for (int st = 0; st < C::NST; ++st) issue(st);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (C::quant) make_frags(0);
 
   // ---- where the thread reads in a tile.  Quantized: key rows g and g + 8 (the
   // second eight rows lie 8 rows on, with the same XOR), value tokens t, t + 4,
@@ -425,7 +489,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 
   for (;;) {
     // ---- q of the unit, in the order of the key fragments
-    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     Seg ns = cs;  // the next unit
     if (cs.i1 < range) {
@@ -433,58 +496,26 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       fetch_q(ns, which ^ 1);
     }
     uint32_t qf[NR];
-    float fac[2], qs[2];  // of heads 2t, 2t + 1: score = fac s acc + qs z (quantized), fac acc (16 bits)
-    {
-      const bool has = g < p.gqa;
-      const T* q = qbuf + (which * 8 + g) * D;
-      which ^= 1;
-      if (!C::quant) {
+    float fac[2], qs[2];  // of heads 2t, 2t + 1: score = fac s acc + qs z (codes), fac acc (16 bits)
+    if constexpr (!C::quant) {
+      const T* q = reinterpret_cast<const T*>(qbuf) + (which * 8 + g) * D;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) qf[r] = has ? *reinterpret_cast<const uint32_t*>(q + 8 * r + 2 * t) : 0u;
-        fac[0] = fac[1] = p.alpha;
-        qs[0] = qs[1] = 0.0f;
-      } else {
-        // A power of two takes the row's largest |q| to [2^13, 2^14): fields'
-        // powers come off without reaching fp16's subnormals (2^-8 at most),
-        // and a bf16 q fits fp16 exactly down to 2^-30 of the row's largest.
-        // The thread's D/4 channels are runs of 16 bytes of codes' worth
-        // (KB = 8: two of 16 channels), read 8 channels at a time.
-        float x[D / 4], mx = 0.0f, sum = 0.0f;
+      for (int r = 0; r < NR; ++r) qf[r] = g < p.gqa ? *reinterpret_cast<const uint32_t*>(q + 8 * r + 2 * t) : 0u;
+      fac[0] = fac[1] = p.alpha;
+      qs[0] = qs[1] = 0.0f;
+    } else {
 #pragma unroll
-        for (int c = 0; c < D / 4; c += 8) {
-          const T* y = q + (KB == 8 && D == 128 ? 16 * t + 64 * (c / 16) + c % 16 : D / 4 * t + c);
-          uint4 raw = make_uint4(0, 0, 0, 0);
-          if (has) raw = *reinterpret_cast<const uint4*>(y);
-          const T* v = reinterpret_cast<const T*>(&raw);
+      for (int r = 0; r < NR; r += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(qfrag + which * 4 * D + r / 4 * 128 + lane * 4);
+        qf[r] = v.x, qf[r + 1] = v.y, qf[r + 2] = v.z, qf[r + 3] = v.w;
+      }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[c + i] = Num<T>::to(v[i]);
-            mx = fmaxf(mx, fabsf(x[c + i]));
-            sum += x[c + i];
-          }
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        }
-        int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // mx in [2^e, 2^(e+1))
-        e = mx < 1e-30f ? 13 : (e > 100 ? 100 : e);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float f = up * (1.0f / (1 << field_shift<KB>(r)));
-          qf[r] = h2_as_u32(__floats2half2_rn(x[key_local<KB>(r, 0)] * f, x[key_local<KB>(r, 1)] * f));
-        }
-        const float a = p.alpha * down * 16777216.0f, c = p.alpha * sum;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          fac[i] = __shfl_sync(0xffffffffu, a, (2 * t + i) * 4);
-          qs[i] = __shfl_sync(0xffffffffu, c, (2 * t + i) * 4);
-        }
+      for (int hd = 0; hd < 2; ++hd) {
+        const float2 v = qstat[which * 8 + 2 * t + hd];
+        fac[hd] = v.x, qs[hd] = v.y;
       }
     }
+    which ^= 1;
     float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, zs[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < MT; ++j)
@@ -692,67 +723,69 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       }
     }
 
-    // ---- the unit's end: merge the four warps, in a fixed order
+    // ---- the unit's end: every warp finishes MT / W of the m-tiles, from what
+    // the others hand it, in a fixed order
+    if (cs.i1 < range) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (C::quant) make_frags(which);
+    }
 #pragma unroll
-    for (int hd = 0; hd < 2; ++hd)
+    for (int hd = 0; hd < 2; ++hd) {
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
         l[hd] += __shfl_xor_sync(0xffffffffu, l[hd], x);
         zs[hd] += __shfl_xor_sync(0xffffffffu, zs[hd], x);
       }
-    if (g == 0) {
-#pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
+      if (g == 0) {
         ml[warp * 16 + 2 * t + hd] = m[hd];
         ml[warp * 16 + 8 + 2 * t + hd] = l[hd];
       }
     }
+    float4 mine4[QT];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int q = 0; q < QT; ++q) {
+        const int j = w * QT + q;
+        float4 v = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+        if constexpr (C::quant) {  // the field's power of two, and the zeros
+          const float u0 = 16777216.0f / (1 << field_shift<VB>(2 * j)), u1 = 16777216.0f / (1 << field_shift<VB>(2 * j + 1));
+          v = make_float4(fmaf(v.x, u0, zs[0]), fmaf(v.y, u0, zs[1]), fmaf(v.z, u1, zs[0]), fmaf(v.w, u1, zs[1]));
+        }
+        if (warp == w)
+          mine4[q] = v;
+        else
+          mergebuf[((warp * (kWarps - 1) + (w < warp ? w : w - 1)) * QT + q) * 32 + lane] = v;
+      }
     __syncthreads();
-    float top[2], sum[2];
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f}, f[kWarps][2];
 #pragma unroll
     for (int hd = 0; hd < 2; ++hd) {
-      top[hd] = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top[hd] = fmaxf(top[hd], ml[w * 16 + 2 * t + hd]);
-      sum[hd] = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = ml[w * 16 + 2 * t + hd], lw = ml[w * 16 + 8 + 2 * t + hd];
-        sum[hd] += lw == 0.0f ? 0.0f : lw * ex2(mw - top[hd]);
+        const float lw = ml[w * 16 + 8 + 2 * t + hd];
+        f[w][hd] = lw == 0.0f ? 0.0f : ex2(ml[w * 16 + 2 * t + hd] - top[hd]);
+        sum[hd] = fmaf(lw, f[w][hd], sum[hd]);
       }
-      const float f = l[hd] == 0.0f ? 0.0f : ex2(m[hd] - top[hd]);
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x = o[j][2 * half + hd];
-          if (C::quant) x = fmaf(x, 16777216.0f / (1 << field_shift<VB>(2 * j + half)), zs[hd]);
-          o[j][2 * half + hd] = x * f;
-        }
     }
-    // warps 1, 2, ... hand theirs to warp 0 in turn
-    float* mb = mergebuf + lane;
+    float4 r[QT];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      if (warp == w) {
+    for (int q = 0; q < QT; ++q) {
+      r[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mb[(4 * j + i) * 32] = o[j][i];
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = w == warp ? mine4[q]
+                                   : mergebuf[((w * (kWarps - 1) + (warp < w ? warp : warp - 1)) * QT + q) * 32 + lane];
+        r[q] = make_float4(fmaf(v.x, f[w][0], r[q].x), fmaf(v.y, f[w][1], r[q].y), fmaf(v.z, f[w][0], r[q].z),
+                           fmaf(v.w, f[w][1], r[q].w));
       }
-      __syncthreads();
-      if (warp == 0) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] += mb[(4 * j + i) * 32];
-      }
-      if (w + 1 < kWarps) __syncthreads();
     }
-    if (warp == 0) {
+    {
       const int64_t unit = static_cast<int64_t>(cs.b) * p.hkv + cs.h;
       const bool ends = cs.cbase + cs.i1 == cs.first / (16 * S) + cs.n;
-      if (whole_start && lane == 0) {
+      if (whole_start && threadIdx.x == 0) {
         const int64_t last = (r0 + cs.i0 + cs.n - 1) / per;
         Meta meta = {static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(ends ? 0 : last - blockIdx.x + 1),
                      cs.i0 > 0 ? 1 : 0, 0};
@@ -767,19 +800,20 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
             const float inv = 1.0f / sum[hd];
             T* out = reinterpret_cast<T*>(p.out) + row * D;
 #pragma unroll
-            for (int j = 0; j < MT; ++j)
+            for (int q = 0; q < QT; ++q)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
+                const int j = warp * QT + q;
                 const int c = C::quant ? NR * g + 2 * j + half : 16 * j + 8 * half + g;
-                out[c] = Num<T>::from(o[j][2 * half + hd] * inv);
+                out[c] = Num<T>::from((half ? (hd ? r[q].w : r[q].z) : (hd ? r[q].y : r[q].x)) * inv);
               }
-            if (p.lse && g == 0) p.lse[row] = (top[hd] + log2f(sum[hd])) * 0.693147180559945f;
+            if (p.lse && g == 0 && warp == 0) p.lse[row] = (top[hd] + log2f(sum[hd])) * 0.693147180559945f;
           }
         }
       } else {
         float* part = reinterpret_cast<float*>(p.ws + p.ws_partials) +
                       (2 * static_cast<int64_t>(blockIdx.x) + (cs.i0 > 0 ? 1 : 0)) * partial_floats(D);
-        if (g == 0) {
+        if (g == 0 && warp == 0) {
 #pragma unroll
           for (int hd = 0; hd < 2; ++hd) {
             part[2 * t + hd] = top[hd];
@@ -788,8 +822,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         }
         // [m-tile][lane][4]
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-          *reinterpret_cast<float4*>(part + 16 + (j * 32 + lane) * 4) = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+        for (int q = 0; q < QT; ++q) *reinterpret_cast<float4*>(part + 16 + ((warp * QT + q) * 32 + lane) * 4) = r[q];
       }
     }
     if (cs.i1 >= range) break;
