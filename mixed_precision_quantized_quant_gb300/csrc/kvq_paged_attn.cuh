@@ -12,10 +12,11 @@
 // and kv head are far below the tensor rate, so the floor is the copy rate,
 // and what competes with it is the issue rate (unpacking, softmax).
 //
-// Work split.  A chunk is S tiles of 16 tokens of one (sequence, kv head).  The
-// chunks of all units in a row are cut into equal ranges, one per CTA of one
-// wave, so that neither many short sequences nor one long one leaves CTAs idle.
-// The four warps of a CTA take its chunks in turn, each with a ring of NST
+// Work split.  A chunk is S tiles of 16 tokens of one unit, a (sequence, kv
+// head).  The chunks of all units in a row, with a few void places ahead of
+// each unit for what starting it costs, are cut into equal ranges, one per CTA
+// of one wave, so that neither many short sequences nor one long one leaves
+// CTAs idle.  The four warps of a CTA take its chunks in turn, each with a ring of NST
 // stages in shared memory that one bulk copy a page fills, and meet only at
 // the end of a unit to merge.  A unit that lies in one range is written by its
 // CTA; one that several share leaves partial results, which a second kernel
@@ -30,6 +31,16 @@
 // is loaded in the same order.  Codes are taken as fp16 subnormals (code *
 // 2^-24 * 2^field), exact, with no conversion; the field's power of two is
 // taken out of q (keys) or of the result (values).
+//
+// Measured (GB300, device time with the join, copy rate 6771 GB/s): 8 x 32K
+// tokens x 8 kv heads in fp16 119 us, 96% of the copy rate; K4V2 39 us, 59%;
+// 16 x 4K x 8 in bf16 38 us, 77%, K8V4 21 us, 55%; one sequence of 256 tokens
+// 6 us.  About 9 us of each are the way to the first chunk (lengths, page
+// table, first copies: 3 dependent loads, 4.7 us), the uneven end of the CTAs
+// (2 to 4 us) and the join (3 us).  In between 16-bit rows stream at the copy
+// rate; narrow codes are bound by the ALU pipe and the issue slots (K4V2: 190
+// instructions a tile, 80 of them the masks, shifts and byte permutes that
+// make registers of two codes).
 #pragma once
 
 #include <type_traits>
@@ -51,10 +62,14 @@ struct Shape {
   // 3 CTAs 41.5 us, 2 on 3 45.3, 2 on 4 47.3, 4 on 2 43.6).  16 bits: one tile,
   // as many CTAs as leave a ring of three stages.
   static constexpr int S = !quant || TB > 3200 ? 1 : (TB > 1664 ? 2 : 4);  // tiles of a chunk
-  static constexpr int Z = S;                                 // tiles of a step
   static constexpr int stage = S * TB;
   static constexpr int W = 4;  // warps
   static constexpr int threads = 32 * W;
+  // What starting another unit costs a CTA (the merge, the drained pipeline), in
+  // chunks: a unit counts that many more when the work is cut.  (Measured 1.2 us
+  // with 16 bits, 1.6 with K8V4, 2.9 with K4V2; 2 W was the best of 0, W, 2 W,
+  // 3 W for all three: K8V4, 16 x 4K tokens, 21.7, 21.2, 20.8, 20.7 us.)
+  static constexpr int E = 2 * W;
   static constexpr int CPS = quant ? 3 : (TB > 4096 ? 2 : 4);
   static constexpr int merge = (W - 1) * 32 * D;            // what each warp hands the others (D/4 fp32 a lane)
   static constexpr int queries = (quant ? 3 : 2) * 16 * D;  // rows of 8 heads (see fetch_q)
@@ -77,12 +92,14 @@ struct Meta {     // start of the workspace: what the join needs of unit u
   int32_t pad;
 };
 
-struct Seg {   // chunks of one unit in a CTA's range
+// One unit's part of a CTA's range.  A unit is `E` void places, which stand for
+// what starting it costs, then its chunks lo .. hi - 1.
+struct Seg {
   int b, h;
   int len, first;  // tokens attended: [first, len)
-  int cbase;       // chunk of the range's i-th chunk: cbase + i
-  int i0, i1;      // the range's chunks [i0, i1)
-  int n;           // chunks of the unit
+  int lo, hi;      // chunks of the unit
+  int cbase;       // chunk at the range's i-th place: cbase + i (void below lo)
+  int i0, i1;      // the range's places [i0, i1)
 };
 
 __device__ __forceinline__ int seq_len(const PagedAttnParams& p, int b) {
@@ -93,23 +110,25 @@ __device__ __forceinline__ int seq_len(const PagedAttnParams& p, int b) {
 __device__ __forceinline__ int seq_first(const PagedAttnParams& p, int len) {
   return p.window > 0 && len > p.window ? len - p.window : 0;
 }
-template <int S>
-__device__ __forceinline__ int chunk_count(const PagedAttnParams& p, int len) {
-  return (len + 16 * S - 1) / (16 * S) - seq_first(p, len) / (16 * S);  // (len + 16 S: below 2^31, see open_call)
+// Places of a unit with `len` tokens.
+template <int S, int E>
+__device__ __forceinline__ int place_count(const PagedAttnParams& p, int len) {
+  return len ? E + (len + 16 * S - 1) / (16 * S) - seq_first(p, len) / (16 * S) : 0;  // (below 2^31, see open_call)
 }
 
-template <int S>
+template <int S, int E>
 __device__ __forceinline__ void seg_at(const PagedAttnParams& p, Seg& s, int i0, int skip, int range) {
   s.len = seq_len(p, s.b);
   s.first = seq_first(p, s.len);
-  s.n = chunk_count<S>(p, s.len);
+  s.lo = s.first / (16 * S);
+  s.hi = (s.len + 16 * S - 1) / (16 * S);
   s.i0 = i0;
-  s.cbase = s.first / (16 * S) + skip - i0;
-  const int left = s.n - skip;
+  s.cbase = s.lo - E + skip - i0;
+  const int left = s.hi - s.lo + E - skip;
   s.i1 = left < range - i0 ? i0 + left : range;
 }
 // The unit after s; there is one while s.i1 < range.
-template <int S>
+template <int S, int E>
 __device__ __forceinline__ void seg_next(const PagedAttnParams& p, Seg& s, int range) {
   const int i0 = s.i1;
   if (++s.h == p.hkv) {
@@ -118,7 +137,7 @@ __device__ __forceinline__ void seg_next(const PagedAttnParams& p, Seg& s, int r
       ++s.b;
     } while (s.b < p.batch.seqs - 1 && seq_len(p, s.b) == 0);
   }
-  seg_at<S>(p, s, i0, 0, range);
+  seg_at<S, E>(p, s, i0, 0, range);
 }
 
 // D = A(16x16) B(16x8) + D.  Not volatile: the compiler may interleave chains.
@@ -230,7 +249,7 @@ __device__ __forceinline__ void val_regs(uint32_t x, uint32_t* r) {
 template <typename T, int KB, int VB, int D>
 __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::CPS) attn_kernel(PagedAttnParams p) {
   using C = Shape<KB, VB, D>;
-  constexpr int S = C::S, Z = C::Z, kWarps = C::W, kThreads = C::threads;
+  constexpr int S = C::S, E = C::E, kWarps = C::W, kThreads = C::threads;
   constexpr int NR = D / 8;   // key fragment registers of a thread, per row
   constexpr int MT = D / 16;  // m-tiles of 16 channels
   constexpr int QT = MT / C::W;  // of which a warp finishes
@@ -238,7 +257,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);           // [warps][NST]
   float* ml = reinterpret_cast<float*>(smem + 256);             // [warps][m 8, l 8]
   int64_t* sums = reinterpret_cast<int64_t*>(smem + 768);       // [2][warps] of the search
-  int* found = reinterpret_cast<int*>(smem + 896);              // where the range starts: sequence, head, chunk
+  int* found = reinterpret_cast<int*>(smem + 896);              // where the range starts: sequence, head, place
   float2* qstat = reinterpret_cast<float2*>(smem + 512);        // [2][8 heads]
   float4* mergebuf = reinterpret_cast<float4*>(smem + C::extra);  // [warps][warps - 1][QT][32]
   // 16 bits: q rows [2][8][D].  Codes: rows as they come [8][D], then their
@@ -262,8 +281,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- the CTA's range of chunks, and the unit it starts in: prefix sums of
-  // the sequences' chunks, 128 sequences at a time
+  // ---- the CTA's range of places, and the unit it starts in: prefix sums of
+  // the sequences' places, 128 sequences at a time
   const int B = p.batch.seqs;
   // the page table on its way into L2 while the lengths are: a small one whole
   {
@@ -276,7 +295,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     if (b >= B) return static_cast<int64_t>(0);
     const int raw = __ldg(p.batch.lens + b), len = seq_len(p, b);
     if (blockIdx.x == 0 && raw != len) atomicExch(p.pool.err, kErrBadState);
-    return static_cast<int64_t>(chunk_count<S>(p, len)) * p.hkv;
+    return static_cast<int64_t>(place_count<S, E>(p, len)) * p.hkv;
   };
   int64_t total = 0;
   for (int b0 = kThreads; b0 < B; b0 += kThreads) total += chunks_of(b0 + threadIdx.x);  // but the first 128
@@ -295,7 +314,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     sums[kWarps + warp] = total;
   }
   __syncthreads();
-  int64_t before = 0;  // chunks of the sequences looked at so far
+  int64_t before = 0;  // places of the sequences looked at so far
   total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -338,8 +357,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   Seg cs;
   cs.b = found[0];
   cs.h = found[1];
-  seg_at<S>(p, cs, 0, found[2], range);
-  bool whole_start = found[2] == 0;  // the segment begins its unit
+  seg_at<S, E>(p, cs, 0, found[2], range);
 
   // ---- q rows of a unit into shared memory: asked for ahead of the copies of
   // its chunks (behind them, the first came 3 us late), of the next unit while
@@ -422,15 +440,18 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   const int nb = 32 / ppc, mine = lane / ppc, piece = lane % ppc;
   int ip = warp, nxt = 0;
   const uint8_t* src = nullptr;
-  uint32_t bytes = 0, chunk_bytes = 0;
+  uint32_t bytes = 0, chunk_bytes = 0, voids = 0;
   uint32_t dst = smem_u32(ring) + piece * tiles_page * C::TB;
   auto fill = [&]() {
     nxt = 0;
     bytes = 0;
+    bool is_void = false;
     const int idx = ip + mine * kWarps;
     const int last = ip + (nb - 1) * kWarps < range ? ip + (nb - 1) * kWarps : range - 1;
     for (;;) {
-      if (idx >= ps.i0 && idx < ps.i1) {
+      if (idx >= ps.i0 && idx < ps.i1 && ps.cbase + idx < ps.lo) {
+        is_void = true;
+      } else if (idx >= ps.i0 && idx < ps.i1) {
         const int tok0 = (ps.cbase + idx) * (16 * S);
         const int left = (ps.len - tok0 + 15) >> 4;
         const int ntiles = left < S ? left : S;
@@ -454,12 +475,16 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         }
       }
       if (last < ps.i1) break;
-      seg_next<S>(p, ps, range);
+      seg_next<S, E>(p, ps, range);
     }
+    voids = __ballot_sync(0xffffffffu, is_void);
   };
   auto issue = [&](int st) {
-    if (ip >= range) return;
-    if (nxt == nb) fill();
+    for (;; ++nxt, ip += kWarps) {
+      if (ip >= range) return;
+      if (nxt == nb) fill();
+      if (!(voids >> (nxt * ppc) & 1)) break;
+    }
     const bool turn = mine == nxt;
     if (turn && piece == 0) mbar_arrive_expect_tx(bar + st, chunk_bytes);
     if (ppc > 1) __syncwarp();
@@ -492,7 +517,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     __syncthreads();
     Seg ns = cs;  // the next unit
     if (cs.i1 < range) {
-      seg_next<S>(p, ns, range);
+      seg_next<S, E>(p, ns, range);
       fetch_q(ns, which ^ 1);
     }
     uint32_t qf[NR];
@@ -523,25 +548,27 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
 
     for (; ic < cs.i1; ic += kWarps) {
-      if (dead) continue;
+      if (dead || cs.cbase + ic < cs.lo) continue;
       dead = __any_sync(0xffffffffu, !mbar_wait(bar + st, phase, p.pool.err));
       if (dead) {
-        flying = (ip - ic) / kWarps;
+        flying = 0;  // of the places between, those that are chunks
+        Seg x = cs;
+        for (int i = ic; i < ip; i += kWarps) {
+          while (i >= x.i1) seg_next<S, E>(p, x, range);
+          flying += x.cbase + i >= x.lo;
+        }
         continue;
       }
-#pragma unroll 1
-      for (int z = 0; z < S; z += Z) {  // steps of Z tiles
-      uint8_t* buf = ring + st * C::stage + z * C::TB;
-      const int base = (cs.cbase + ic) * (16 * S) + 16 * z;
-      if (z > 0 && base >= cs.len) break;
-      const bool edge = base < cs.first || base + 16 * Z > cs.len;
-      float sc[Z][4];  // scores of (row g, heads 2t, 2t+1), (row g + 8, the same)
-      float vs[Z][2], vz[Z][2];  // value scales and zeros of the two rows
+      uint8_t* buf = ring + st * C::stage;
+      const int base = (cs.cbase + ic) * (16 * S);
+      const bool edge = base < cs.first || base + 16 * S > cs.len;
+      float sc[S][4];  // scores of (row g, heads 2t, 2t+1), (row g + 8, the same)
+      float vs[S][2], vz[S][2];  // value scales and zeros of the two rows
 
       if constexpr (!C::quant) {
         const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
 #pragma unroll
-        for (int s = 0; s < Z; ++s) {
+        for (int s = 0; s < S; ++s) {
           float acc[2][4] = {};
           const uint8_t* row = buf + s * C::TB + r * 2 * D;
 #pragma unroll
@@ -556,7 +583,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         if (edge) {
           // rows outside [first, len) may hold anything: no score, and values set to 0
 #pragma unroll
-          for (int s = 0; s < Z; ++s) {
+          for (int s = 0; s < S; ++s) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int tok = base + 16 * s + g + 8 * (i >> 1);
@@ -576,10 +603,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         // tiles inside, so that their S chains of dependent MMAs interleave
         constexpr int NW = rk / 16;  // words of a thread's part of a row
         constexpr int R = 16 / KB;   // registers of a word
-        uint32_t wa[Z][NW], wb[Z][NW];
-        float acc[Z][4] = {};
+        uint32_t wa[S][NW], wb[S][NW];
+        float acc[S][4] = {};
 #pragma unroll
-        for (int s = 0; s < Z; ++s) {
+        for (int s = 0; s < S; ++s) {
           const uint8_t* kp = buf + s * C::TB + koff;
           load_words<(NW < 4 ? NW : 4)>(kp, wa[s]);
           load_words<(NW < 4 ? NW : 4)>(kp + 8 * rk, wb[s]);
@@ -592,7 +619,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 #pragma unroll
         for (int w = 0; w < NW; ++w)
 #pragma unroll
-          for (int s = 0; s < Z; ++s) {
+          for (int s = 0; s < S; ++s) {
             uint32_t x[R], y[R];
             key_regs<KB>(wa[s][w], x);
             key_regs<KB>(wb[s][w], y);
@@ -601,7 +628,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
               mma_t<__half>(acc[s], x[j], y[j], x[j + 1], y[j + 1], qf[w * R + j], qf[w * R + j + 1]);
           }
 #pragma unroll
-        for (int s = 0; s < Z; ++s)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint2 raw = *reinterpret_cast<const uint2*>(buf + s * C::TB + soff + 64 * i);
@@ -614,7 +641,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         if (edge) {  // rows outside [first, len) may hold anything
           const int lo = cs.first - base - tile_row_token(g), hi = cs.len - base - tile_row_token(g);
 #pragma unroll
-          for (int s = 0; s < Z; ++s)
+          for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               if (16 * s + 8 * i < lo || 16 * s + 8 * i >= hi) {
@@ -628,7 +655,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       // is 2^(t - m) s, which then stays in fp16's range whatever the scales are
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int s = 0; s < Z; ++s)
+      for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float lv = 0.0f;
@@ -655,9 +682,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       }
 
       // ---- probabilities, transposed into the second product's fragments
-      uint32_t pb[Z][2];
+      uint32_t pb[S][2];
 #pragma unroll
-      for (int s = 0; s < Z; ++s)
+      for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float p0 = ex2(sc[s][2 * i] - m[0]), p1 = ex2(sc[s][2 * i + 1] - m[1]);
@@ -675,7 +702,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 
       // ---- the second product
 #pragma unroll
-      for (int s = 0; s < Z; ++s) {
+      for (int s = 0; s < S; ++s) {
         const uint8_t* tile = buf + s * C::TB;
         if constexpr (!C::quant) {
           const int r = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
@@ -714,7 +741,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
             mma_t<__half>(o[j], v[0][2 * j], v[0][2 * j + 1], v[1][2 * j], v[1][2 * j + 1], pb[s][0], pb[s][1]);
         }
       }
-      }
       __syncwarp();
       issue(st);
       if (++st == C::NST) {
@@ -723,6 +749,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       }
     }
 
+    if (cs.cbase + cs.i1 <= cs.lo) break;  // the range ends before the unit's first chunk
     // ---- the unit's end: every warp finishes MT / W of the m-tiles, from what
     // the others hand it, in a fixed order
     if (cs.i1 < range) {
@@ -784,14 +811,14 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     }
     {
       const int64_t unit = static_cast<int64_t>(cs.b) * p.hkv + cs.h;
-      const bool ends = cs.cbase + cs.i1 == cs.first / (16 * S) + cs.n;
-      if (whole_start && threadIdx.x == 0) {
-        const int64_t last = (r0 + cs.i0 + cs.n - 1) / per;
+      const bool starts = cs.cbase + cs.i0 <= cs.lo, ends = cs.cbase + cs.i1 == cs.hi;
+      if (starts && threadIdx.x == 0) {
+        const int64_t last = (r0 + cs.hi - 1 - cs.cbase) / per;  // the CTA of the unit's last chunk
         Meta meta = {static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(ends ? 0 : last - blockIdx.x + 1),
                      cs.i0 > 0 ? 1 : 0, 0};
         *reinterpret_cast<int4*>(p.ws + unit * sizeof(Meta)) = *reinterpret_cast<int4*>(&meta);
       }
-      if (whole_start && ends) {
+      if (starts && ends) {
 #pragma unroll
         for (int hd = 0; hd < 2; ++hd) {
           const int head = 2 * t + hd;
@@ -827,7 +854,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     }
     if (cs.i1 >= range) break;
     cs = ns;
-    whole_start = true;
   }
   if (dead) {  // copies under way must not outlive the CTA's shared memory
     for (int i = 0; i < flying; ++i) {
@@ -927,7 +953,7 @@ cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
     return cudaFuncSetAttribute(attn_kernel<T, KB, VB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   const PagedAttnParams& p = *pp;
   // no more CTAs than the longest sequences that fit the tables can fill
-  const int64_t chunks = (static_cast<int64_t>(p.batch.max_pages) << p.pool.page_shift) / (16 * C::S) + 1;
+  const int64_t chunks = (static_cast<int64_t>(p.batch.max_pages) << p.pool.page_shift) / (16 * C::S) + 1 + C::E;
   const int64_t most = (chunks * p.hkv * p.batch.seqs + C::W - 1) / C::W;
   const int64_t wave = static_cast<int64_t>(sms) * C::CPS;
   cudaLaunchConfig_t cfg = {};
