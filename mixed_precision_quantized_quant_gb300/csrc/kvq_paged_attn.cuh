@@ -3,10 +3,15 @@
 //
 // Mathematics.  For the up to 8 query heads of a kv head, with t = scale
 // log2(e) q.k, running maximum m and l = sum 2^(t - m), o = sum 2^(t - m) v.
-// A key k = s c + z (c its codes) gives q.k = s (q.c) + z sum(q); a value row
-// gives p v = (p s) c + p z, whose second part is the same for every channel:
-// the codes go into the tensor cores as they are and the scales and zeros are
-// one multiply-add per (token, head).
+// A key k = s c + z (c its codes) gives q.k = s (q.c) + z sum(q).  A value row
+// is s (c - h) + z' with h the middle code, (2^b - 1) / 2, and z' = z + s h, so
+// p v = (p s)(c - h) + p z', whose second part is the same for every channel:
+// the codes go into the tensor cores as they are, the scales and zeros are one
+// multiply-add per (token, head), and h sum(p s), summed over the very weights
+// that were rounded by one more MMA on a row of ones, is taken off at the end.
+// Taking values from the middle code keeps the rounding of p s to what it would
+// be on the values themselves: with z below and s c above, both large, it was
+// twice that.
 //
 // Bound.  Every cached byte is read once; 2 * 8 heads * D products per token
 // and kv head are far below the tensor rate, so the floor is the copy rate,
@@ -16,8 +21,8 @@
 // head).  The chunks of all units in a row, with a few void places ahead of
 // each unit for what starting it costs, are cut into equal ranges, one per CTA
 // of one wave, so that neither many short sequences nor one long one leaves
-// CTAs idle.  The four warps of a CTA take its chunks in turn, each with a ring of NST
-// stages in shared memory that one bulk copy a page fills, and meet only at
+// CTAs idle.  The four warps of a CTA take its chunks in turn, each with a ring
+// of NST stages in shared memory that one bulk copy a page fills, and meet at
 // the end of a unit to merge.  A unit that lies in one range is written by its
 // CTA; one that several share leaves partial results, which a second kernel
 // (a programmatic dependent, resident when the first drains) joins in a fixed
@@ -29,16 +34,20 @@
 // second product, whose rows are channels.  The channel order inside each
 // product is free: a thread takes the channels that its own bytes hold, and q
 // is loaded in the same order.  Codes are taken as fp16 subnormals (code *
-// 2^-24 * 2^field), exact, with no conversion; the field's power of two is
-// taken out of q (keys) or of the result (values).
+// 2^-24 * 2^field): exact, one AND for two codes; a key field's power of two is
+// taken out of q, a value field's out of the result.  The tensor cores align
+// sums by the exponent field, so that a sum of subnormals keeps fewer bits the
+// lower the field: scores are 4e-6 to 9e-6 off (rms), which the weights can
+// bear.  Value fields are moved to bit 4 or higher first (one more shift for
+// four codes): at bits 0 .. 3 they cost half the bits of an fp16 output.
 //
 // Measured (GB300, device time with the join, copy rate 6771 GB/s): 8 x 32K
-// tokens x 8 kv heads in fp16 119 us, 96% of the copy rate; K4V2 39 us, 59%;
+// tokens x 8 kv heads in fp16 119 us, 96% of the copy rate; K4V2 41 us, 56%;
 // 16 x 4K x 8 in bf16 38 us, 77%, K8V4 21 us, 55%; one sequence of 256 tokens
 // 6 us.  About 9 us of each are the way to the first chunk (lengths, page
 // table, first copies: 3 dependent loads, 4.7 us), the uneven end of the CTAs
 // (2 to 4 us) and the join (3 us).  In between 16-bit rows stream at the copy
-// rate; narrow codes are bound by the ALU pipe and the issue slots (K4V2: 190
+// rate; narrow codes are bound by the ALU pipe and the issue slots (K4V2: 200
 // instructions a tile, 80 of them the masks, shifts and byte permutes that
 // make registers of two codes).
 #pragma once
@@ -207,13 +216,21 @@ template <int KB>
 __host__ __device__ constexpr int key_local(int r, int hi) {
   return KB == 8 ? 2 * r + hi : KB == 4 ? 8 * (r / 4) + r % 4 + 4 * hi : 16 * (r / 8) + r % 8 + 8 * hi;
 }
-// log2 of the power of two that the field of register (or channel) r carries
+// log2 of the power of two that the field of key register r, and of value
+// register (channel) r, carries
 template <int B>
-__host__ __device__ constexpr int field_shift(int r) {
+__host__ __device__ constexpr int key_field(int r) {
   return B == 4 ? 4 * (r % 2) : B == 2 ? 2 * (r % 8 < 5 ? r % 8 : r % 8 - 5) : 0;
 }
+template <int B>
+__host__ __device__ constexpr int val_field(int r) {
+  constexpr int two[8] = {4, 6, 4, 6, 8, 4, 6, 8};
+  return B == 8 ? 0 : B == 4 ? 4 : two[r % 8];
+}
 
-// Words of code rows -> registers of two fp16 subnormals each.
+__host__ __device__ constexpr float mid_code(int bits) { return 0.5f * ((1 << bits) - 1); }
+
+// Words of key code rows -> registers of two fp16 subnormals each.
 template <int B>
 __device__ __forceinline__ void key_regs(uint32_t w, uint32_t* r) {
   if (B == 8) {
@@ -233,14 +250,29 @@ __device__ __forceinline__ void key_regs(uint32_t w, uint32_t* r) {
     for (int i = 0; i < 3; ++i) r[5 + i] = u & (0x00030003u << (2 * i));
   }
 }
-// x: two tokens' 16 bits of codes (low half one token, high half the other).
+// x: two tokens' 16 bits of value codes (low half one token, high half the
+// other) -> registers of two fp16 subnormals each.
 template <int B>
 __device__ __forceinline__ void val_regs(uint32_t x, uint32_t* r) {
   if (B == 8) {
     r[0] = prmt(x, 0, 0x4240);
     r[1] = prmt(x, 0, 0x4341);
-  } else {
-    key_regs<B>(x, r);
+  } else if (B == 4) {  // fields at bits 4 .. 7
+    const uint32_t u = x >> 8;
+    r[0] = (x << 4) & 0x00f000f0u;
+    r[1] = x & 0x00f000f0u;
+    r[2] = (u << 4) & 0x00f000f0u;
+    r[3] = u & 0x00f000f0u;
+  } else {  // fields at bits 4, 6 and 8
+    const uint32_t y = x << 4, u = x >> 6;
+    r[0] = y & 0x00300030u;
+    r[1] = y & 0x00c000c0u;
+    r[2] = x & 0x00300030u;
+    r[3] = x & 0x00c000c0u;
+    r[4] = x & 0x03000300u;
+    r[5] = u & 0x00300030u;
+    r[6] = u & 0x00c000c0u;
+    r[7] = u & 0x03000300u;
   }
 }
 
@@ -258,7 +290,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   float* ml = reinterpret_cast<float*>(smem + 256);             // [warps][m 8, l 8]
   int64_t* sums = reinterpret_cast<int64_t*>(smem + 768);       // [2][warps] of the search
   int* found = reinterpret_cast<int*>(smem + 896);              // where the range starts: sequence, head, place
-  float2* qstat = reinterpret_cast<float2*>(smem + 512);        // [2][8 heads]
+  float2* qstat = reinterpret_cast<float2*>(smem + 512);        // [2][8 heads]: fac, qs (below)
   float4* mergebuf = reinterpret_cast<float4*>(smem + C::extra);  // [warps][warps - 1][QT][32]
   // 16 bits: q rows [2][8][D].  Codes: rows as they come [8][D], then their
   // fragments [2][NR / 4][32 lanes][4 registers]
@@ -415,13 +447,13 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       __half* h = reinterpret_cast<__half*>(f + in_run / 16 * 256) + in_run / 8 % 2;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        h[i / 4 * 256 + i % 4 * 2] = __float2half_rn(x[i] * (up * (1.0f / (1 << field_shift<KB>(i)))));
+        h[i / 4 * 256 + i % 4 * 2] = __float2half_rn(x[i] * (up * (1.0f / (1 << key_field<KB>(i)))));
     } else {
       uint32_t r[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = x[KB == 8 ? 2 * i : i], b = x[KB == 8 ? 2 * i + 1 : i + 4];
-        const float u = up * (1.0f / (1 << field_shift<KB>(i)));
+        const float u = up * (1.0f / (1 << key_field<KB>(i)));
         r[i] = h2_as_u32(__floats2half2_rn(a * u, b * u));
       }
       *reinterpret_cast<uint4*>(f + in_run / 8 * 128) = make_uint4(r[0], r[1], r[2], r[3]);
@@ -542,6 +574,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     }
     which ^= 1;
     float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, zs[2] = {0.0f, 0.0f};
+    float ones[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // codes: sum of the rounded weights, in every row
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -633,7 +666,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
           for (int i = 0; i < 2; ++i) {
             const uint2 raw = *reinterpret_cast<const uint2*>(buf + s * C::TB + soff + 64 * i);
             const float ks = __low2float(u32_as_h2(raw.x)), kz = __high2float(u32_as_h2(raw.x));
-            vs[s][i] = __low2float(u32_as_h2(raw.y)), vz[s][i] = __high2float(u32_as_h2(raw.y));
+            vs[s][i] = __low2float(u32_as_h2(raw.y));
+            vz[s][i] = fmaf(vs[s][i], mid_code(VB), __high2float(u32_as_h2(raw.y)));
 #pragma unroll
             for (int hd = 0; hd < 2; ++hd)
               sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[s][2 * i + hd], kz * qs[hd]);
@@ -673,6 +707,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
           m[hd] = mn;
           l[hd] *= f;
           zs[hd] *= f;
+          ones[hd] *= f;
 #pragma unroll
           for (int j = 0; j < MT; ++j) {
             o[j][hd] *= f;
@@ -736,6 +771,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
               val_regs<VB>(x, v[h]);
             }
           }
+          mma_t<__half>(ones, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[s][0], pb[s][1]);
 #pragma unroll
           for (int j = 0; j < MT; ++j)
             mma_t<__half>(o[j], v[0][2 * j], v[0][2 * j + 1], v[1][2 * j], v[1][2 * j + 1], pb[s][0], pb[s][1]);
@@ -763,6 +799,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         l[hd] += __shfl_xor_sync(0xffffffffu, l[hd], x);
         zs[hd] += __shfl_xor_sync(0xffffffffu, zs[hd], x);
       }
+      if constexpr (C::quant) zs[hd] = fmaf(ones[hd], -mid_code(VB), zs[hd]);  // values are taken from the middle code
       if (g == 0) {
         ml[warp * 16 + 2 * t + hd] = m[hd];
         ml[warp * 16 + 8 + 2 * t + hd] = l[hd];
@@ -775,8 +812,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       for (int q = 0; q < QT; ++q) {
         const int j = w * QT + q;
         float4 v = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
-        if constexpr (C::quant) {  // the field's power of two, and the zeros
-          const float u0 = 16777216.0f / (1 << field_shift<VB>(2 * j)), u1 = 16777216.0f / (1 << field_shift<VB>(2 * j + 1));
+        if constexpr (C::quant) {  // the field's power of two, and what all channels share
+          const float u0 = 16777216.0f / (1 << val_field<VB>(2 * j)), u1 = 16777216.0f / (1 << val_field<VB>(2 * j + 1));
           v = make_float4(fmaf(v.x, u0, zs[0]), fmaf(v.y, u0, zs[1]), fmaf(v.z, u1, zs[0]), fmaf(v.w, u1, zs[1]));
         }
         if (warp == w)
