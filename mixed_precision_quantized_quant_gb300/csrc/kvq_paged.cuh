@@ -76,6 +76,7 @@ struct PagedAttnParams {
   int q_vec;              // every row of q is 16-byte aligned
   uint8_t* ws;             // what the join needs of every unit, then partial results
   int64_t ws_partials;    // where those start
+  int solo;               // a CTA for each unit, no join (set at launch)
 };
 
 // ---------------------------------------------------------------- tile layout

@@ -228,6 +228,10 @@ kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch*
       (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
     return KVQ_ERR_ALIGN;
   if (workspace_bytes < kvq_paged_workspace_bytes(h, batch->num_seqs)) return KVQ_ERR_CAPACITY;
+  // a CTA's share of the work is held in 32 bits
+  const int64_t units = static_cast<int64_t>(batch->num_seqs) * h->cfg.num_kv_heads;
+  const int64_t tiles = static_cast<int64_t>(batch->max_pages) * h->cfg.page_size / kvq::kTile + 16;
+  if (tiles > (static_cast<int64_t>(INT_MAX) / 2 * h->sms) / units) return KVQ_ERR_UNSUPPORTED;
   const double sc = scale == 0.0f ? 1.0 / std::sqrt(static_cast<double>(h->cfg.head_dim)) : scale;
   p.out = out;
   p.lse = lse;

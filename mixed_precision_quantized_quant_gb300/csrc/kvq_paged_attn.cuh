@@ -27,6 +27,7 @@
 // CTA; one that several share leaves partial results, which a second kernel
 // (a programmatic dependent, resident when the first drains) joins in a fixed
 // order.  Nothing is counted across CTAs, so the workspace needs no clearing.
+// Short tables are not split (see attn_as).
 //
 // Layout.  Products are taken transposed: keys are the 16 rows of an MMA and
 // query heads its 8 columns, so that 8 heads fill it.  The score fragment,
@@ -44,7 +45,7 @@
 // Measured (GB300, device time with the join, copy rate 6771 GB/s): 8 x 32K
 // tokens x 8 kv heads in fp16 119 us, 96% of the copy rate; K4V2 41 us, 56%;
 // 16 x 4K x 8 in bf16 38 us, 77%, K8V4 21 us, 55%; one sequence of 256 tokens
-// 6 us.  About 9 us of each are the way to the first chunk (lengths, page
+// 5 us.  About 9 us of each are the way to the first chunk (lengths, page
 // table, first copies: 3 dependent loads, 4.7 us), the uneven end of the CTAs
 // (2 to 4 us) and the join (3 us).  In between 16-bit rows stream at the copy
 // rate; narrow codes are bound by the ALU pipe and the issue slots (K4V2: 200
@@ -52,6 +53,7 @@
 // make registers of two codes).
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "kvq_paged.cuh"
@@ -313,83 +315,101 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- the CTA's range of places, and the unit it starts in: prefix sums of
-  // the sequences' places, 128 sequences at a time
-  const int B = p.batch.seqs;
-  // the page table on its way into L2 while the lengths are: a small one whole
-  {
-    const int64_t lines = (static_cast<int64_t>(B - 1) * p.batch.table_stride + p.batch.max_pages + 31) / 32;
-    const int line = blockIdx.x * kThreads + threadIdx.x;
-    if (lines <= 2048 && line < lines)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.batch.table + 32 * line));
-  }
-  auto chunks_of = [&](int b) {
-    if (b >= B) return static_cast<int64_t>(0);
-    const int raw = __ldg(p.batch.lens + b), len = seq_len(p, b);
-    if (blockIdx.x == 0 && raw != len) atomicExch(p.pool.err, kErrBadState);
-    return static_cast<int64_t>(place_count<S, E>(p, len)) * p.hkv;
-  };
-  int64_t total = 0;
-  for (int b0 = kThreads; b0 < B; b0 += kThreads) total += chunks_of(b0 + threadIdx.x);  // but the first 128
-  int64_t held = chunks_of(threadIdx.x), incl = held;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (B > kThreads) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 31) {
-    sums[warp] = incl;
-    sums[kWarps + warp] = total;
-  }
-  __syncthreads();
-  int64_t before = 0;  // places of the sequences looked at so far
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    total += sums[w] + sums[kWarps + w];
-    before += sums[w];
-    if (w < warp) incl += sums[w];
-  }
-  int64_t per = total + gridDim.x - 1;
-  per = per >> 32 ? per / gridDim.x : static_cast<uint32_t>(per) / gridDim.x;  // (64 bits cost over 100 instructions)
-  if (per < kWarps) per = kWarps;
-  const int64_t r0 = per * blockIdx.x;
-  if (r0 >= total) return;  // the same for every thread
-  const int range = static_cast<int>(total - r0 < per ? total - r0 : per);
-  for (int b0 = 0;;) {
-    const int64_t at = incl - held;
-    if (r0 >= at && r0 < incl) {
-      const int n = static_cast<int>(held / p.hkv), off = static_cast<int>(r0 - at);
-      found[0] = b0 + threadIdx.x;
-      found[1] = off / n;
-      found[2] = off % n;
+  Seg cs;
+  int64_t per = 0, r0 = 0;
+  int range = 0;
+  if (p.solo) {
+    // one CTA for each unit: no search, and nothing to join
+    cs.b = blockIdx.x / p.hkv;
+    cs.h = blockIdx.x - cs.b * p.hkv;
+    if (seq_len(p, cs.b) == 0) {
+      const int64_t row = static_cast<int64_t>(blockIdx.x) * p.gqa;
+      for (int x = threadIdx.x; x < p.gqa * D; x += kThreads) reinterpret_cast<T*>(p.out)[row * D + x] = Num<T>::from(0.0f);
+      if (p.lse && threadIdx.x < p.gqa) p.lse[row + threadIdx.x] = -INFINITY;
     }
-    __syncthreads();
-    if (r0 < before) break;
-    b0 += kThreads;
-    held = incl = chunks_of(b0 + threadIdx.x);
+    if (threadIdx.x == 0 && __ldg(p.batch.lens + cs.b) != seq_len(p, cs.b)) atomicExch(p.pool.err, kErrBadState);
+    if (seq_len(p, cs.b) == 0) return;
+    seg_at<S, E>(p, cs, 0, 0, INT_MAX);
+    range = cs.i1;
+    __syncthreads();  // the barriers and the cleared fragments are there
+  } else {
+    // ---- the CTA's range of places, and the unit it starts in: prefix sums of
+    // the sequences' places, 128 sequences at a time
+    const int B = p.batch.seqs;
+    // the page table on its way into L2 while the lengths are: a small one whole
+    {
+      const int64_t lines = (static_cast<int64_t>(B - 1) * p.batch.table_stride + p.batch.max_pages + 31) / 32;
+      const int line = blockIdx.x * kThreads + threadIdx.x;
+      if (lines <= 2048 && line < lines)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.batch.table + 32 * line));
+    }
+    auto chunks_of = [&](int b) {
+      if (b >= B) return static_cast<int64_t>(0);
+      const int raw = __ldg(p.batch.lens + b), len = seq_len(p, b);
+      if (blockIdx.x == 0 && raw != len) atomicExch(p.pool.err, kErrBadState);
+      return static_cast<int64_t>(place_count<S, E>(p, len)) * p.hkv;
+    };
+    int64_t total = 0;
+    for (int b0 = kThreads; b0 < B; b0 += kThreads) total += chunks_of(b0 + threadIdx.x);  // but the first 128
+    int64_t held = chunks_of(threadIdx.x), incl = held;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (lane == 31) sums[warp] = incl;
+    if (B > kThreads) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 31) {
+      sums[warp] = incl;
+      sums[kWarps + warp] = total;
+    }
     __syncthreads();
-    incl += before;
+    int64_t before = 0;  // places of the sequences looked at so far
+    total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
+      total += sums[w] + sums[kWarps + w];
       before += sums[w];
       if (w < warp) incl += sums[w];
     }
+    per = total + gridDim.x - 1;
+    per = per >> 32 ? per / gridDim.x : static_cast<uint32_t>(per) / gridDim.x;  // (64 bits cost over 100 instructions)
+    if (per < kWarps) per = kWarps;
+    r0 = per * blockIdx.x;
+    if (r0 >= total) return;  // the same for every thread
+    range = static_cast<int>(total - r0 < per ? total - r0 : per);
+    for (int b0 = 0;;) {
+      const int64_t at = incl - held;
+      if (r0 >= at && r0 < incl) {
+        const int64_t n = held / p.hkv, off = r0 - at;
+        found[0] = b0 + threadIdx.x;
+        found[1] = static_cast<int>(off / n);
+        found[2] = static_cast<int>(off % n);
+      }
+      __syncthreads();
+      if (r0 < before) break;
+      b0 += kThreads;
+      held = incl = chunks_of(b0 + threadIdx.x);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) sums[warp] = incl;
+      __syncthreads();
+      incl += before;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        before += sums[w];
+        if (w < warp) incl += sums[w];
+      }
+    }
+    cs.b = found[0];
+    cs.h = found[1];
+    seg_at<S, E>(p, cs, 0, found[2], range);
   }
-  Seg cs;
-  cs.b = found[0];
-  cs.h = found[1];
-  seg_at<S, E>(p, cs, 0, found[2], range);
 
   // ---- q rows of a unit into shared memory: asked for ahead of the copies of
   // its chunks (behind them, the first came 3 us late), of the next unit while
@@ -849,7 +869,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     {
       const int64_t unit = static_cast<int64_t>(cs.b) * p.hkv + cs.h;
       const bool starts = cs.cbase + cs.i0 <= cs.lo, ends = cs.cbase + cs.i1 == cs.hi;
-      if (starts && threadIdx.x == 0) {
+      if (starts && !p.solo && threadIdx.x == 0) {
         const int64_t last = (r0 + cs.hi - 1 - cs.cbase) / per;  // the CTA of the unit's last chunk
         Meta meta = {static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(ends ? 0 : last - blockIdx.x + 1),
                      cs.i0 > 0 ? 1 : 0, 0};
@@ -988,10 +1008,19 @@ cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
   using C = Shape<KB, VB, D>;
   if (!pp)
     return cudaFuncSetAttribute(attn_kernel<T, KB, VB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
-  const PagedAttnParams& p = *pp;
-  // no more CTAs than the longest sequences that fit the tables can fill
-  const int64_t chunks = (static_cast<int64_t>(p.batch.max_pages) << p.pool.page_shift) / (16 * C::S) + 1 + C::E;
-  const int64_t most = (chunks * p.hkv * p.batch.seqs + C::W - 1) / C::W;
+  PagedAttnParams p = *pp;
+  // Short tables are not split: a CTA for each unit, and no join.  Measured with
+  // 1, 8 and 64 sequences x 8 kv heads, unsplit against split, us: fp16, 512
+  // tokens 7.0, 7.5, 26 against 7.7, 9.5, 30, 1024 tokens 10.6, 11.1, 44 against
+  // 9.6, 10.1, 50; K8V4, 512 tokens 6.5, 6.9, 17 against 7.5, 8.7, 19, 1024
+  // tokens 9.8, 10.1, 28 against 8.1, 10.3, 26; K4V2, 1024 tokens 8.1, 8.6, 21
+  // against 7.9, 9.7, 23, 2048 tokens 13.0, 13.7, 33 against 8.4, 11.8, 34.
+  // Otherwise one wave, or as many CTAs as the longest sequences that fit the
+  // tables can fill.
+  const int64_t tokens = static_cast<int64_t>(p.batch.max_pages) << p.pool.page_shift;
+  const int64_t units = static_cast<int64_t>(p.hkv) * p.batch.seqs;
+  p.solo = tokens <= (C::S == 4 ? 1024 : 512);
+  const int64_t most = ((tokens / (16 * C::S) + 1 + C::E) * units + C::W - 1) / C::W;
   const int64_t wave = static_cast<int64_t>(sms) * C::CPS;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1000,12 +1029,12 @@ cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = s;
-  cfg.gridDim = dim3(static_cast<unsigned>(most < wave ? most : wave));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.solo ? units : most < wave ? most : wave));
   cfg.blockDim = dim3(C::threads);
   cfg.dynamicSmemBytes = C::smem;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kernel<T, KB, VB, D>, p);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.hkv * p.batch.seqs));
+  if (e != cudaSuccess || p.solo) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(units));
   cfg.blockDim = dim3(2 * D);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<T, C::quant, D>, p);
