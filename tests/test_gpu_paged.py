@@ -145,6 +145,54 @@ def test_append_heads_and_odd_strides(d, hq, hkv, kb, vb):
         _check_append(c, how=how, dim=d // 2)
 
 
+@pytest.mark.parametrize("how", ["fused", "odd"])
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 4), (2, 2)])
+@pytest.mark.parametrize("d,hq,hkv,interleaved", [(64, 6, 3, False), (128, 5, 1, True)])
+def test_append_and_read_many_rows(d, hq, hkv, interleaved, kb, vb, how):
+    # enough rows for several a CTA (the few-row form is left at 3 an SM): runs that cross tokens,
+    # sequences and sequences without rows, then rows behind the last one
+    lens = [300, 7, 0, 0, 260, 1, 90]
+    c = Case(lens, [290, 7, 0, 0, 250, 1, 60], kb=kb, vb=vb, d=d, hq=hq, hkv=hkv, page=64, fill=False, dtype="bf16")
+    _check_append(c, how=how, dim=d // 2, interleaved=interleaved, extra=9)
+    k, v = (torch.full((617, hkv, d), 7.0, dtype=c.dtype, device="cuda") for _ in range(2))
+    c.cache.read(0, c.batch, 617, K=k, V=v)
+    exp = [torch.full((617, hkv, d), 7.0, dtype=c.dtype) for _ in range(2)]
+    for row, b, p in c.places():
+        for h in range(hkv):
+            for is_v in (0, 1):
+                x, _, _ = c.model.get(c.table[b, p // 64], p % 64, h, bool(is_v))
+                exp[is_v][row, h] = torch.from_numpy(x).float().to(c.dtype)
+    assert torch.equal(k.cpu(), exp[0]) and torch.equal(v.cpu(), exp[1])
+
+
+@pytest.mark.parametrize("kb,vb", [(16, 16), (4, 2)])
+def test_append_of_several_waves_is_that_of_its_parts(kb, vb):
+    n, hq, hkv, d, P = 20_011, 4, 2, 64, 64
+    pages = -(-n // P)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = torch.randn(n, hq + 2 * hkv, d, generator=g, device="cuda").half()
+    q, k, v = rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:]
+    rot = K.Rotation(K.rotation_table(n, d))
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    bufs = [torch.zeros(K.kvq_paged_bytes(K.make_paged_config([(kb, vb)], hq, hkv, d, P, pages)), dtype=torch.uint8, device="cuda")
+            for _ in range(2)]
+    whole, parts = (K.KVQPagedCache([(kb, vb)], hq, hkv, d, P, pages, buffer=x) for x in bufs)
+
+    def batch(a, b):
+        return K.PagedBatch(table, torch.tensor([b], dtype=torch.int32).cuda(), torch.tensor([0, b - a], dtype=torch.int32).cuda())
+
+    qo = whole.append(0, batch(0, n), k, v, q=q, rotation=rot)
+    for a in range(0, n, 400):
+        b = min(n, a + 400)
+        assert torch.equal(parts.append(0, batch(a, b), k[a:b], v[a:b], q=q[a:b], rotation=rot), qo[a:b])
+    assert torch.equal(*bufs)
+    rk, rv = whole.read(0, batch(0, n), n)
+    for a in range(0, n, 400):
+        b = min(n, a + 400)
+        pk, pv = parts.read(0, batch(a, b), b - a)
+        assert torch.equal(pk, rk[a:b]) and torch.equal(pv, rv[a:b])
+
+
 def test_append_without_queries_or_rotation_and_in_place():
     _check_append(Case([33, 2], fill=False), with_q=False)
     _check_append(Case([33, 2], kb=4, vb=4, fill=False), with_q=False, dim=64)
@@ -225,24 +273,32 @@ def _check_attn(c, scale=0.0, window=0, how="fused", q=None, stream=None):
 LENS = [0, 1, 2, 15, 16, 17, 31, 33, 64, 65, 129, 200]
 
 
+# narrow tables give each (sequence, head) a CTA of its own, wide ones are split
+@pytest.mark.parametrize("width", [None, 200])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("kb,vb", PAIRS)
-def test_attn_pairs(kb, vb, d, dtype):
-    _check_attn(Case(LENS, kb=kb, vb=vb, d=d, dtype=dtype, page=32))
+def test_attn_pairs(kb, vb, d, dtype, width):
+    _check_attn(Case(LENS, kb=kb, vb=vb, d=d, dtype=dtype, page=32, width=width))
 
 
+@pytest.mark.parametrize("width", [None, 100])
 @pytest.mark.parametrize("kb,vb", [(16, 16), (8, 8), (4, 2)])
 @pytest.mark.parametrize("page", [16, 64, 128])
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1), (7, 1), (6, 2), (28, 4), (5, 5)])
-def test_attn_heads_and_pages(hq, hkv, page, kb, vb):
-    _check_attn(Case([70, 1, 130, 0, 19], kb=kb, vb=vb, d=128, hq=hq, hkv=hkv, page=page), how="odd")
+def test_attn_heads_and_pages(hq, hkv, page, kb, vb, width):
+    _check_attn(Case([70, 1, 130, 0, 19], kb=kb, vb=vb, d=128, hq=hq, hkv=hkv, page=page, width=width), how="odd")
 
 
+@pytest.mark.parametrize("width", [None, 300])
 @pytest.mark.parametrize("kb,vb", [(16, 16), (8, 4), (2, 2)])
 @pytest.mark.parametrize("window", [1, 5, 16, 50, 128, 4000])
-def test_attn_window(window, kb, vb):
-    _check_attn(Case(LENS, kb=kb, vb=vb, d=128, page=16), window=window, scale=0.3)
+def test_attn_window(window, kb, vb, width):
+    c = Case(LENS, kb=kb, vb=vb, d=128, page=16, width=width)
+    for b, n in enumerate(c.lens):  # pages wholly before the window may be gone
+        c.table[b, :max(0, n - window) // 16] = -1
+    c.batch = K.PagedBatch(torch.from_numpy(c.table).cuda(), torch.tensor(c.lens, dtype=torch.int32).cuda())
+    _check_attn(c, window=window, scale=0.3)
 
 
 @pytest.mark.parametrize("kb,vb", [(16, 16), (4, 4)])
@@ -250,6 +306,80 @@ def test_attn_window(window, kb, vb):
 def test_attn_long_and_unequal(kb, vb, dtype):
     # one long sequence beside short ones: splits of one unit, and many units in one split
     _check_attn(Case([3000, 1, 40, 0, 700] + [3] * 20, kb=kb, vb=vb, d=64, hq=4, hkv=1, page=64, dtype=dtype))
+
+
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 2)])
+@pytest.mark.parametrize("width", [4, 80])
+def test_attn_many_sequences(kb, vb, width):
+    # more sequences than a CTA looks at together, runs of empty ones among them
+    lens = [0] * 140 + [5, 0, 33] * 40 + [0] * 30 + [61, 2]
+    _check_attn(Case(lens, kb=kb, vb=vb, d=64, hq=2, hkv=1, page=16, width=width))
+
+
+@pytest.mark.parametrize("kb,vb", [(16, 16), (4, 2), (8, 8)])
+def test_attn_very_long_over_repeated_pages(kb, vb):
+    # 300,000 tokens made of 16 pages in random order: a weight counts as often as its page
+    n, P = 300_000, 128
+    c = Case([16 * P], kb=kb, vb=vb, d=128, hq=8, hkv=1, page=P)
+    k, kc, _ = c.model.rows(c.table[0], 0, 16 * P, 0, False)
+    v, vc, vs = c.model.rows(c.table[0], 0, 16 * P, 0, True)
+    order = np.random.default_rng(3).integers(0, 16, -(-n // P))
+    table = torch.from_numpy(c.table[0][order][None].astype(np.int32)).cuda()
+    batch = K.PagedBatch(table, torch.tensor([n], dtype=torch.int32).cuda())
+    q = c.rows(1, 8)
+    out, lse = c.cache.decode_attn(0, batch, q, return_lse=True)
+    count = np.zeros(16 * P)
+    for i, o in enumerate(order):
+        m = min(P, n - i * P)
+        count[o * P:o * P + m] += 1
+    qq = q[0].double().cpu().numpy()
+    t = qq @ k.T / math.sqrt(128)
+    p = np.exp(t - t.max(1, keepdims=True)) * count
+    eo, el = p @ v / p.sum(1, keepdims=True), t.max(1) + np.log(p.sum(1))
+    # as in paged_testutil.attend, with chains of n / 8 / 4 tiles' additions at the most in a warp of a full wave
+    u = 2.0 ** -11
+    e = 144 * 2.0 ** -23 / math.sqrt(128) * (np.abs(qq) @ (np.abs(kc) + np.abs(k - kc)).T).max(1)[:, None] + 2.0 ** -20
+    f = (n / 400 + 64) * 2.0 ** -23
+    codes = np.abs(vc) / np.where(vs > 0, vs, 1.0)[:, None]
+    tol = (u * np.abs(eo) + (u * (p @ np.abs(vc)) + 2.0 ** -25 * (p / np.maximum(count, 1) * vs).max(1)[:, None]
+                             * (count @ codes)) / p.sum(1, keepdims=True)
+           + (2 * e + f) * (p @ (np.abs(v) + np.abs(v - vc))) / p.sum(1, keepdims=True))
+    assert (np.abs(out[0].double().cpu().numpy() - eo) <= tol).all()
+    assert (np.abs(lse[0].double().cpu().numpy() - el) <= 2 * e[:, 0] + f + 2.0 ** -19 * np.abs(el)).all()
+    assert c.cache.device_error() == 0
+
+
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 4)])
+def test_pages_past_32_bits(kb, vb):
+    # a pool of over 4 GiB: its last pages hold what its first ones do
+    P, hkv, d = 128, 8, 128
+    page = hkv * P * (512 if kb == 16 else 200)
+    pages = (5 << 30) // page
+    c = K.KVQPagedCache([(kb, vb)], 8, hkv, d, P, pages)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(300, hkv, d, generator=g, device="cuda").half() for _ in range(2))
+    q = torch.randn(1, 8, d, generator=g, device="cuda").half()
+    rot = K.Rotation(K.rotation_table(300, d))
+    res = []
+    for t in ([0, 1, 2], [pages - 1, pages - 3, pages - 2]):
+        b = K.PagedBatch(torch.tensor([t], dtype=torch.int32).cuda(), torch.tensor([300], dtype=torch.int32).cuda(),
+                         torch.tensor([0, 300], dtype=torch.int32).cuda())
+        c.append(0, b, k, v, rotation=rot)
+        res.append((c.decode_attn(0, b, q), *c.read(0, b, 300)))
+    assert all(torch.equal(x, y) for x, y in zip(*res))
+    assert c.device_error() == 0 and float(res[0][0].abs().max()) > 0
+
+
+def test_nan_in_an_attended_row_shows():
+    for kb in (16, 8):
+        c = Case([40, 20], kb=kb, vb=kb, d=64)
+        x = torch.ones(1, 2, 64, dtype=torch.float16, device="cuda")
+        bad = x.clone()
+        bad[0, 1, 3] = math.nan
+        b = K.PagedBatch(c.batch._keep[0][:1].contiguous(), torch.tensor([12], dtype=torch.int32).cuda())
+        c.cache.append(0, b, x, bad)
+        out = c.cache.decode_attn(0, c.batch, c.rows(2, 8))
+        assert out[0, 4:].isnan().any() and not out[0, :4].isnan().any() and not out[1].isnan().any()
 
 
 def test_attn_rising_scores_and_large_ones():
@@ -423,3 +553,74 @@ def test_bad_pages_lengths_and_positions_are_reported_and_not_followed():
     assert c.cache.device_error() == 5
     assert np.array_equal(c.download(), before)
     assert c.cache.device_error() == 0
+
+
+def test_refusals():
+    c = Case([20, 5], kb=4, vb=4, d=64, hq=4, hkv=2)
+    q, k, v = c.rows(2, 4), c.rows(2, 2), c.rows(2, 2)
+    a, t, r = c.cache.append, c.cache.decode_attn, c.cache.read
+    half, table, lens = torch.float16, c.batch._keep[0], c.batch._keep[1]
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32).cuda()
+    before = c.download().copy()
+    for fn in (lambda: a(0, c.batch, k[:1], v[:1]), lambda: a(0, c.batch, k, v[:1]), lambda: a(0, c.batch, k.float(), v),
+               lambda: a(0, c.batch, k.cpu(), v), lambda: a(0, c.batch, k, v, q_out=q), lambda: a(0, c.batch, k, q),
+               lambda: a(0, c.batch, k, v, q=k), lambda: a(0, c.batch, k.transpose(1, 2).contiguous().transpose(1, 2), v),
+               lambda: a(0, c.batch, k, v, rotation=K.Rotation(K.rotation_table(40, 128))),
+               lambda: a(0, c.batch, k, v, rotation=K.Rotation(K.rotation_table(40, 64), positions=cu[:1])),
+               lambda: t(0, c.batch, q[:1]), lambda: t(0, c.batch, q.bfloat16()), lambda: t(0, c.batch, k),
+               lambda: t(0, c.batch, q, out=torch.empty(2, 4, 64, device="cuda")),
+               lambda: t(0, c.batch, q, out=torch.empty(2, 64, 4, dtype=half, device="cuda").transpose(1, 2)),
+               lambda: r(0, c.batch, 3), lambda: r(0, c.batch, 2, K=torch.empty(2, 2, 64, device="cuda")),
+               lambda: K.PagedBatch(table.long(), lens), lambda: K.PagedBatch(table, lens.cpu()),
+               lambda: K.PagedBatch(table, lens[:1]), lambda: K.PagedBatch(table.t(), lens),
+               lambda: K.PagedBatch(table, lens, lens), lambda: K.PagedBatch(table[:0], lens[:0]),
+               lambda: K.Rotation(torch.zeros(4, 24, device="cuda")), lambda: K.Rotation(torch.zeros(4, 0, device="cuda")),
+               lambda: K.Rotation(torch.zeros(4, 64, dtype=half, device="cuda")),
+               lambda: K.KVQPagedCache([(4, 4)], 4, 2, 64, 16, 4, dtype=torch.float32),
+               lambda: K.KVQPagedCache([(4, 4)], 4, 2, 64, 16, 4, buffer=torch.zeros(9, device="cuda"))):
+        with pytest.raises(ValueError):
+            fn()
+    for fn, code in ((lambda: a(1, c.batch, k, v), 1), (lambda: a(-1, c.batch, k, v), 1), (lambda: t(1, c.batch, q), 1),
+                     (lambda: t(0, c.batch, q, window=-1), 1), (lambda: t(0, c.batch, q, scale=math.nan), 1),
+                     (lambda: t(0, c.batch, q, scale=math.inf), 1), (lambda: r(2, c.batch, 2), 1),
+                     (lambda: t(0, c.batch, q, out=torch.empty(2 * 4 * 64 + 1, dtype=half, device="cuda")[1:].view(2, 4, 64)), 3),
+                     (lambda: K.KVQPagedCache([(3, 3)], 4, 2, 64, 16, 4), 1),
+                     (lambda: K.KVQPagedCache([(4, 4)], 4, 2, 64, 16, 4, buffer=torch.zeros(64, dtype=torch.uint8, device="cuda")), 4)):
+        with pytest.raises(K.KVQError) as e:
+            fn()
+        assert e.value.status == code
+    # the C entry itself: missing rows, workspaces and counts
+    L, h, b, s = K.load(), c.cache.h, c.batch.args, torch.cuda.current_stream().cuda_stream
+    rk, rq = c.cache._rows(k, "k", 2, 2), c.cache._rows(q, "q", 2, 4)
+    out, ws = torch.empty(2, 4, 64, dtype=half, device="cuda"), torch.empty(K.kvq_paged_workspace_bytes(h, 2), dtype=torch.uint8, device="cuda")
+    o, w, nw = out.data_ptr(), ws.data_ptr(), ws.numel()
+    assert L.kvq_paged_append(h, 0, b, rk, None, None, None, None, 2, s) == 1
+    assert L.kvq_paged_append(h, 0, b, rk, rk, rq, None, None, 2, s) == 1
+    assert L.kvq_paged_append(h, 0, b, rk, rk, None, None, None, -1, s) == 1
+    assert L.kvq_paged_append(h, 0, None, rk, rk, None, None, None, 2, s) == 1
+    assert L.kvq_paged_append(h, 0, b, K.Rows(rk.data + 1, 1, 1), rk, None, None, None, 2, s) == 3
+    assert L.kvq_paged_append(h, 0, b, K.Rows(None, 1, 1), rk, None, None, None, 2, s) == 1
+    rot = K.RotationArgs(w + 4, None, 1, 64, 0)
+    assert L.kvq_paged_append(h, 0, b, rk, rk, None, None, rot, 2, s) == 3
+    for bad in (K.RotationArgs(w, None, 0, 64, 0), K.RotationArgs(w, None, 1, 24, 0), K.RotationArgs(w, None, 1, 80, 0),
+                K.RotationArgs(w, None, 1, 64, 2), K.RotationArgs(None, None, 1, 64, 0)):
+        assert L.kvq_paged_append(h, 0, b, rk, rk, None, None, bad, 2, s) == 1
+    assert L.kvq_paged_read(h, 0, b, None, None, 2, s) == 1
+    assert L.kvq_paged_decode_attn(h, 0, b, rq, None, None, 0.0, 0, w, nw, s) == 1
+    assert L.kvq_paged_decode_attn(h, 0, b, rq, o, None, 0.0, 0, None, nw, s) == 1
+    assert L.kvq_paged_decode_attn(h, 0, b, rq, o, None, 0.0, 0, w + 16, nw, s) == 3
+    assert L.kvq_paged_decode_attn(h, 0, b, rq, o, o + 2, 0.0, 0, w, nw, s) == 3
+    assert L.kvq_paged_decode_attn(h, 0, b, rq, o, None, 0.0, 0, w, nw - 1, s) == 4
+    for field, value in (("num_seqs", 0), ("max_pages", 0), ("table_stride", 1), ("page_table", None), ("seq_lens", None),
+                         ("max_pages", 2 ** 27)):
+        x = K.PagedBatchArgs.from_buffer_copy(b)
+        setattr(x, field, value)
+        if field == "max_pages" and value:
+            x.table_stride = value
+        assert L.kvq_paged_decode_attn(h, 0, x, rq, o, None, 0.0, 0, w, nw, s) == 1, field
+    assert np.array_equal(c.download(), before) and c.cache.device_error() == 0
+    # nothing to do
+    a(0, K.PagedBatch(table, lens, torch.zeros(3, dtype=torch.int32, device="cuda")), k[:0], v[:0])
+    c.cache.close()
+    with pytest.raises(K.KVQError):
+        t(0, c.batch, q)
