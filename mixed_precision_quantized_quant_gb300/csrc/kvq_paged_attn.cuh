@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       }
 
       // ---- probabilities, transposed into the second product's fragments
-      uint32_t pb[S][2];
+      uint32_t pb[S][2], rest[S][2];  // (rest: 16 bits only)
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -751,7 +751,12 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
             // one rounding to fp16: at most 2^-11 of the weight
             pb[s][i] = transpose8(h2_as_u32(__floats2half2_rn(p0 * vs[s][i], p1 * vs[s][i])));
           } else {
-            pb[s][i] = transpose8(pack2<T>(p0, p1));  // one rounding of the weight to the cache's type
+            // the weight as two numbers of the cache's type, 16 (bf16) or 22 bits
+            // of it: the second product costs 8 MMAs a tile that memory hides
+            const uint32_t hi = pack2<T>(p0, p1);
+            const T* h = reinterpret_cast<const T*>(&hi);
+            pb[s][i] = transpose8(hi);
+            rest[s][i] = transpose8(pack2<T>(p0 - Num<T>::to(h[0]), p1 - Num<T>::to(h[1])));
           }
         }
 
@@ -767,6 +772,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
             uint32_t a[4];
             ldsm_x4_t(a, row + 16 * tile_chunk16(2 * j + c, r));
             mma_t<T>(o[j], a[0], a[1], a[2], a[3], pb[s][0], pb[s][1]);
+            mma_t<T>(o[j], a[0], a[1], a[2], a[3], rest[s][0], rest[s][1]);
           }
         } else {
           // [pair (t, t+4) or (t+8, t+12)][channel of the thread]
