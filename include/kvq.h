@@ -342,6 +342,9 @@ const char* kvq_status_string(kvq_status s);
  *     it may come from several threads and streams.  The caller orders calls
  *     that append to a page with those that read or append to the same page.
  *   - The current device must be the one of kvq_paged_create() (KVQ_ERR_ARG).
+ *   - The tensors of a batch must not change while a call that reads them runs:
+ *     its result has no meaning then (but nothing outside its tensors is
+ *     touched, and every wait ends).
  *   - What only the device can see (a page number outside the pool, a length
  *     past the table's width, a position past the rotation's table, fewer
  *     tokens in a sequence than it has new rows) is never followed:
@@ -358,8 +361,8 @@ typedef struct {
   uint8_t v_bits;
 } kvq_paged_layer_cfg;
 
-/* num_q_heads % num_kv_heads == 0 and num_q_heads / num_kv_heads <= 8;
- * head_dim in {64, 128}; page_size in {16, 32, 64, 128};
+/* num_q_heads % num_kv_heads == 0 and num_q_heads / num_kv_heads <= 8, at most
+ * 65536 heads and layers; head_dim in {64, 128}; page_size in {16, 32, 64, 128};
  * dtype: KVQ_FP16 or KVQ_BF16, the type of q, K, V, out and of 16-bit rows. */
 typedef struct {
   int32_t num_layers;
@@ -469,7 +472,7 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
  * positions max(0, len - window) .. len - 1 (window 0: all of them).
  *   q: [num_seqs][num_q_heads] rows (cu_tokens is not looked at).
  *   out: [num_seqs][num_q_heads][head_dim] contiguous, 16-byte aligned, the
- *     cache's type; lse: fp32 [num_seqs][num_q_heads] or NULL: the natural
+ *     cache's type, overlapping no other argument; lse: fp32 [num_seqs][num_q_heads] or NULL: the natural
  *     logarithm of the sum of exp(scale * q.k).  A sequence with no token gets
  *     0, and -infinity.
  *   scale: multiplies the scores; 0 means 1 / sqrt(head_dim).

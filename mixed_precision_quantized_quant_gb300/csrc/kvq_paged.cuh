@@ -77,6 +77,7 @@ struct PagedAttnParams {
   uint8_t* ws;             // what the join needs of every unit, then partial results
   int64_t ws_partials;    // where those start
   int solo;               // a CTA for each unit, no join (set at launch)
+  int ctas;               // of the attention kernel (set at launch)
 };
 
 // ---------------------------------------------------------------- tile layout

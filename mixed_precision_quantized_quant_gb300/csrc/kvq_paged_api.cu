@@ -23,7 +23,7 @@ struct Trace {
 
 constexpr int64_t kAlign = 256;
 constexpr int64_t kTail = 256;  // the library's own bytes behind the pages: the error word
-constexpr int kMaxLayers = 1 << 16;
+constexpr int kMaxLayers = 1 << 16, kMaxHeads = 1 << 16;
 
 struct PagedLayer {
   int kb, vb, tile_bytes;
@@ -32,6 +32,7 @@ struct PagedLayer {
 
 bool shape_ok(const kvq_paged_config* c) {
   return c && c->layers && c->num_layers >= 1 && c->num_layers <= kMaxLayers && c->num_q_heads >= 1 &&
+         c->num_q_heads <= kMaxHeads &&
          c->num_kv_heads >= 1 && c->num_q_heads % c->num_kv_heads == 0 && (c->head_dim == 64 || c->head_dim == 128) &&
          (c->page_size == 16 || c->page_size == 32 || c->page_size == 64 || c->page_size == 128) &&
          c->num_pages >= 1 && (c->dtype == KVQ_FP16 || c->dtype == KVQ_BF16);

@@ -128,8 +128,8 @@ __device__ __forceinline__ int place_count(const PagedAttnParams& p, int len) {
 }
 
 template <int S, int E>
-__device__ __forceinline__ void seg_at(const PagedAttnParams& p, Seg& s, int i0, int skip, int range) {
-  s.len = seq_len(p, s.b);
+__device__ __forceinline__ void seg_at(const PagedAttnParams& p, Seg& s, int len, int i0, int skip, int range) {
+  s.len = len;
   s.first = seq_first(p, s.len);
   s.lo = s.first / (16 * S);
   s.hi = (s.len + 16 * S - 1) / (16 * S);
@@ -138,17 +138,22 @@ __device__ __forceinline__ void seg_at(const PagedAttnParams& p, Seg& s, int i0,
   const int left = s.hi - s.lo + E - skip;
   s.i1 = left < range - i0 ? i0 + left : range;
 }
-// The unit after s; there is one while s.i1 < range.
+// The unit after s; there is one while s.i1 < range.  (Where there is none,
+// because the lengths change under the call, the rest of the range is void.)
 template <int S, int E>
 __device__ __forceinline__ void seg_next(const PagedAttnParams& p, Seg& s, int range) {
   const int i0 = s.i1;
+  int len = s.len;
   if (++s.h == p.hkv) {
     s.h = 0;
-    do {
-      ++s.b;
-    } while (s.b < p.batch.seqs - 1 && seq_len(p, s.b) == 0);
+    len = 0;
+    while (len == 0 && ++s.b < p.batch.seqs) len = seq_len(p, s.b);
+    if (len == 0) {
+      s = Seg{0, 0, 0, 0, INT_MAX / 2, INT_MAX / 2, 0, i0, range};
+      return;
+    }
   }
-  seg_at<S, E>(p, s, i0, 0, range);
+  seg_at<S, E>(p, s, len, i0, 0, range);
 }
 
 // D = A(16x16) B(16x8) + D.  Not volatile: the compiler may interleave chains.
@@ -291,7 +296,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);           // [warps][NST]
   float* ml = reinterpret_cast<float*>(smem + 256);             // [warps][m 8, l 8]
   int64_t* sums = reinterpret_cast<int64_t*>(smem + 768);       // [2][warps] of the search
-  int* found = reinterpret_cast<int*>(smem + 896);              // where the range starts: sequence, head, place
+  // This unit's part and the next one's.  One thread reads the lengths for all:
+  // warps that read them for themselves, while something changed them, could
+  // differ on how often they meet.
+  Seg* segs = reinterpret_cast<Seg*>(smem + 896);
   float2* qstat = reinterpret_cast<float2*>(smem + 512);        // [2][8 heads]: fac, qs (below)
   float4* mergebuf = reinterpret_cast<float4*>(smem + C::extra);  // [warps][warps - 1][QT][32]
   // 16 bits: q rows [2][8][D].  Codes: rows as they come [8][D], then their
@@ -320,18 +328,23 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   int range = 0;
   if (p.solo) {
     // one CTA for each unit: no search, and nothing to join
-    cs.b = blockIdx.x / p.hkv;
-    cs.h = blockIdx.x - cs.b * p.hkv;
-    if (seq_len(p, cs.b) == 0) {
+    if (threadIdx.x == 0) {
+      cs.b = blockIdx.x / p.hkv;
+      cs.h = blockIdx.x - cs.b * p.hkv;
+      const int len = seq_len(p, cs.b);
+      if (len != __ldg(p.batch.lens + cs.b)) atomicExch(p.pool.err, kErrBadState);
+      seg_at<S, E>(p, cs, len, 0, 0, INT_MAX);
+      segs[0] = cs;
+    }
+    __syncthreads();
+    cs = segs[0];
+    if (cs.len == 0) {
       const int64_t row = static_cast<int64_t>(blockIdx.x) * p.gqa;
       for (int x = threadIdx.x; x < p.gqa * D; x += kThreads) reinterpret_cast<T*>(p.out)[row * D + x] = Num<T>::from(0.0f);
       if (p.lse && threadIdx.x < p.gqa) p.lse[row + threadIdx.x] = -INFINITY;
+      return;
     }
-    if (threadIdx.x == 0 && __ldg(p.batch.lens + cs.b) != seq_len(p, cs.b)) atomicExch(p.pool.err, kErrBadState);
-    if (seq_len(p, cs.b) == 0) return;
-    seg_at<S, E>(p, cs, 0, 0, INT_MAX);
     range = cs.i1;
-    __syncthreads();  // the barriers and the cleared fragments are there
   } else {
     // ---- the CTA's range of places, and the unit it starts in: prefix sums of
     // the sequences' places, 128 sequences at a time
@@ -343,10 +356,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       if (lines <= 2048 && line < lines)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.batch.table + 32 * line));
     }
+    int len = 0;  // of the sequence looked at last
     auto chunks_of = [&](int b) {
       if (b >= B) return static_cast<int64_t>(0);
-      const int raw = __ldg(p.batch.lens + b), len = seq_len(p, b);
-      if (blockIdx.x == 0 && raw != len) atomicExch(p.pool.err, kErrBadState);
+      len = seq_len(p, b);
+      if (blockIdx.x == 0 && __ldg(p.batch.lens + b) != len) atomicExch(p.pool.err, kErrBadState);
       return static_cast<int64_t>(place_count<S, E>(p, len)) * p.hkv;
     };
     int64_t total = 0;
@@ -384,13 +398,20 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       const int64_t at = incl - held;
       if (r0 >= at && r0 < incl) {
         const int64_t n = held / p.hkv, off = r0 - at;
-        found[0] = b0 + threadIdx.x;
-        found[1] = static_cast<int>(off / n);
-        found[2] = static_cast<int>(off % n);
+        cs.b = b0 + threadIdx.x;
+        cs.h = static_cast<int>(off / n);
+        seg_at<S, E>(p, cs, len, 0, static_cast<int>(off % n), range);
+        segs[0] = cs;
+        if (cs.i1 < range) seg_next<S, E>(p, cs, range);
+        segs[1] = cs;
       }
       __syncthreads();
       if (r0 < before) break;
       b0 += kThreads;
+      if (b0 >= B) {  // the lengths change under the call
+        if (threadIdx.x == 0) atomicExch(p.pool.err, kErrBadState);
+        return;
+      }
       held = incl = chunks_of(b0 + threadIdx.x);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -406,10 +427,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         if (w < warp) incl += sums[w];
       }
     }
-    cs.b = found[0];
-    cs.h = found[1];
-    seg_at<S, E>(p, cs, 0, found[2], range);
+    cs = segs[0];
   }
+  Seg ns = segs[1];  // (of no meaning where cs is the range's last)
 
   // ---- q rows of a unit into shared memory: asked for ahead of the copies of
   // its chunks (behind them, the first came 3 us late), of the next unit while
@@ -567,10 +587,13 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   for (;;) {
     // ---- q of the unit, in the order of the key fragments
     __syncthreads();
-    Seg ns = cs;  // the next unit
     if (cs.i1 < range) {
-      seg_next<S, E>(p, ns, range);
       fetch_q(ns, which ^ 1);
+      if (threadIdx.x == 0) {  // the unit after the next
+        Seg after = ns;
+        if (ns.i1 < range) seg_next<S, E>(p, after, range);
+        segs[1] = after;
+      }
     }
     uint32_t qf[NR];
     float fac[2], qs[2];  // of heads 2t, 2t + 1: score = fac s acc + qs z (codes), fac acc (16 bits)
@@ -917,6 +940,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     }
     if (cs.i1 >= range) break;
     cs = ns;
+    ns = segs[1];  // (written before the barrier of the merge)
   }
   if (dead) {  // copies under way must not outlive the CTA's shared memory
     for (int i = 0; i < flying; ++i) {
@@ -947,6 +971,11 @@ __global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
   }
   const int first = raw.x, count = raw.y, second = raw.z;
   if (count == 0) return;
+  if (first < 0 || count < 0 || second < 0 || second > 1 || first >= p.ctas || count > p.ctas - first) {
+    // no CTA began the unit: the lengths changed under the call
+    if (threadIdx.x == 0) atomicExch(p.pool.err, kErrBadState);
+    return;
+  }
   const float* base = reinterpret_cast<const float*>(p.ws + p.ws_partials);
   auto part = [&](int i) {
     return base + (2 * (static_cast<int64_t>(first) + i) + (i == 0 ? second : 0)) * partial_floats(D);
@@ -1035,7 +1064,8 @@ cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = s;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.solo ? units : most < wave ? most : wave));
+  p.ctas = static_cast<int>(p.solo ? units : most < wave ? most : wave);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
   cfg.blockDim = dim3(C::threads);
   cfg.dynamicSmemBytes = C::smem;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kernel<T, KB, VB, D>, p);

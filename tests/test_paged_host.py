@@ -36,9 +36,9 @@ def test_bytes_by_hand(lib):
 def test_bytes_refuses_bad_configs(lib):
     bad = [dict(head_dim=96), dict(page_size=8), dict(page_size=48), dict(page_size=256), dict(num_pages=0),
            dict(num_q_heads=6, num_kv_heads=4), dict(num_q_heads=18, num_kv_heads=2), dict(num_q_heads=0),
-           dict(num_kv_heads=0), dict(layers=[(3, 4)]), dict(layers=[(4, 3)]), dict(layers=[(16, 8)]),
+           dict(num_kv_heads=0), dict(num_q_heads=2 ** 17, num_kv_heads=2 ** 16), dict(layers=[(3, 4)]), dict(layers=[(4, 3)]), dict(layers=[(16, 8)]),
            dict(layers=[(8, 16)]), dict(layers=[(0, 0)]), dict(dtype=2), dict(dtype=-1), dict(layers=[]),
-           dict(layers=[(16, 16)] * 60000, num_pages=2 ** 31 - 1, num_q_heads=2 ** 20, num_kv_heads=2 ** 20)]
+           dict(layers=[(16, 16)] * 60000, num_pages=2 ** 31 - 1, num_q_heads=2 ** 16, num_kv_heads=2 ** 16)]
     for b in bad:
         assert K.kvq_paged_bytes(_cfg(**b)) == 0, b
     assert lib.kvq_paged_bytes(None) == 0
