@@ -582,7 +582,7 @@ class KVQPagedCache:
         self._c_append, self._c_attn, self._c_read = lib.kvq_paged_append, lib.kvq_paged_decode_attn, lib.kvq_paged_read
         self._empty, self._f32, self._u8 = torch.empty, torch.float32, torch.uint8
         self._raw_stream, self._index = torch._C._cuda_getCurrentRawStream, self.device.index
-        self._current_device, self._device_guard = torch.cuda.current_device, torch.cuda.device
+        self._current_device, self._device_guard = torch._C._cuda_getDevice, torch.cuda.device
         self._stream_guard = torch.cuda.stream
 
     def _rows(self, t, name: str, n: int, heads: int) -> Rows:
@@ -607,16 +607,12 @@ class KVQPagedCache:
             raise ValueError(f"batch must be on {self.device}, got {batch.device}")
         return batch.args
 
-    def _call(self, where: str, fn, stream, *args) -> None:
-        """fn(*args, stream) with the cache's device current."""
-        s = self._raw_stream(self._index) if stream is None else stream.cuda_stream
-        if self._current_device() == self._index:
-            st = fn(*args, s)
-        else:
-            with self._device_guard(self.device):
-                st = fn(*args, s)
-        if st:
-            raise KVQError(st, where)
+    def _stream(self, stream) -> int:
+        return self._raw_stream(self._index) if stream is None else stream.cuda_stream
+
+    def _on_device(self, fn, *args) -> int:
+        with self._device_guard(self.device):
+            return fn(*args)
 
     def append(self, layer: int, batch: PagedBatch, K, V, q=None, rotation: Optional[Rotation] = None, q_out=None,
                stream=None):
@@ -643,7 +639,10 @@ class KVQPagedCache:
             qo = self._rows(q_out, "q_out", n, self.Hq)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        self._call("kvq_paged_append", self._c_append, stream, self.h, layer, b, k, v, qr, qo, r, n)
+        args = self.h, layer, b, k, v, qr, qo, r, n, self._stream(stream)
+        st = self._c_append(*args) if self._current_device() == self._index else self._on_device(self._c_append, *args)
+        if st:
+            raise KVQError(st, "kvq_paged_append")
         return q_out
 
     def decode_attn(self, layer: int, batch: PagedBatch, q, out=None, scale: float = 0.0, window: int = 0,
@@ -666,8 +665,11 @@ class KVQPagedCache:
         # every call has a workspace of its own, so that calls on several
         # streams, or of several captured graphs, never share one
         ws = self._new(stream, nws, self._u8)
-        self._call("kvq_paged_decode_attn", self._c_attn, stream, self.h, layer, b, qr, out.data_ptr(),
-                   lse.data_ptr() if return_lse else None, scale, window, ws.data_ptr(), nws)
+        args = (self.h, layer, b, qr, out.data_ptr(), lse.data_ptr() if return_lse else None, scale, window,
+                ws.data_ptr(), nws, self._stream(stream))
+        st = self._c_attn(*args) if self._current_device() == self._index else self._on_device(self._c_attn, *args)
+        if st:
+            raise KVQError(st, "kvq_paged_decode_attn")
         return (out, lse) if return_lse else out
 
     def read(self, layer: int, batch: PagedBatch, n: int, K=None, V=None, stream=None):
@@ -682,7 +684,10 @@ class KVQPagedCache:
         if V is None:
             V = self._new(stream, (n, self.Hkv, self.D), self.dtype)
         k, v = self._rows(K, "K", n, self.Hkv), self._rows(V, "V", n, self.Hkv)
-        self._call("kvq_paged_read", self._c_read, stream, self.h, layer, b, k, v, n)
+        args = self.h, layer, b, k, v, n, self._stream(stream)
+        st = self._c_read(*args) if self._current_device() == self._index else self._on_device(self._c_read, *args)
+        if st:
+            raise KVQError(st, "kvq_paged_read")
         return K, V
 
     def view(self, layer: int) -> dict:
