@@ -70,9 +70,10 @@ struct Shape {
   // Tiles of a chunk, and CTAs per SM.  Codes: a chunk costs about 50
   // instructions beside its tiles (wait, maximum, next copy), so larger chunks
   // on 12 warps an SM beat smaller ones on 16 (K4V2, 8 x 32K tokens: 4 tiles on
-  // 3 CTAs 41.5 us, 2 on 3 45.3, 2 on 4 47.3, 4 on 2 43.6).  16 bits: one tile,
-  // as many CTAs as leave a ring of three stages.
-  static constexpr int S = !quant || TB > 3200 ? 1 : (TB > 1664 ? 2 : 4);  // tiles of a chunk
+  // 3 CTAs 41.5 us, 2 on 3 45.3, 2 on 4 47.3, 4 on 2 43.6; K8V8, 32 sequences of
+  // up to 8K, window 4096: 2 tiles on 2 CTAs 29.7 us, 1 on 3 31.4).  16 bits: one
+  // tile, as many CTAs as leave a ring of three stages.
+  static constexpr int S = !quant ? 1 : (TB > 1664 ? 2 : 4);  // tiles of a chunk
   static constexpr int stage = S * TB;
   static constexpr int W = 4;  // warps
   static constexpr int threads = 32 * W;
@@ -81,7 +82,7 @@ struct Shape {
   // with 16 bits, 1.6 with K8V4, 2.9 with K4V2; 2 W was the best of 0, W, 2 W,
   // 3 W for all three: K8V4, 16 x 4K tokens, 21.7, 21.2, 20.8, 20.7 us.)
   static constexpr int E = 2 * W;
-  static constexpr int CPS = quant ? 3 : (TB > 4096 ? 2 : 4);
+  static constexpr int CPS = quant && TB <= 3200 ? 3 : (TB > 4096 ? 2 : 4);
   static constexpr int merge = (W - 1) * 32 * D;            // what each warp hands the others (D/4 fp32 a lane)
   static constexpr int queries = (quant ? 3 : 2) * 16 * D;  // rows of 8 heads (see fetch_q)
   static constexpr int extra = 1024;             // barriers, maxima and sums, q's factors, the search's sums
