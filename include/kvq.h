@@ -459,8 +459,9 @@ kvq_status kvq_paged_create(const kvq_paged_config* cfg, void* dev_buf, size_t b
  *   n_tokens: rows of the tensors; without cu_tokens, equal to num_seqs.
  * Rows need only their type's alignment; 16-byte aligned rows are faster.
  * Quantized rows are taken in fp16 (clamped to +-65504): zero = min,
- * scale = fp16((max - min) / (2^b - 1)), code = clamp(rint((x - zero) /
- * scale), 0, 2^b - 1), as kvq_append does per token; a row with a NaN gets
+ * scale = fp16((max - min) * r) with r = fp32(1 / (2^b - 1)), code =
+ * clamp(rint((x - zero) / scale), 0, 2^b - 1), as kvq_append does per token but
+ * for the scale's last bit (it divides by 2^b - 1); a row with a NaN gets
  * NaN scales.  Two rows of one call with the same slot (one page in the tables
  * of two sequences that both append to it) leave one of them or a mixture
  * there. */

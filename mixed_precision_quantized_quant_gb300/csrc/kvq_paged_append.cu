@@ -146,7 +146,10 @@ struct RowWork {
     const float mn = __half2float(mnh), mx = __half2float(__hmax_nan(__low2half(mx2), __high2half(mx2)));
     const int bits = KIND == kValues ? p.pool.vb : p.pool.kb;
     const float qmax = static_cast<float>((1 << bits) - 1);
-    const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), qmax));
+    // by the reciprocal, rounded once: the scale's last bit may differ from a
+    // division's, its error from the range over the codes hardly
+    const float steps = bits == 8 ? 1.0f / 255.0f : bits == 4 ? 1.0f / 15.0f : 1.0f / 3.0f;
+    const __half sh = __float2half_rn(__fmul_rn(__fsub_rn(mx, mn), steps));
     const float s = __half2float(sh);
     const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
     if (!live) return;

@@ -63,7 +63,8 @@ class Pages:
         bits = self.vb if is_value else self.kb
         h = x.float().clamp(-65504, 65504).half().numpy()[None]
         mn, mx = h.min(1), h.max(1)
-        s = O.asym_scale(mn, mx, bits)
+        # the range times the reciprocal of the code range, as documented (kvq_append divides)
+        s = ((mx.astype(np.float32) - mn.astype(np.float32)) * (np.float32(1) / np.float32(2 ** bits - 1))).astype(np.float16)
         codes = O.asym_codes(h, mn[:, None], s.astype(np.float32)[:, None], 2 ** bits - 1)[0]
         tile[at] = pack(codes, bits)
         off = 16 * (self.rk + self.rv) + key_row(i) * 8 + (4 if is_value else 0)
