@@ -38,18 +38,19 @@
 // 2^-24 * 2^field): exact, one AND for two codes; a key field's power of two is
 // taken out of q, a value field's out of the result.  The tensor cores align
 // sums by the exponent field, so that a sum of subnormals keeps fewer bits the
-// lower the field: scores are 4e-6 to 9e-6 off (rms), which the weights can
-// bear.  Value fields are moved to bit 4 or higher first (one more shift for
-// four codes): at bits 0 .. 3 they cost half the bits of an fp16 output.
+// lower the field; fields are therefore moved to bit 4 or higher first (one
+// more shift for four codes).  At bits 0 .. 3 the scores of 4-bit keys were
+// 8.5e-6 off (rms) instead of 1.4e-6, those of 2-bit keys over 1e-5 of a short
+// sequence's, and outputs lost half the bits of fp16; the shifts cost 2 us of 42.
 //
 // Measured (GB300, device time with the join, copy rate 6771 GB/s): 8 x 32K
-// tokens x 8 kv heads in fp16 119 us, 96% of the copy rate; K4V2 41 us, 56%;
-// 16 x 4K x 8 in bf16 38 us, 77%, K8V4 21 us, 55%; one sequence of 256 tokens
+// tokens x 8 kv heads in fp16 119 us, 96% of the copy rate; K4V2 44 us, 53%;
+// 16 x 4K x 8 in bf16 38 us, 76%, K8V4 22 us, 53%; one sequence of 256 tokens
 // 5 us.  About 9 us of each are the way to the first chunk (lengths, page
 // table, first copies: 3 dependent loads, 4.7 us), the uneven end of the CTAs
 // (2 to 4 us) and the join (3 us).  In between 16-bit rows stream at the copy
-// rate; narrow codes are bound by the ALU pipe and the issue slots (K4V2: 200
-// instructions a tile, 80 of them the masks, shifts and byte permutes that
+// rate; narrow codes are bound by the ALU pipe and the issue slots (K4V2: 210
+// instructions a tile, 100 of them the masks, shifts and byte permutes that
 // make registers of two codes).
 #pragma once
 
@@ -224,48 +225,19 @@ template <int KB>
 __host__ __device__ constexpr int key_local(int r, int hi) {
   return KB == 8 ? 2 * r + hi : KB == 4 ? 8 * (r / 4) + r % 4 + 4 * hi : 16 * (r / 8) + r % 8 + 8 * hi;
 }
-// log2 of the power of two that the field of key register r, and of value
-// register (channel) r, carries
+// log2 of the power of two that the field of key register (value channel) r carries
 template <int B>
-__host__ __device__ constexpr int key_field(int r) {
-  return B == 4 ? 4 * (r % 2) : B == 2 ? 2 * (r % 8 < 5 ? r % 8 : r % 8 - 5) : 0;
-}
-template <int B>
-__host__ __device__ constexpr int val_field(int r) {
+__host__ __device__ constexpr int code_field(int r) {
   constexpr int two[8] = {4, 6, 4, 6, 8, 4, 6, 8};
   return B == 8 ? 0 : B == 4 ? 4 : two[r % 8];
 }
 
 __host__ __device__ constexpr float mid_code(int bits) { return 0.5f * ((1 << bits) - 1); }
 
-// Words of key code rows -> registers of two fp16 subnormals each.
+// 32 bits of codes -> registers of two fp16 subnormals, one from each half.
 template <int B>
-__device__ __forceinline__ void key_regs(uint32_t w, uint32_t* r) {
-  if (B == 8) {
-    r[0] = prmt(w, 0, 0x4140);
-    r[1] = prmt(w, 0, 0x4342);
-  } else if (B == 4) {
-    const uint32_t u = w >> 8;
-    r[0] = w & 0x000f000fu;
-    r[1] = w & 0x00f000f0u;
-    r[2] = u & 0x000f000fu;
-    r[3] = u & 0x00f000f0u;
-  } else {
-    const uint32_t u = w >> 10;
-#pragma unroll
-    for (int i = 0; i < 5; ++i) r[i] = w & (0x00030003u << (2 * i));
-#pragma unroll
-    for (int i = 0; i < 3; ++i) r[5 + i] = u & (0x00030003u << (2 * i));
-  }
-}
-// x: two tokens' 16 bits of value codes (low half one token, high half the
-// other) -> registers of two fp16 subnormals each.
-template <int B>
-__device__ __forceinline__ void val_regs(uint32_t x, uint32_t* r) {
-  if (B == 8) {
-    r[0] = prmt(x, 0, 0x4240);
-    r[1] = prmt(x, 0, 0x4341);
-  } else if (B == 4) {  // fields at bits 4 .. 7
+__device__ __forceinline__ void split_codes(uint32_t x, uint32_t* r) {
+  if (B == 4) {  // fields at bits 4 .. 7
     const uint32_t u = x >> 8;
     r[0] = (x << 4) & 0x00f000f0u;
     r[1] = x & 0x00f000f0u;
@@ -281,6 +253,26 @@ __device__ __forceinline__ void val_regs(uint32_t x, uint32_t* r) {
     r[5] = u & 0x00300030u;
     r[6] = u & 0x00c000c0u;
     r[7] = u & 0x03000300u;
+  }
+}
+// A word of a key row; two tokens' 16 bits of value codes (low half one token,
+// high half the other).
+template <int B>
+__device__ __forceinline__ void key_regs(uint32_t w, uint32_t* r) {
+  if constexpr (B == 8) {
+    r[0] = prmt(w, 0, 0x4140);
+    r[1] = prmt(w, 0, 0x4342);
+  } else {
+    split_codes<B>(w, r);
+  }
+}
+template <int B>
+__device__ __forceinline__ void val_regs(uint32_t x, uint32_t* r) {
+  if constexpr (B == 8) {
+    r[0] = prmt(x, 0, 0x4240);
+    r[1] = prmt(x, 0, 0x4341);
+  } else {
+    split_codes<B>(x, r);
   }
 }
 
@@ -488,13 +480,13 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       __half* h = reinterpret_cast<__half*>(f + in_run / 16 * 256) + in_run / 8 % 2;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        h[i / 4 * 256 + i % 4 * 2] = __float2half_rn(x[i] * (up * (1.0f / (1 << key_field<KB>(i)))));
+        h[i / 4 * 256 + i % 4 * 2] = __float2half_rn(x[i] * (up * (1.0f / (1 << code_field<KB>(i)))));
     } else {
       uint32_t r[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = x[KB == 8 ? 2 * i : i], b = x[KB == 8 ? 2 * i + 1 : i + 4];
-        const float u = up * (1.0f / (1 << key_field<KB>(i)));
+        const float u = up * (1.0f / (1 << code_field<KB>(i)));
         r[i] = h2_as_u32(__floats2half2_rn(a * u, b * u));
       }
       *reinterpret_cast<uint4*>(f + in_run / 8 * 128) = make_uint4(r[0], r[1], r[2], r[3]);
@@ -863,7 +855,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         const int j = w * QT + q;
         float4 v = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
         if constexpr (C::quant) {  // the field's power of two, and what all channels share
-          const float u0 = 16777216.0f / (1 << val_field<VB>(2 * j)), u1 = 16777216.0f / (1 << val_field<VB>(2 * j + 1));
+          const float u0 = 16777216.0f / (1 << code_field<VB>(2 * j)), u1 = 16777216.0f / (1 << code_field<VB>(2 * j + 1));
           v = make_float4(fmaf(v.x, u0, zs[0]), fmaf(v.y, u0, zs[1]), fmaf(v.z, u1, zs[0]), fmaf(v.w, u1, zs[1]));
         }
         if (warp == w)
