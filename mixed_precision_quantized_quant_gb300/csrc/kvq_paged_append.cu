@@ -9,6 +9,10 @@
 // no lane needs another's, and one store of a row's lanes covers whole 32-byte
 // sectors.  Finding a token's place takes three dependent loads, which two
 // forms of the kernel hide in two ways (see them below).
+//
+// Measured (GB300): 8,000 rows of 32 query and 8 kv heads in bf16 35 us, 84% of
+// the copy rate; 9,500 rows of 64 and 8 heads into K4V2 72 us, 75%, bound by the
+// issue slots (half used) and the latency of 24 warps an SM; one row 1.9 us.
 #include "kvq_paged_rows.cuh"
 
 namespace kvq {
@@ -267,7 +271,11 @@ __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) paged_append_kernel
 
 // Few tokens, where latency counts: a CTA takes one, a warp one group of its
 // rows (more where there are over 32), each finding the token's place by
-// itself while its row is on its way; no shared memory and no barrier.
+// itself while its row is on its way; no shared memory and no barrier.  Against
+// the form above, us (bf16, 32 query and 8 kv heads, D = 128): 1 row 2.2 and 3.6,
+// 256 rows 4.5 and 5.0, 456 rows 4.6 and 5.1, 912 rows 8.2 and 6.2; codes (K4V2,
+// with the read back): 1 row 4.8 and 6.2, 256 rows 7.5 and 9.1, 456 rows 10.6
+// and 9.3.
 template <typename T, int D, bool QUANT>
 __global__ void __launch_bounds__(1024) paged_append_few_kernel(const __grid_constant__ PagedAppendParams p) {
   using W = RowWork<T, D, QUANT>;
@@ -311,7 +319,7 @@ template <typename T, int D>
 cudaError_t append_as(PagedAppendParams p, int sms, cudaStream_t s) {
   p.tokens = cta_tokens(p.n, sms, kAppendPerSm);
   const dim3 grid(static_cast<unsigned>((p.n - 1) / p.tokens + 1));
-  if (p.tokens == 1) {
+  if (p.n <= sms * (p.pool.kb == 16 ? 3 : 2)) {  // (p.tokens is 1)
     constexpr int RPW = 32 / (D / 16);
     const int groups = (p.hq + RPW - 1) / RPW + 2 * ((p.hkv + RPW - 1) / RPW);
     const int threads = groups < 32 ? 32 * groups : 1024;

@@ -6,6 +6,10 @@
 // that one store of a row's lanes covers whole 32-byte sectors.  A CTA takes up to
 // 32 tokens: its first warp finds their places, a lane each; then each
 // of its eight warps takes a run of the (token, group of rows) pairs.
+//
+// Measured (GB300): 52,000 rows of 8 kv heads from K4V2 to bf16 45.5 us, 83% of
+// the copy rate (a kernel for every pair of widths; one for all took 52), bound by
+// the ALU pipe, 61% busy with converting codes; 515 rows 3.2 us.
 #include "kvq_paged_rows.cuh"
 
 namespace kvq {
