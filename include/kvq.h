@@ -473,12 +473,15 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
  * positions max(0, len - window) .. len - 1 (window 0: all of them).
  *   q: [num_seqs][num_q_heads] rows (cu_tokens is not looked at).
  *   out: [num_seqs][num_q_heads][head_dim] contiguous, 16-byte aligned, the
- *     cache's type, overlapping no other argument; lse: fp32 [num_seqs][num_q_heads] or NULL: the natural
- *     logarithm of the sum of exp(scale * q.k).  A sequence with no token gets
- *     0, and -infinity.
+ *     cache's type, overlapping no other argument.
+ *   lse: fp32 [num_seqs][num_q_heads] or NULL: the natural logarithm of the sum
+ *     of exp(scale * q.k).  A sequence with no token gets 0, and -infinity.
  *   scale: multiplies the scores; 0 means 1 / sqrt(head_dim).
  *   workspace: device scratch of kvq_paged_workspace_bytes(h, num_seqs) bytes,
- *     256-byte aligned, whatever it holds; not shared with a call in flight. */
+ *     256-byte aligned, whatever it holds; not shared with a call in flight.
+ * KVQ_ERR_ARG for a negative window or a scale that is not finite;
+ * KVQ_ERR_CAPACITY for a small workspace; KVQ_ERR_UNSUPPORTED where the tables
+ * could hold more than 2^30 tiles of work for every SM. */
 kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* q, void* out,
                                  float* lse, float scale, int window, void* workspace, size_t workspace_bytes,
                                  void* stream);
