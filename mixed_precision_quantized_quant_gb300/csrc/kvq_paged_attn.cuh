@@ -62,7 +62,14 @@
 namespace kvq {
 namespace paged {
 
-constexpr float kLazy = 8.0f;  // the maximum follows the scores only past 2^8: rescaling is rare, and P stays below 256
+// A running maximum m is kept kRoom below the greatest score that it was taken
+// from, and follows only scores kLazy above itself.  So rescaling is rare (2^8
+// past the last one), weights 2^(t - m) stay below 2^15, and in fp16, whose
+// steps end at 2^-24, the greatest has kRoom more bits below it than it would at
+// 1: there a weight under 2^-25 of the greatest would be 0 in the product with the
+// values, yet counted in the sum, so that up to 2^-25 of the output for every such token
+// were lost.
+constexpr float kRoom = 7.0f, kLazy = kRoom + 8.0f;
 
 template <int KB, int VB, int D>
 struct Shape {
@@ -738,7 +745,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         for (int hd = 0; hd < 2; ++hd) {
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mx[hd] = fmaxf(mx[hd], __shfl_xor_sync(0xffffffffu, mx[hd], x));
-          const float mn = fmaxf(m[hd], mx[hd]);
+          const float mn = fmaxf(m[hd], mx[hd] - kRoom);
           const float f = m[hd] == mn ? 1.0f : ex2(m[hd] - mn);
           m[hd] = mn;
           l[hd] *= f;
