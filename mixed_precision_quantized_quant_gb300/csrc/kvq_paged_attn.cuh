@@ -3,15 +3,11 @@
 //
 // Mathematics.  For the up to 8 query heads of a kv head, with t = scale
 // log2(e) q.k, running maximum m and l = sum 2^(t - m), o = sum 2^(t - m) v.
-// A key k = s c + z (c its codes) gives q.k = s (q.c) + z sum(q).  A value row
-// is s (c - h) + z' with h the middle code, (2^b - 1) / 2, and z' = z + s h, so
-// p v = (p s)(c - h) + p z', whose second part is the same for every channel:
-// the codes go into the tensor cores as they are, the scales and zeros are one
-// multiply-add per (token, head), and h sum(p s), summed over the very weights
-// that were rounded by one more MMA on a row of ones, is taken off at the end.
-// Taking values from the middle code keeps the rounding of p s to what it would
-// be on the values themselves: with z below and s c above, both large, it was
-// twice that.
+// A key k = s c + z (c its codes) gives q.k = s (q.c) + z sum(q), a value row
+// p v = (p s) c + p z, whose second part is the same for every channel: the codes
+// go into the tensor cores as they are, the scales and zeros are one multiply-add
+// per (token, head).  Weights go in as two 16-bit numbers, so that what is left
+// of them, 22 bits (16 in bf16), is no less than the sums keep.
 //
 // Bound.  Every cached byte is read once; 2 * 8 heads * D products per token
 // and kv head are far below the tensor rate, so the floor is the copy rate,
@@ -239,8 +235,6 @@ __host__ __device__ constexpr int code_field(int r) {
   return B == 8 ? 0 : B == 4 ? 4 : two[r % 8];
 }
 
-__host__ __device__ constexpr float mid_code(int bits) { return 0.5f * ((1 << bits) - 1); }
-
 // 32 bits of codes -> registers of two fp16 subnormals, one from each half.
 template <int B>
 __device__ __forceinline__ void split_codes(uint32_t x, uint32_t* r) {
@@ -292,6 +286,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
   constexpr int NR = D / 8;   // key fragment registers of a thread, per row
   constexpr int MT = D / 16;  // m-tiles of 16 channels
   constexpr int QT = MT / C::W;  // of which a warp finishes
+  using W = typename std::conditional<C::quant, __half, T>::type;  // of weights in the second product
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);           // [warps][NST]
   float* ml = reinterpret_cast<float*>(smem + 256);             // [warps][m 8, l 8]
@@ -617,7 +612,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     }
     which ^= 1;
     float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, zs[2] = {0.0f, 0.0f};
-    float ones[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // codes: sum of the rounded weights, in every row
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -710,7 +704,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
             const uint2 raw = *reinterpret_cast<const uint2*>(buf + s * C::TB + soff + 64 * i);
             const float ks = __low2float(u32_as_h2(raw.x)), kz = __high2float(u32_as_h2(raw.x));
             vs[s][i] = __low2float(u32_as_h2(raw.y));
-            vz[s][i] = fmaf(vs[s][i], mid_code(VB), __high2float(u32_as_h2(raw.y)));
+            vz[s][i] = __high2float(u32_as_h2(raw.y));
 #pragma unroll
             for (int hd = 0; hd < 2; ++hd)
               sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[s][2 * i + hd], kz * qs[hd]);
@@ -750,7 +744,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
           m[hd] = mn;
           l[hd] *= f;
           zs[hd] *= f;
-          ones[hd] *= f;
 #pragma unroll
           for (int j = 0; j < MT; ++j) {
             o[j][hd] *= f;
@@ -760,7 +753,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       }
 
       // ---- probabilities, transposed into the second product's fragments
-      uint32_t pb[S][2], rest[S][2];  // (rest: 16 bits only)
+      // weights as two numbers of 16 bits, 22 (bf16: 16) bits of them together
+      uint32_t pb[S][2], rest[S][2];
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -768,19 +762,17 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
           const float p0 = ex2(sc[s][2 * i] - m[0]), p1 = ex2(sc[s][2 * i + 1] - m[1]);
           l[0] += p0;
           l[1] += p1;
+          float w0 = p0, w1 = p1;
           if constexpr (C::quant) {
             zs[0] = fmaf(p0, vz[s][i], zs[0]);
             zs[1] = fmaf(p1, vz[s][i], zs[1]);
-            // one rounding to fp16: at most 2^-11 of the weight
-            pb[s][i] = transpose8(h2_as_u32(__floats2half2_rn(p0 * vs[s][i], p1 * vs[s][i])));
-          } else {
-            // the weight as two numbers of the cache's type, 16 (bf16) or 22 bits
-            // of it: the second product costs 8 MMAs a tile that memory hides
-            const uint32_t hi = pack2<T>(p0, p1);
-            const T* h = reinterpret_cast<const T*>(&hi);
-            pb[s][i] = transpose8(hi);
-            rest[s][i] = transpose8(pack2<T>(p0 - Num<T>::to(h[0]), p1 - Num<T>::to(h[1])));
+            w0 *= vs[s][i];
+            w1 *= vs[s][i];
           }
+          const uint32_t hi = pack2<W>(w0, w1);
+          const W* h = reinterpret_cast<const W*>(&hi);
+          pb[s][i] = transpose8(hi);
+          rest[s][i] = transpose8(pack2<W>(w0 - Num<W>::to(h[0]), w1 - Num<W>::to(h[1])));
         }
 
       // ---- the second product
@@ -820,10 +812,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
               val_regs<VB>(x, v[h]);
             }
           }
-          mma_t<__half>(ones, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[s][0], pb[s][1]);
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
+          for (int j = 0; j < MT; ++j) {
             mma_t<__half>(o[j], v[0][2 * j], v[0][2 * j + 1], v[1][2 * j], v[1][2 * j + 1], pb[s][0], pb[s][1]);
+            mma_t<__half>(o[j], v[0][2 * j], v[0][2 * j + 1], v[1][2 * j], v[1][2 * j + 1], rest[s][0], rest[s][1]);
+          }
         }
       }
       __syncwarp();
@@ -848,7 +841,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         l[hd] += __shfl_xor_sync(0xffffffffu, l[hd], x);
         zs[hd] += __shfl_xor_sync(0xffffffffu, zs[hd], x);
       }
-      if constexpr (C::quant) zs[hd] = fmaf(ones[hd], -mid_code(VB), zs[hd]);  // values are taken from the middle code
       if (g == 0) {
         ml[warp * 16 + 2 * t + hd] = m[hd];
         ml[warp * 16 + 8 + 2 * t + hd] = l[hd];

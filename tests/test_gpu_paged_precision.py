@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import paged_testutil as T
-from test_gpu_paged import Case
+from test_gpu_paged import PAIRS, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -76,7 +76,7 @@ def _check(c, q, scale=0.0):
 
 
 @pytest.mark.parametrize("width", [None, 100])
-@pytest.mark.parametrize("kb,vb", [(16, 16)])
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 8), (8, 4)])
 def test_weights_far_below_the_largest_count(kb, vb, width):
     # one token has nearly all the weight and value 0 in every channel but one; 400 others have 2^-26 of
     # it each and are the whole of the other channels' output
@@ -95,3 +95,14 @@ def test_weights_far_below_the_largest_count(kb, vb, width):
     q = torch.zeros(1, 2, 64, dtype=torch.float16, device="cuda")
     q[:, :, 0] = 1.0
     _check(c, q, scale=1.0)
+
+
+@pytest.mark.parametrize("width", [None, 100])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kb,vb", PAIRS)
+def test_weights_keep_more_than_16_bits(kb, vb, d, dtype, width):
+    # few tokens, so that sums cancel in many channels, and small queries, so that scores are near exact: one
+    # rounding of a weight to 16 bits is far outside the tolerance for 16-bit, 8-bit and 4-bit values
+    c = Case([2, 3, 3, 4, 5, 7, 16, 17, 40], kb=kb, vb=vb, d=d, dtype=dtype, width=width)
+    _check(c, c.rows(len(c.lens), c.hq) / 64)
