@@ -145,14 +145,18 @@ __device__ __forceinline__ void seg_at(const PagedAttnParams& p, Seg& s, int len
 }
 // The unit after s; there is one while s.i1 < range.  (Where there is none,
 // because the lengths change under the call, the rest of the range is void.)
-template <int S, int E>
+// WARP: a whole warp calls it, and takes the lengths that its first lane read.
+template <int S, int E, bool WARP>
 __device__ __forceinline__ void seg_next(const PagedAttnParams& p, Seg& s, int range) {
   const int i0 = s.i1;
   int len = s.len;
   if (++s.h == p.hkv) {
     s.h = 0;
     len = 0;
-    while (len == 0 && ++s.b < p.batch.seqs) len = seq_len(p, s.b);
+    while (len == 0 && ++s.b < p.batch.seqs) {
+      len = seq_len(p, s.b);
+      if (WARP) len = __shfl_sync(0xffffffffu, len, 0);
+    }
     if (len == 0) {
       s = Seg{0, 0, 0, 0, INT_MAX / 2, INT_MAX / 2, 0, i0, range};
       return;
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         cs.h = static_cast<int>(off / n);
         seg_at<S, E>(p, cs, len, 0, static_cast<int>(off % n), range);
         segs[0] = cs;
-        if (cs.i1 < range) seg_next<S, E>(p, cs, range);
+        if (cs.i1 < range) seg_next<S, E, false>(p, cs, range);
         segs[1] = cs;
       }
       __syncthreads();
@@ -500,8 +504,15 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 
   // ---- the producer's side of the ring: the addresses of the warp's next
   // copies are worked out one a lane, 32 / ppc chunks at a time (one alone
-  // costs as many instructions as all of them); chunk `ip` is the next to copy
+  // costs as many instructions as all of them); chunk `ip` is the next to copy.
+  // The warp reads the lengths for itself here, ahead of thread 0 (segs).  Should
+  // something change them in between, the two sides differ on the places, so
+  // that a wait is for a copy that was started, whichever place it was for,
+  // and all of them are waited for at the end.
   Seg ps = cs;
+  // Copies started and not waited for yet; -1 less that many once a wait gave
+  // up or had none to wait for: nothing more is copied or computed then.
+  int flight = 0;
   const int tiles_page = 1 << (p.pool.page_shift - 4);
   const int ppc = S > tiles_page ? S / tiles_page : 1;  // pages of a chunk
   const int nb = 32 / ppc, mine = lane / ppc, piece = lane % ppc;
@@ -542,7 +553,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         }
       }
       if (last < ps.i1) break;
-      seg_next<S, E>(p, ps, range);
+      seg_next<S, E, true>(p, ps, range);
     }
     voids = __ballot_sync(0xffffffffu, is_void);
   };
@@ -556,6 +567,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     if (turn && piece == 0) mbar_arrive_expect_tx(bar + st, chunk_bytes);
     if (ppc > 1) __syncwarp();
     if (turn && bytes) bulk_g2s_at(dst + st * C::stage, src, bytes, bar + st);
+    ++flight;
     ++nxt;
     ip += kWarps;
   };
@@ -576,8 +588,6 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
 
   int ic = warp, st = 0, which = 0;
   uint32_t phase = 0;
-  bool dead = false;  // a wait gave up: nothing more is copied or computed
-  int flying = 0;     // copies that were then under way
 
   for (;;) {
     // ---- q of the unit, in the order of the key fragments
@@ -586,7 +596,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       fetch_q(ns, which ^ 1);
       if (threadIdx.x == 0) {  // the unit after the next
         Seg after = ns;
-        if (ns.i1 < range) seg_next<S, E>(p, after, range);
+        if (ns.i1 < range) seg_next<S, E, false>(p, after, range);
         segs[1] = after;
       }
     }
@@ -618,17 +628,17 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
 
     for (; ic < cs.i1; ic += kWarps) {
-      if (dead || cs.cbase + ic < cs.lo) continue;
-      dead = __any_sync(0xffffffffu, !mbar_wait(bar + st, phase, p.pool.err));
-      if (dead) {
-        flying = 0;  // of the places between, those that are chunks
-        Seg x = cs;
-        for (int i = ic; i < ip; i += kWarps) {
-          while (i >= x.i1) seg_next<S, E>(p, x, range);
-          flying += x.cbase + i >= x.lo;
-        }
+      if (flight < 0 || cs.cbase + ic < cs.lo) continue;
+      if (flight == 0) {  // the lengths change under the call
+        if (lane == 0) atomicExch(p.pool.err, kErrBadState);
+        flight = -1;
         continue;
       }
+      if (__any_sync(0xffffffffu, !mbar_wait(bar + st, phase, p.pool.err))) {
+        flight = -1 - flight;
+        continue;
+      }
+      --flight;
       uint8_t* buf = ring + st * C::stage;
       const int base = (cs.cbase + ic) * (16 * S);
       const bool edge = base < cs.first || base + 16 * S > cs.len;
@@ -934,13 +944,12 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     cs = ns;
     ns = segs[1];  // (written before the barrier of the merge)
   }
-  if (dead) {  // copies under way must not outlive the CTA's shared memory
-    for (int i = 0; i < flying; ++i) {
-      mbar_wait(bar + st, phase, p.pool.err);
-      if (++st == C::NST) {
-        st = 0;
-        phase ^= 1;
-      }
+  if (flight < 0) flight = -1 - flight;
+  for (; flight > 0; --flight) {  // copies under way must not outlive the CTA's shared memory
+    mbar_wait(bar + st, phase, p.pool.err);
+    if (++st == C::NST) {
+      st = 0;
+      phase ^= 1;
     }
   }
 }
