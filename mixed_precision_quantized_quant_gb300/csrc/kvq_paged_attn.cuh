@@ -452,10 +452,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     }
   };
   // Codes: the thread's 8 channels, which it fetched itself, into the order of
-  // the key fragments.  A power of two takes the row's largest |q| to
-  // [2^13, 2^14): the fields' powers come off without reaching fp16's
-  // subnormals (2^-8 at most), and a bf16 q fits fp16 exactly down to 2^-30 of
-  // the row's largest.
+  // the key fragments.  A power of two takes the row's largest |q|, with the
+  // fields' least power off it, to [2^15, 2^16), where 11 bits still fit fp16.
+  // What fp16's steps of 2^-24 cut off is then at most 2^-40 of the row's largest for 8- and
+  // 4-bit keys and 2^-36 for 2-bit ones, whose fields differ by up to 2^4: a bf16
+  // q is exact down to 2^-32 (2^-28) of it.
   auto make_frags = [&](int which) {
     float x[8], mx = 0.0f, sum = 0.0f;
     uint4 raw = make_uint4(0, 0, 0, 0);
@@ -474,9 +475,10 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     }
     if (qhead >= p.gqa) return;
     int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;  // mx in [2^e, 2^(e+1))
-    e = mx < 1e-30f ? 13 : (e > 100 ? 100 : e);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+    constexpr int top = 15 + code_field<KB>(0);  // (register 0 has the lowest field)
+    e = mx < 1e-30f ? top : (e > 100 ? 100 : e);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + top - e) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - top + e) << 23);
     // channel 8 qchunk + i: thread column, register and half (see key_local)
     constexpr bool two_runs = KB == 8 && D == 128;
     const int col = two_runs ? qchunk / 2 % 4 : qchunk / (RC / 4);

@@ -106,3 +106,50 @@ def test_weights_keep_more_than_16_bits(kb, vb, d, dtype, width):
     # rounding of a weight to 16 bits is far outside the tolerance for 16-bit, 8-bit and 4-bit values
     c = Case([2, 3, 3, 4, 5, 7, 16, 17, 40], kb=kb, vb=vb, d=d, dtype=dtype, width=width)
     _check(c, c.rows(len(c.lens), c.hq) / 64)
+
+
+def _wide_queries(kb, below, d, width, small):
+    """Keys that are 0 where the row's largest query, 1, is; the others, 2^-below times `small`, make the scores."""
+    c = Case([60], kb=kb, vb=8, d=d, hq=4, hkv=1, dtype="bf16", fill=False, width=width)
+    top = 2 ** kb - 1
+    for p in range(60):
+        at = (c.table[0, p // 16], p % 16, 0)
+        k = torch.randint(0, top + 1, (d,), generator=c.g).float()
+        k[0], k[1] = 0, top
+        c.model.put(*at, False, k)
+        c.model.put(*at, True, torch.randn(d, generator=c.g))
+    c.upload()
+    q = small(c.g, (1, 4, d)) * 2.0 ** -below
+    q[:, :, 0] = 1.0
+    q = q.bfloat16()
+    scale = 2.0 ** below / (top * 8)
+    out, lse = c.cache.decode_attn(0, c.batch, q.cuda(), scale=scale, return_lse=True)
+    eo, el, tol, ltol = T.attend(c.model, c.table, c.lens, q, scale, 0, c.dtype)
+    k, _, _ = c.model.rows(c.table[0], 0, 60, 0, False)
+    v, _, _ = c.model.rows(c.table[0], 0, 60, 0, True)
+    return (np.abs(out.double().cpu().numpy() - eo), tol, np.abs(lse.double().cpu().numpy() - el), ltol,
+            scale * np.abs(k).sum(1).max(), np.abs(v).max())
+
+
+@pytest.mark.parametrize("width", [None, 100])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kb,below", [(8, 31), (4, 31), (2, 27)])
+def test_queries_keep_their_bits_far_below_the_largest(kb, below, d, width):
+    # 8 significant bits whose first is `below` under the row's largest fit fp16 exactly: no term for their rounding
+    def small(g, shape):
+        return (1 + torch.randint(0, 128, shape, generator=g) / 128) * (1 - 2 * torch.randint(0, 2, shape, generator=g))
+
+    o, tol, l, ltol, _, _ = _wide_queries(kb, below, d, width, small)
+    assert (l <= ltol).all() and (o <= tol).all() and (ltol < 2e-3).all()
+
+
+@pytest.mark.parametrize("width", [None, 100])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kb,below", [(8, 29), (4, 29), (2, 25)])
+def test_queries_below_fp16_steps(kb, below, d, width):
+    # smaller ones lose what lies below fp16's half step of 2^-25: 2^-40 (2-bit keys: 2^-36) of the row's
+    # largest, 1, a channel, so that a score is off by r = that times scale * sum_c |k_c| at the most, every weight by
+    # exp(2 r), the log-sum-exp by r and an output by under 3 r of the largest value
+    o, tol, l, ltol, keys, value = _wide_queries(kb, below, d, width, lambda g, s: torch.randn(s, generator=g).clamp(-3, 3))
+    r = 2.0 ** (-36 if kb == 2 else -40) * keys
+    assert (l <= ltol + r).all() and (o <= tol + 3 * r * value).all() and r < 1e-2
