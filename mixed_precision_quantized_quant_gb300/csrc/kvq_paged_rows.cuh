@@ -53,11 +53,12 @@ __device__ __forceinline__ RowPlace find_places(const PagedBatch& b, const Paged
       base += 32;
     }
     if (!live || seq >= b.seqs || row < b.cu[0]) return r;
-    if (row < b.cu[seq]) {  // not ascending
+    const int end = b.cu[seq + 1];
+    if (row < b.cu[seq] || row >= end) {  // not ascending: the count of ends is not the row's sequence
       atomicExch(pool.err, kErrBadState);
       return r;
     }
-    back = static_cast<int64_t>(b.cu[seq + 1]) - row;
+    back = static_cast<int64_t>(end) - row;
   } else if (!live || seq >= b.seqs) {
     return r;
   }

@@ -1,0 +1,48 @@
+"""Calls at the edges of what the paged cache documents."""
+
+import numpy as np
+import pytest
+import torch
+
+from mixed_precision_quantized_quant_gb300 import kvq as K
+from test_gpu_paged import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+# ---------------------------------------------------------------- rows of sequences
+
+# a row a CTA, 2 rows a CTA, 31 rows a CTA
+@pytest.mark.parametrize("n", [12, 612, 14_000])
+def test_ends_that_do_not_ascend(n):
+    # a row is written only where a sequence's two ends hold it, and only to its place there
+    rng = np.random.default_rng(n)
+    cases = [[0, 5, 1, 2, 9], [0, 9, 9, 9, 9, 1, 1, 2], [3, 4, 4, 1, 2, 7]]
+    cases += [rng.integers(0, 13, rng.integers(3, 12)).tolist() for _ in range(20)]
+    for ends in cases:
+        S = len(ends) - 1
+        c = Case([10] * S, page=16, fill=False)
+        batch = K.PagedBatch(_i32(c.table), _i32(c.lens), _i32(ends))
+        may = np.zeros(c.model.data.shape, bool)
+        for s in range(S):
+            for row in range(ends[s], min(ends[s + 1], n)):
+                p = 10 - (ends[s + 1] - row)
+                for is_v in (False, True):
+                    start, m, xor = c.model._row(is_v, max(p, 0))
+                    if p >= 0:
+                        may[c.table[s, 0], :, 0, start + (np.arange(m) ^ xor)] = True
+        c.cache.append(0, batch, c.rows(n, 2), c.rows(n, 2))
+        assert (c.download()[~may] == 0xFF).all(), ends
+        k, v = (torch.full((n, 2, 64), 7.0, dtype=c.dtype, device="cuda") for _ in range(2))
+        code = c.cache.device_error()
+        c.cache.read(0, batch, n, K=k, V=v)
+        held = [any(ends[s] <= row < ends[s + 1] and ends[s + 1] - row <= 10 for s in range(S)) for row in range(n)]
+        for x in (k, v):
+            assert bool((x[~torch.tensor(held).cuda()] == 7).all()), ends
+        assert c.cache.device_error() == code and code in (0, 2)
+        if ends == [0, 9, 9, 9, 9, 1, 1, 2] and n == 12 or ends == [0, 5, 1, 2, 9] and n == 14_000:
+            assert code == 2, ends  # row 3 counts as a sequence's whose ends are 1 and 2
