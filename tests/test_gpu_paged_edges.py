@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from mixed_precision_quantized_quant_gb300 import kvq as K
-from test_gpu_paged import Case
+from test_gpu_paged import Case, _check_append
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,40 @@ def test_ends_that_do_not_ascend(n):
         assert c.cache.device_error() == code and code in (0, 2)
         if ends == [0, 9, 9, 9, 9, 1, 1, 2] and n == 12 or ends == [0, 5, 1, 2, 9] and n == 14_000:
             assert code == 2, ends  # row 3 counts as a sequence's whose ends are 1 and 2
+
+
+@pytest.mark.parametrize("kb,vb", [(16, 16), (4, 2)])
+@pytest.mark.parametrize("seqs", [33, 70, 200])
+def test_append_and_read_of_many_sequences(seqs, kb, vb):
+    # rows whose sequences' ends are found 32 at a time, runs of sequences without rows among them
+    g = torch.Generator().manual_seed(seqs)
+    news = torch.randint(0, 6, (seqs,), generator=g)
+    news[3:3 + seqs // 2:2] = 0
+    news[seqs // 3:seqs // 3 + 40] = 0
+    news[-1] = 3
+    lens = (news + torch.randint(0, 20, (seqs,), generator=g)).tolist()
+    c = Case(lens, news.tolist(), kb=kb, vb=vb, d=64, hq=2, hkv=1, page=16, fill=False)
+    _check_append(c, dim=64, extra=2)
+    n = int(news.sum())
+    k, v = c.cache.read(0, c.batch, n)
+    for row, b, p in c.places():
+        for x, is_v in ((k, False), (v, True)):
+            e, _, _ = c.model.get(c.table[b, p // 16], p % 16, 0, is_v)
+            assert torch.equal(x[row, 0].cpu(), torch.from_numpy(e).float().to(c.dtype))
+
+
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 4)])
+def test_append_and_read_on_a_stream_of_their_own(kb, vb):
+    c = Case([40, 3], [30, 3], kb=kb, vb=vb, d=64, fill=False)
+    s = torch.cuda.Stream()
+    k, v, q = c.rows(33, 2), c.rows(33, 2), c.rows(33, 8)
+    rot = K.Rotation(K.rotation_table(60, 64))
+    s.wait_stream(torch.cuda.current_stream())
+    got = c.cache.append(0, c.batch, k, v, q=q, rotation=rot, stream=s)
+    rk, rv = c.cache.read(0, c.batch, 33, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    got, rk, rv = got.clone(), rk.clone(), rv.clone()
+    again = c.cache.append(0, c.batch, k, v, q=q, rotation=rot)
+    ak, av = c.cache.read(0, c.batch, 33)
+    assert torch.equal(got, again) and torch.equal(rk, ak) and torch.equal(rv, av)
+    assert float(rk.abs().max()) > 0 and c.cache.device_error(s) == 0
