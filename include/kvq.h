@@ -400,7 +400,7 @@ typedef struct {
  *     elements apart; entry k of a row holds positions k * page_size .. .
  *     Entries past a sequence's last page, and in attention those of pages
  *     wholly before its window, are not read.  max_pages * page_size is at
- *     most 2^30.
+ *     most 2^30, and num_seqs * num_kv_heads below 2^31 (KVQ_ERR_ARG).
  *   seq_lens: [num_seqs] tokens of each sequence, the new ones included.
  *   cu_tokens: [num_seqs + 1] ascending, or NULL.  Rows cu_tokens[s] ..
  *     cu_tokens[s + 1] - 1 of a call's row tensors are the newest tokens of

@@ -91,8 +91,8 @@ kvq_status open_call(const kvq_paged* h, int layer, const kvq_paged_batch* b, kv
   if (!h || layer < 0 || layer >= h->cfg.num_layers || !b) return KVQ_ERR_ARG;
   if (b->num_seqs < 1 || b->max_pages < 1 || b->table_stride < b->max_pages || !b->page_table || !b->seq_lens)
     return KVQ_ERR_ARG;
-  // positions, with room to round them up to a chunk, and units are held in 32 bits
-  if (static_cast<int64_t>(b->max_pages) * h->cfg.page_size > INT_MAX / 2 ||
+  // positions, rounded up to a chunk, and units are held in 32 bits
+  if (static_cast<int64_t>(b->max_pages) * h->cfg.page_size > 1 << 30 ||
       static_cast<int64_t>(b->num_seqs) * h->cfg.num_kv_heads > INT_MAX)
     return KVQ_ERR_ARG;
   int cur = -1;

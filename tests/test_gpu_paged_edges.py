@@ -83,3 +83,30 @@ def test_append_and_read_on_a_stream_of_their_own(kb, vb):
     ak, av = c.cache.read(0, c.batch, 33)
     assert torch.equal(got, again) and torch.equal(rk, ak) and torch.equal(rv, av)
     assert float(rk.abs().max()) > 0 and c.cache.device_error(s) == 0
+
+
+# ---------------------------------------------------------------- tables
+
+def test_the_widest_table():
+    # max_pages * page_size = 2^30 positions, the documented limit; one page more is refused
+    P, pages = 128, 1 << 23
+    c = Case([300], [300], d=64, hq=2, hkv=1, page=P, fill=False)
+    table = torch.zeros(1, pages + 1, dtype=torch.int32, device="cuda")
+    table[0, :3] = torch.from_numpy(c.table[0]).cuda()
+    lens, cu = _i32([300]), _i32([0, 300])
+    k, v, q = c.rows(300, 1), c.rows(300, 1), c.rows(1, 2)
+    narrow = K.PagedBatch(table[:, :3].contiguous(), lens, cu)
+    c.cache.append(0, narrow, k, v)
+    expect = c.cache.decode_attn(0, narrow, q), *c.cache.read(0, narrow, 300)
+    b = K.PagedBatch(table[:, :pages].contiguous(), lens, cu)
+    c.cache.append(0, b, k, v)
+    got = c.cache.decode_attn(0, b, q), *c.cache.read(0, b, 300)
+    assert torch.equal(got[1], expect[1]) and torch.equal(got[2], expect[2])
+    assert float((got[0].float() - expect[0].float()).abs().max()) <= 2 ** -11 * 2 * float(expect[0].abs().max())
+    wide = K.PagedBatch(table, lens, cu)
+    for fn in (lambda: c.cache.append(0, wide, k, v), lambda: c.cache.decode_attn(0, wide, q),
+               lambda: c.cache.read(0, wide, 300)):
+        with pytest.raises(K.KVQError) as e:
+            fn()
+        assert e.value.status == 1
+    assert c.cache.device_error() == 0
