@@ -475,7 +475,9 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
  *   out: [num_seqs][num_q_heads][head_dim] contiguous, 16-byte aligned, the
  *     cache's type, overlapping no other argument.
  *   lse: fp32 [num_seqs][num_q_heads] or NULL: the natural logarithm of the sum
- *     of exp(scale * q.k).  A sequence with no token gets 0, and -infinity.
+ *     of exp(scale * q.k).  A sequence with no token, or with no score above
+ *     -infinity, gets 0, and -infinity.  (A NaN in an attended row, a score of
+ *     +infinity or an infinite value leaves NaN or infinity where it counts.)
  *   scale: multiplies the scores; 0 means 1 / sqrt(head_dim).
  *   workspace: device scratch of kvq_paged_workspace_bytes(h, num_seqs) bytes,
  *     256-byte aligned, whatever it holds; not shared with a call in flight.

@@ -50,6 +50,7 @@
 // make registers of two codes).
 #pragma once
 
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -623,7 +624,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       }
     }
     which ^= 1;
-    float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, zs[2] = {0.0f, 0.0f};
+    // (the maximum begins at a number: from -infinity, scores that are all
+    // -infinity would get weights of NaN instead of 0)
+    float o[MT][4], m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.0f, 0.0f}, zs[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -914,7 +917,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
           const int head = 2 * t + hd;
           if (head < p.gqa) {
             const int64_t row = unit * p.gqa + head;
-            const float inv = 1.0f / sum[hd];
+            const float inv = sum[hd] == 0.0f ? 0.0f : 1.0f / sum[hd];
             T* out = reinterpret_cast<T*>(p.out) + row * D;
 #pragma unroll
             for (int q = 0; q < QT; ++q)
@@ -1028,7 +1031,7 @@ __global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
     const int head = 2 * t + hd;
     if (head >= p.gqa) continue;
     const int64_t row = unit * p.gqa + head;
-    const float inv = 1.0f / sum[hd];
+    const float inv = sum[hd] == 0.0f ? 0.0f : 1.0f / sum[hd];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int c = QUANT ? D / 8 * g + 2 * j + half : 16 * j + 8 * half + g;

@@ -1,5 +1,7 @@
 """Calls at the edges of what the paged cache documents."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -109,4 +111,37 @@ def test_the_widest_table():
         with pytest.raises(K.KVQError) as e:
             fn()
         assert e.value.status == 1
+    assert c.cache.device_error() == 0
+
+
+# ---------------------------------------------------------------- scores
+
+@pytest.mark.parametrize("width", [None, 200])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_scores_of_minus_infinity_have_no_weight(dtype, width):
+    # keys of -infinity over whole chunks, ahead of and between others, and over all of a sequence
+    c = Case([200, 200, 33], d=64, hq=4, hkv=1, dtype=dtype, width=width)
+    dark = [(0, p) for p in range(0, 70)] + [(0, p) for p in range(128, 150)] + [(1, p) for p in range(199)] + \
+           [(2, p) for p in range(33)]
+    for b, p in dark:
+        c.model.put(c.table[b, p // 16], p % 16, 0, False, torch.full((64,), -math.inf))
+    c.upload()
+    q = c.rows(3, 4).abs() + 0.1
+    out, lse = c.cache.decode_attn(0, c.batch, q, return_lse=True)
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    gone = {b: [p for x, p in dark if x == b] for b in range(3)}
+    for b, n in ((0, 200), (1, 200)):
+        live = [p for p in range(n) if p not in gone[b]]
+        k, _, _ = c.model.rows(c.table[b], 0, n, 0, False)
+        v, _, _ = c.model.rows(c.table[b], 0, n, 0, True)
+        for j in range(4):
+            qq = q[b, j].double().cpu().numpy()
+            t = k[live] @ qq / 8
+            p = np.exp(t - t.max())
+            e = 80 * 2.0 ** -23 / 8 * (np.abs(k[live]) @ np.abs(qq)).max() + 2.0 ** -20
+            tol = torch.finfo(c.dtype).eps / 2 * np.abs(p @ v[live] / p.sum()) + \
+                (2.0 ** -16 + 2 * e + 89 * 2.0 ** -23) * (p @ np.abs(v[live])) / p.sum() + 2.0 ** -24
+            assert (np.abs(o[b, j] - p @ v[live] / p.sum()) <= tol).all()
+            assert abs(l[b, j] - t.max() - np.log(p.sum())) <= 2 * e + 2.0 ** -16 + 2.0 ** -20 * abs(l[b, j])
+    assert (o[2] == 0).all() and (l[2] == -math.inf).all()
     assert c.cache.device_error() == 0
