@@ -481,7 +481,8 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
  *   scale: multiplies the scores; 0 means 1 / sqrt(head_dim).
  *   workspace: device scratch of kvq_paged_workspace_bytes(h, num_seqs) bytes,
  *     256-byte aligned, whatever it holds; not shared with a call in flight.
- * KVQ_ERR_ARG for a negative window or a scale that is not finite;
+ * KVQ_ERR_ARG for a negative window or a scale that is not finite, or not so
+ * times log2(e) (above 2.35e38);
  * KVQ_ERR_CAPACITY for a small workspace; KVQ_ERR_UNSUPPORTED where the tables
  * could hold more than 2^30 tiles of work for every SM. */
 kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* q, void* out,

@@ -237,6 +237,7 @@ kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch*
   p.out = out;
   p.lse = lse;
   p.alpha = static_cast<float>(sc * 1.4426950408889634);
+  if (!std::isfinite(p.alpha)) return KVQ_ERR_ARG;  // scores are taken in base 2
   p.window = window;
   p.hkv = h->cfg.num_kv_heads;
   p.gqa = h->cfg.num_q_heads / h->cfg.num_kv_heads;

@@ -67,6 +67,7 @@ class LayerView(ctypes.Structure):
 
 
 KVQ_FP16, KVQ_BF16 = 0, 1
+_FLT_MIN = 2.0 ** -126
 
 
 class PagedLayerCfg(ctypes.Structure):
@@ -659,6 +660,8 @@ class KVQPagedCache:
                 not out.is_contiguous():
             raise ValueError(f"out must be contiguous {self.dtype} of shape {(S, self.Hq, self.D)} on {self.device}")
         lse = self._new(stream, (S, self.Hq), self._f32) if return_lse else None
+        if scale and -_FLT_MIN < scale < _FLT_MIN:  # as a C float it could be 0, which means another scale
+            raise ValueError(f"scale must be 0 or at least {_FLT_MIN} in magnitude, got {scale}")
         nws = self._ws.get(S)
         if nws is None:
             nws = self._ws[S] = kvq_paged_workspace_bytes(self.h, S)

@@ -145,3 +145,15 @@ def test_scores_of_minus_infinity_have_no_weight(dtype, width):
             assert abs(l[b, j] - t.max() - np.log(p.sum())) <= 2 * e + 2.0 ** -16 + 2.0 ** -20 * abs(l[b, j])
     assert (o[2] == 0).all() and (l[2] == -math.inf).all()
     assert c.cache.device_error() == 0
+
+
+@pytest.mark.parametrize("width", [None, 200])
+def test_a_scale_that_leaves_fp32_is_refused(width):
+    c = Case([40], d=64, width=width)
+    q = c.rows(1, 8)
+    for scale in (3e38, -3e38, 1e-46):
+        with pytest.raises((K.KVQError, ValueError)):
+            c.cache.decode_attn(0, c.batch, q, scale=scale)
+    out, lse = c.cache.decode_attn(0, c.batch, q, scale=1e-30, return_lse=True)
+    v = c.model.rows(c.table[0], 0, 40, 0, True)[0].mean(0)
+    assert np.abs(out[0, 0].double().cpu().numpy() - v).max() <= 2 ** -11 * 4 and float((lse - math.log(40)).abs().max()) < 1e-5
