@@ -279,6 +279,9 @@ def kvq_destroy(h: int) -> None:
 def make_paged_config(layers: Sequence[Tuple[int, int]], num_q_heads: int, num_kv_heads: int, head_dim: int,
                       page_size: int, num_pages: int, dtype: int = KVQ_FP16):
     """layers: (k_bits, v_bits) per layer; dtype: KVQ_FP16 or KVQ_BF16."""
+    sizes = (num_q_heads, num_kv_heads, head_dim, page_size, num_pages, dtype)
+    if any(not -2 ** 31 <= x < 2 ** 31 for x in sizes) or any(not 0 <= b < 256 for x in layers for b in x):
+        raise ValueError("a size that 32 bits, or a width that 8 bits do not hold")  # C types would cut it
     arr = (PagedLayerCfg * len(layers))()
     for i, (kb, vb) in enumerate(layers):
         arr[i].k_bits, arr[i].v_bits = kb, vb
@@ -608,6 +611,11 @@ class KVQPagedCache:
             raise ValueError(f"batch must be on {self.device}, got {batch.device}")
         return batch.args
 
+    def _counts(self, layer: int, n: int, where: str) -> None:
+        """Refuses what a C int would cut to another number."""
+        if not 0 <= layer < len(self.layers) or not 0 <= n < 2 ** 31:
+            raise KVQError(1, where)
+
     def _stream(self, stream) -> int:
         return self._raw_stream(self._index) if stream is None else stream.cuda_stream
 
@@ -622,6 +630,7 @@ class KVQPagedCache:
         None without q.  Rows of q_out that belong to no sequence are not
         written."""
         n = K.shape[0]
+        self._counts(layer, n, "kvq_paged_append")
         k, v = self._rows(K, "K", n, self.Hkv), self._rows(V, "V", n, self.Hkv)
         b = self._batch(batch)
         if b.cu_tokens is None and n != batch.num_seqs:
@@ -652,6 +661,7 @@ class KVQPagedCache:
         tokens (0: all): q [S, Hq, d] -> [S, Hq, d] in the cache's dtype, and
         with return_lse (out, fp32 [S, Hq] log-sum-exp of the scaled scores)."""
         S = batch.num_seqs
+        self._counts(layer, window, "kvq_paged_decode_attn")
         b = self._batch(batch)
         qr = self._rows(q, "q", S, self.Hq)
         if out is None:
@@ -679,6 +689,7 @@ class KVQPagedCache:
         """The newest rows of every sequence as the cache holds them: (K, V),
         [n, Hkv, d] in the cache's dtype; rows that belong to no sequence are
         not written."""
+        self._counts(layer, n, "kvq_paged_read")
         b = self._batch(batch)
         if b.cu_tokens is None and n != batch.num_seqs:
             raise ValueError(f"n is {n}, expected one row for each of {batch.num_seqs} sequences")
@@ -694,6 +705,7 @@ class KVQPagedCache:
         return K, V
 
     def view(self, layer: int) -> dict:
+        self._counts(layer, 0, "kvq_paged_view_get")
         return kvq_paged_view_get(self.h, layer)
 
     def device_error(self, stream=None) -> int:

@@ -157,3 +157,29 @@ def test_a_scale_that_leaves_fp32_is_refused(width):
     out, lse = c.cache.decode_attn(0, c.batch, q, scale=1e-30, return_lse=True)
     v = c.model.rows(c.table[0], 0, 40, 0, True)[0].mean(0)
     assert np.abs(out[0, 0].double().cpu().numpy() - v).max() <= 2 ** -11 * 4 and float((lse - math.log(40)).abs().max()) < 1e-5
+
+
+# ---------------------------------------------------------------- what the binding takes
+
+def test_numbers_that_do_not_fit_the_c_types_are_refused():
+    c = Case([40, 20], [1, 1], kb=8, vb=4, d=64)
+    q, k, v = c.rows(2, 8), c.rows(2, 2), c.rows(2, 2)
+    before = c.download().copy()
+    for layer in (2 ** 32, -2 ** 32, 2 ** 64):
+        for fn in (lambda: c.cache.append(layer, c.batch, k, v), lambda: c.cache.decode_attn(layer, c.batch, q),
+                   lambda: c.cache.read(layer, c.batch, 2), lambda: c.cache.view(layer)):
+            with pytest.raises(K.KVQError) as e:
+                fn()
+            assert e.value.status == 1
+    for window in (2 ** 32, 2 ** 32 + 5, 2 ** 31, -2 ** 32 + 7):
+        with pytest.raises(K.KVQError) as e:
+            c.cache.decode_attn(0, c.batch, q, window=window)
+        assert e.value.status == 1
+    wide = k[:1].expand(2 ** 32 + 2, 2, 64)
+    for fn in (lambda: c.cache.append(0, c.batch, wide, wide),
+               lambda: c.cache.read(0, c.batch, 2 ** 32 + 2, K=wide, V=wide)):
+        with pytest.raises((K.KVQError, ValueError)):
+            fn()
+    assert np.array_equal(c.download(), before) and c.cache.device_error() == 0
+    a = c.cache.decode_attn(0, c.batch, q, window=2 ** 31 - 1)
+    assert torch.equal(a, c.cache.decode_attn(0, c.batch, q))
