@@ -455,7 +455,8 @@ kvq_status kvq_paged_create(const kvq_paged_config* cfg, void* dev_buf, size_t b
  * `rotation` (NULL: as they are), rounded to the cache's type or quantized,
  * and written to their slots with the values; queries turned alike into q_out.
  *   K, V: [n_tokens][num_kv_heads] rows.  q, q_out: [n_tokens][num_q_heads]
- *     rows, or both NULL; q_out may be q itself, and overlaps nothing else.
+ *     rows, or both NULL; q_out may be q itself, and overlaps nothing else, nor
+ *     its rows one another.
  *   n_tokens: rows of the tensors; without cu_tokens, equal to num_seqs.
  * Rows need only their type's alignment; 16-byte aligned rows are faster.
  * Quantized rows are taken in fp16 (clamped to +-65504): zero = min,
@@ -494,7 +495,8 @@ size_t kvq_paged_workspace_bytes(const kvq_paged* h, int num_seqs);
 
 /* Reads the newest rows of every sequence (cu_tokens as for an append) back as
  * the cache holds them: code * scale + zero in fp32, rounded once to the
- * cache's type.  K, V: [n_tokens][num_kv_heads] rows; either may be NULL.
+ * cache's type.  K, V: [n_tokens][num_kv_heads] rows, none of which overlaps
+ * another; either may be NULL.
  * Rows with a bad page are left as they were. */
 kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K, const kvq_rows* V,
                           int n_tokens, void* stream);

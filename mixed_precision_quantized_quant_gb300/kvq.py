@@ -599,6 +599,15 @@ class KVQPagedCache:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, self.D)}")
         raise ValueError(f"{name} must be {self.dtype} on {self.device}, got {t.dtype} on {t.device}")
 
+    def _out_rows(self, t, name: str, n: int, heads: int) -> Rows:
+        """Rows to write, none of which may share a place with another."""
+        r, d = self._rows(t, name, n, heads), self.D
+        a, b = r.token_stride, r.head_stride
+        if (n > 1 and a < d) or (heads > 1 and b < d) or \
+                (n > 1 and heads > 1 and a < (heads - 1) * b + d and b < (n - 1) * a + d):
+            raise ValueError(f"{name}'s rows overlap one another")
+        return r
+
     def _new(self, stream, shape, dtype):
         """An output or scratch tensor that the allocator ties to the call's stream."""
         if stream is None:
@@ -646,7 +655,7 @@ class KVQPagedCache:
             qr = self._rows(q, "q", n, self.Hq)
             if q_out is None:
                 q_out = self._new(stream, (n, self.Hq, self.D), self.dtype)
-            qo = self._rows(q_out, "q_out", n, self.Hq)
+            qo = self._out_rows(q_out, "q_out", n, self.Hq)
         elif q_out is not None:
             raise ValueError("q_out without q")
         args = self.h, layer, b, k, v, qr, qo, r, n, self._stream(stream)
@@ -697,7 +706,7 @@ class KVQPagedCache:
             K = self._new(stream, (n, self.Hkv, self.D), self.dtype)
         if V is None:
             V = self._new(stream, (n, self.Hkv, self.D), self.dtype)
-        k, v = self._rows(K, "K", n, self.Hkv), self._rows(V, "V", n, self.Hkv)
+        k, v = self._out_rows(K, "K", n, self.Hkv), self._out_rows(V, "V", n, self.Hkv)
         args = self.h, layer, b, k, v, n, self._stream(stream)
         st = self._c_read(*args) if self._current_device() == self._index else self._on_device(self._c_read, *args)
         if st:

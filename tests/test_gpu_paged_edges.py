@@ -183,3 +183,26 @@ def test_numbers_that_do_not_fit_the_c_types_are_refused():
     assert np.array_equal(c.download(), before) and c.cache.device_error() == 0
     a = c.cache.decode_attn(0, c.batch, q, window=2 ** 31 - 1)
     assert torch.equal(a, c.cache.decode_attn(0, c.batch, q))
+
+
+def test_outputs_that_overlap_themselves_are_refused():
+    c = Case([40, 20, 9], [1, 1, 1], kb=8, vb=4, d=64, hq=4, hkv=2)
+    q, k, v = c.rows(3, 4), c.rows(3, 2), c.rows(3, 2)
+    before = c.download().copy()
+    half = torch.float16
+    flat = torch.zeros(3 * 4 * 64, dtype=half, device="cuda")
+    for n, strides in ((4, (0, 64, 1)), (4, (4 * 64, 0, 1)), (4, (128, 64, 1)), (4, (64, 32, 1)), (2, (0, 64, 1)), (2, (64, 64, 1)),
+                       (2, (128, 63, 1))):
+        out = flat.as_strided((3, n, 64), strides)
+        for fn in (lambda: c.cache.append(0, c.batch, k, v, q=q, q_out=out),) if n == 4 else (
+                lambda: c.cache.read(0, c.batch, 3, K=out), lambda: c.cache.read(0, c.batch, 3, V=out)):
+            with pytest.raises(ValueError):
+                fn()
+    assert np.array_equal(c.download(), before) and not bool(flat.any())
+    # heads outside, tokens inside; inputs that repeat a row
+    out = torch.zeros(4, 3, 64, dtype=half, device="cuda").transpose(0, 1)
+    one = k[:1].expand(3, 2, 64)
+    got = c.cache.append(0, c.batch, one, one, q=q, q_out=out)
+    assert got is out and torch.equal(got, q)
+    rk, _ = c.cache.read(0, c.batch, 3)
+    assert torch.equal(rk[0], rk[2])
