@@ -206,3 +206,27 @@ def test_outputs_that_overlap_themselves_are_refused():
     assert got is out and torch.equal(got, q)
     rk, _ = c.cache.read(0, c.batch, 3)
     assert torch.equal(rk[0], rk[2])
+
+
+def test_the_functions_of_the_c_names():
+    # the binding's functions by the names of the C entries do what the class does
+    c = Case([40, 20], [3, 2], kb=8, vb=4, d=64, hq=4, hkv=2)
+    h, s = c.cache.h, torch.cuda.current_stream().cuda_stream
+    q, k, v = c.rows(5, 4), c.rows(5, 2), c.rows(5, 2)
+    out, rk, rv = torch.empty(2, 4, 64, dtype=c.dtype, device="cuda"), torch.empty_like(k), torch.empty_like(v)
+    qo = torch.empty(5, 4, 64, dtype=c.dtype, device="cuda")
+    rot = K.Rotation(K.rotation_table(60, 64))
+
+    def rows(x):
+        return K.Rows(x.data_ptr(), x.stride(0), x.stride(1))
+
+    K.kvq_paged_append(h, 0, c.batch.args, rows(k), rows(v), rows(q), rows(qo), rot.args, 5, s)
+    mine = c.download().copy()
+    K.kvq_paged_read(h, 0, c.batch.args, rows(rk), rows(rv), 5, s)
+    ws = torch.empty(K.kvq_paged_workspace_bytes(h, 2), dtype=torch.uint8, device="cuda")
+    K.kvq_paged_decode_attn(h, 0, c.batch.args, rows(qo), out.data_ptr(), None, 0.0, 0, ws.data_ptr(), ws.numel(), s)
+    assert torch.equal(qo, c.cache.append(0, c.batch, k, v, q=q, rotation=rot))
+    assert np.array_equal(mine, c.download())
+    ek, ev = c.cache.read(0, c.batch, 5)
+    assert torch.equal(rk, ek) and torch.equal(rv, ev)
+    assert torch.equal(out, c.cache.decode_attn(0, c.batch, qo[:2]))
