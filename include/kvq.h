@@ -338,7 +338,7 @@ const char* kvq_status_string(kvq_status s);
  *   - Lengths, tables and rows are read on the device: nothing of a call but
  *     pointers, strides and counts is fixed on the host, so a captured call
  *     follows the tensors it was captured with.
- *   - The handle is not changed by any call after kvq_paged_create(): calls on
+ *   - What a call works by is not changed after kvq_paged_create(): calls on
  *     it may come from several threads and streams.  The caller orders calls
  *     that append to a page with those that read or append to the same page.
  *   - The current device must be the one of kvq_paged_create() (KVQ_ERR_ARG).
@@ -503,7 +503,8 @@ kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch,
 
 kvq_status kvq_paged_view_get(const kvq_paged* h, int layer, kvq_paged_view* v);
 
-/* Reads and clears the error word, synchronizing `stream`: 0, or 1 a device
+/* Takes the error word, synchronizing `stream`; what calls on other streams
+ * set meanwhile is in it or stays for the next call.  0, or 1 a device
  * wait gave up, 2 a length or a row count that the batch's tensors cannot
  * mean, 4 a bad page number, 5 a position outside the rotation's table. */
 kvq_status kvq_paged_device_error(kvq_paged* h, int32_t* code, void* stream);

@@ -6,6 +6,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -22,7 +23,7 @@ struct Trace {
 };
 
 constexpr int64_t kAlign = 256;
-constexpr int64_t kTail = 256;  // the library's own bytes behind the pages: the error word
+constexpr int64_t kTail = 256;  // the library's own bytes behind the pages: the error word, and where it is taken to
 constexpr int kMaxLayers = 1 << 16, kMaxHeads = 1 << 16;
 
 struct PagedLayer {
@@ -71,6 +72,9 @@ kvq_status paged_size(const kvq_paged_config* c, int64_t* bytes) {
   return KVQ_OK;
 }
 
+// Takes the error word in one step, so that no call of another stream sets it between its reading and its clearing.
+__global__ void take_error_kernel(int32_t* err) { err[1] = atomicExch(err, 0); }
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -81,6 +85,7 @@ struct kvq_paged {
   uint8_t* base = nullptr;
   int32_t* err = nullptr;
   int device = 0, sms = 0;
+  std::mutex taking;  // of the error word: err[1] is one call's at a time
 };
 
 namespace {
@@ -285,12 +290,20 @@ kvq_status kvq_paged_device_error(kvq_paged* h, int32_t* code, void* stream) {
   Trace trace("kvq_paged_device_error");
   if (!h || !code) return KVQ_ERR_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (cur != h->device) return KVQ_ERR_ARG;
   int32_t v = 0;
-  // copied and cleared in the stream's order, so that a word set by work
-  // queued behind this call is not lost
-  if (cudaMemcpyAsync(&v, h->err, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaMemsetAsync(h->err, 0, 4, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+  try {
+    const std::lock_guard<std::mutex> one(h->taking);
+    take_error_kernel<<<1, 1, 0, s>>>(h->err);
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyAsync(&v, h->err + 1, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+  } catch (...) {
     return KVQ_ERR_CUDA;
+  }
   *code = v;
   return KVQ_OK;
 }

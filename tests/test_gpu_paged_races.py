@@ -1,5 +1,5 @@
 """The paged cache under what its caller does at the same time: lengths that
-change while the attention reads them."""
+change while the attention reads them, errors of one stream read on another."""
 
 import pytest
 import torch
@@ -41,3 +41,22 @@ def test_lengths_that_change_under_the_attention(kb, vb):
     lens.fill_(64)
     assert torch.equal(c.cache.decode_attn(0, batch, q), alone)
     assert (c.download() == before).all() and c.cache.device_error() == 0
+
+
+def test_errors_of_another_stream_are_not_lost():
+    # one bad call each time, whose report is taken while it runs or after it, but taken
+    c = Case([40], d=64, hq=8, hkv=1, fill=False)
+    bad = K.PagedBatch(torch.full((1, 3), -1, dtype=torch.int32, device="cuda"), torch.tensor([40], dtype=torch.int32).cuda())
+    k, q = c.rows(1, 1), c.rows(1, 8)
+    work, side = torch.cuda.Stream(), torch.cuda.Stream()
+    a = torch.randn(256, 256, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(400):
+        with torch.cuda.stream(work):
+            for _ in range(i % 5):
+                a @ a
+            c.cache.append(0, bad, k, k, q=q)
+        first = c.cache.device_error(side)
+        work.synchronize()
+        assert 4 in (first, c.cache.device_error(side)), i
+    assert c.cache.device_error() == 0
