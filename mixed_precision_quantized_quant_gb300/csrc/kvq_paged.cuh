@@ -35,12 +35,14 @@ struct PagedPool {
   int page_shift;         // log2(page_size)
   int kb, vb;
   int32_t* err;
+  const uint8_t* hi;      // end of the layer's pages (checked in debug builds)
 };
 
 struct PagedRows {
   uint8_t* data;
   int64_t token_stride;   // elements
   int64_t head_stride;
+  const uint8_t *lo, *hi; // where the rows lie (checked in debug builds)
 };
 
 struct PagedAppendParams {
@@ -76,9 +78,24 @@ struct PagedAttnParams {
   int q_vec;              // every row of q is 16-byte aligned
   uint8_t* ws;             // what the join needs of every unit, then partial results
   int64_t ws_partials;    // where those start
+  const uint8_t* ws_hi;   // end of the workspace (checked in debug builds)
   int solo;               // a CTA for each unit, no join (set at launch)
   int ctas;               // of the attention kernel (set at launch)
 };
+
+// ---------------------------------------------------------------- debug checks
+
+// in_range (kvq_device.cuh) on what these calls were given; `true` in a release
+// build.  A miss is reported, and the access skipped.
+__device__ __forceinline__ bool pool_ok(const PagedPool& p, const void* a, size_t bytes) {
+  return in_range(a, bytes, p.pages, p.hi, p.err);
+}
+__device__ __forceinline__ bool rows_ok(const PagedRows& r, const void* a, size_t bytes, int32_t* err) {
+  return in_range(a, bytes, r.lo, r.hi, err);
+}
+__device__ __forceinline__ bool table_ok(const PagedBatch& b, const int32_t* a, int32_t* err) {
+  return in_range(a, 4, b.table, b.table + (b.seqs - 1) * b.table_stride + b.max_pages, err);
+}
 
 // ---------------------------------------------------------------- tile layout
 

@@ -86,6 +86,7 @@ struct kvq_paged {
   int32_t* err = nullptr;
   int device = 0, sms = 0;
   std::mutex taking;  // of the error word: err[1] is one call's at a time
+  int64_t checked_bytes = INT64_MAX;  // debug builds: where the checks take a layer's pages to end at the latest
 };
 
 namespace {
@@ -119,18 +120,22 @@ kvq_status open_call(const kvq_paged* h, int layer, const kvq_paged_batch* b, kv
   pool->kb = l.kb;
   pool->vb = l.vb;
   pool->err = h->err;
+  pool->hi = pool->pages + (l.page_stride * h->cfg.num_pages < h->checked_bytes ? l.page_stride * h->cfg.num_pages : h->checked_bytes);
   return KVQ_OK;
 }
 
-// Rows of 2-byte values: at least their own alignment; *vec cleared unless
-// every row starts on 16 bytes.
-kvq_status take_rows(const kvq_rows* r, kvq::PagedRows* out, int* vec) {
+// `n` rows of `heads` rows of `d` 2-byte values: at least their own alignment;
+// *vec cleared unless every row starts on 16 bytes.
+kvq_status take_rows(const kvq_rows* r, int n, int heads, int d, kvq::PagedRows* out, int* vec) {
   if (!r || !r->data) return KVQ_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(r->data) & 1u) return KVQ_ERR_ALIGN;
   if (!aligned16(r->data) || r->token_stride % 8 != 0 || r->head_stride % 8 != 0) *vec = 0;
   out->data = static_cast<uint8_t*>(r->data);
   out->token_stride = r->token_stride;
   out->head_stride = r->head_stride;
+  const int64_t tokens = (n - 1) * r->token_stride, others = (heads - 1) * r->head_stride;
+  out->lo = out->data + 2 * ((tokens < 0 ? tokens : 0) + (others < 0 ? others : 0));
+  out->hi = out->data + 2 * ((tokens > 0 ? tokens : 0) + (others > 0 ? others : 0) + d);
   return KVQ_OK;
 }
 
@@ -193,8 +198,13 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
   if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!q != !q_out)) return KVQ_ERR_ARG;
   if (n_tokens == 0) return KVQ_OK;
   p.vec = 1;
-  if ((st = take_rows(K, &p.k, &p.vec)) != KVQ_OK || (st = take_rows(V, &p.v, &p.vec)) != KVQ_OK) return st;
-  if (q && ((st = take_rows(q, &p.q, &p.vec)) != KVQ_OK || (st = take_rows(q_out, &p.qo, &p.vec)) != KVQ_OK)) return st;
+  const int hq = h->cfg.num_q_heads, hkv = h->cfg.num_kv_heads, d = h->cfg.head_dim;
+  if ((st = take_rows(K, n_tokens, hkv, d, &p.k, &p.vec)) != KVQ_OK ||
+      (st = take_rows(V, n_tokens, hkv, d, &p.v, &p.vec)) != KVQ_OK)
+    return st;
+  if (q && ((st = take_rows(q, n_tokens, hq, d, &p.q, &p.vec)) != KVQ_OK ||
+            (st = take_rows(q_out, n_tokens, hq, d, &p.qo, &p.vec)) != KVQ_OK))
+    return st;
   if (rotation) {
     if (!rotation->table || rotation->rows < 1 || rotation->dim < 16 || rotation->dim % 16 != 0 ||
         rotation->dim > h->cfg.head_dim || (rotation->interleaved != 0 && rotation->interleaved != 1))
@@ -207,9 +217,9 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
     p.interleaved = rotation->interleaved;
   }
   p.n = n_tokens;
-  p.hq = q ? h->cfg.num_q_heads : 0;
-  p.hkv = h->cfg.num_kv_heads;
-  return kvq::paged_append_launch(p, h->cfg.head_dim, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  p.hq = q ? hq : 0;
+  p.hkv = hkv;
+  return kvq::paged_append_launch(p, d, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }
@@ -228,7 +238,7 @@ kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch*
   kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
   if (st != KVQ_OK) return st;
   p.q_vec = 1;
-  if ((st = take_rows(q, &p.q, &p.q_vec)) != KVQ_OK) return st;
+  if ((st = take_rows(q, batch->num_seqs, h->cfg.num_q_heads, h->cfg.head_dim, &p.q, &p.q_vec)) != KVQ_OK) return st;
   if (!out || !workspace || window < 0 || !std::isfinite(scale)) return KVQ_ERR_ARG;
   if (!aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
       (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
@@ -247,6 +257,7 @@ kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch*
   p.hkv = h->cfg.num_kv_heads;
   p.gqa = h->cfg.num_q_heads / h->cfg.num_kv_heads;
   p.ws = static_cast<uint8_t*>(workspace);
+  p.ws_hi = p.ws + workspace_bytes;
   return kvq::paged_attn_launch(p, h->cfg.head_dim, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? KVQ_OK
@@ -262,11 +273,12 @@ kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch,
   if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!K && !V)) return KVQ_ERR_ARG;
   if (n_tokens == 0) return KVQ_OK;
   p.vec = 1;
-  if (K && (st = take_rows(K, &p.k, &p.vec)) != KVQ_OK) return st;
-  if (V && (st = take_rows(V, &p.v, &p.vec)) != KVQ_OK) return st;
+  const int hkv = h->cfg.num_kv_heads, d = h->cfg.head_dim;
+  if (K && (st = take_rows(K, n_tokens, hkv, d, &p.k, &p.vec)) != KVQ_OK) return st;
+  if (V && (st = take_rows(V, n_tokens, hkv, d, &p.v, &p.vec)) != KVQ_OK) return st;
   p.n = n_tokens;
-  p.hkv = h->cfg.num_kv_heads;
-  return kvq::paged_read_launch(p, h->cfg.head_dim, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  p.hkv = hkv;
+  return kvq::paged_read_launch(p, d, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }
@@ -307,6 +319,17 @@ kvq_status kvq_paged_device_error(kvq_paged* h, int32_t* code, void* stream) {
   *code = v;
   return KVQ_OK;
 }
+
+#ifdef KVQ_DEBUG
+// For the tests of the checks: accesses past the first `bytes` of a layer's
+// pages count as outside them, so that a check fires on memory that is there.
+kvq_status kvq_paged_debug_limit(kvq_paged* h, int64_t bytes);
+kvq_status kvq_paged_debug_limit(kvq_paged* h, int64_t bytes) {
+  if (!h || bytes < 0) return KVQ_ERR_ARG;
+  h->checked_bytes = bytes;
+  return KVQ_OK;
+}
+#endif
 
 kvq_status kvq_paged_destroy(kvq_paged* h) {
   Trace trace("kvq_paged_destroy");

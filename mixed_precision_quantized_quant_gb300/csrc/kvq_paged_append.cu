@@ -38,6 +38,10 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ bool angles_ok(const PagedAppendParams& p, const void* a, size_t bytes) {  // (debug builds)
+  return in_range(a, bytes, p.rope, p.rope + static_cast<int64_t>(p.rope_rows) * p.rope_dim, p.pool.err);
+}
+
 struct AppendSmem {
   RowPlace places[kRowTokens];
   uint4 ring[kRowThreads / 32][kDepth][2][32];  // each lane's two chunks of the groups under way
@@ -108,7 +112,13 @@ struct RowWork {
         b = pack8<T>(f[1]);
       }
     }
-    const bool live = head < heads<KIND>();
+    bool live = head < heads<KIND>();
+    if constexpr (KIND == kQueries) {
+      const T* y = reinterpret_cast<const T*>(p.qo.data) + row * p.qo.token_stride + head * p.qo.head_stride;
+      live = live && rows_ok(p.qo, y, 2 * D, p.pool.err);
+    } else {
+      live = live && pool_ok(p.pool, p.pool.pages + pl.tile + head * p.pool.head_stride, p.pool.tile_bytes);
+    }
     if constexpr (KIND == kQueries) {
       if (live) {
         T* y = reinterpret_cast<T*>(p.qo.data) + row * p.qo.token_stride + head * p.qo.head_stride;
@@ -199,6 +209,7 @@ struct Appender {
     const int head = ahead.g * W::RPW + w.sub;
     if (head >= w.template heads<KIND>()) return;
     const T* x = w.template row_of<KIND>(row0 + ahead.tk, head);
+    if (!rows_ok(w.template rows<KIND>(), x, 2 * D, w.p.pool.err)) return;
     uint4* y = &sm.ring[warp][slot][0][lane];
     if (w.p.vec) {
       copy16(y, x + 8 * w.c0);
@@ -258,9 +269,10 @@ __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) paged_append_kernel
   if (p.rope) {  // every token's angles once, for all its rows
     const int quads = p.rope_dim / 4;
     for (int tk = warp; tk < count; tk += kRowThreads / 32)
-      if (sm.places[tk].ok && lane < quads)
-        *reinterpret_cast<float4*>(&sm.angles[tk][4 * lane]) =
-            __ldg(reinterpret_cast<const float4*>(p.rope + static_cast<int64_t>(sm.places[tk].rope) * p.rope_dim) + lane);
+      if (sm.places[tk].ok && lane < quads) {
+        const float4* x = reinterpret_cast<const float4*>(p.rope + static_cast<int64_t>(sm.places[tk].rope) * p.rope_dim) + lane;
+        if (angles_ok(p, x, 16)) *reinterpret_cast<float4*>(&sm.angles[tk][4 * lane]) = __ldg(x);
+      }
     __syncthreads();
   }
   int slot = 0;
@@ -293,8 +305,10 @@ __global__ void __launch_bounds__(1024) paged_append_few_kernel(const __grid_con
     if (head < (q ? p.hq : p.hkv)) {
       const T* x = q ? w.template row_of<kQueries>(row, head)
                      : k ? w.template row_of<kKeys>(row, head) : w.template row_of<kValues>(row, head);
-      load8(x + 8 * w.c0, p.vec, a);
-      load8(x + 8 * w.c1, p.vec, b);
+      if (rows_ok(q ? p.q : k ? p.k : p.v, x, 2 * D, p.pool.err)) {
+        load8(x + 8 * w.c0, p.vec, a);
+        load8(x + 8 * w.c1, p.vec, b);
+      }
     }
     if (!found) {
       pl = find_places(p.batch, p.pool, row, 1, p.rope, p.positions, p.rope_rows, lane);
@@ -306,6 +320,7 @@ __global__ void __launch_bounds__(1024) paged_append_few_kernel(const __grid_con
     }
     if (!pl.ok) return;
     const float* angles = p.rope ? p.rope + static_cast<int64_t>(pl.rope) * p.rope_dim : nullptr;
+    if (angles && !angles_ok(p, angles, 4 * p.rope_dim)) return;
     if (q)
       w.template one<kQueries>(row, head, pl, angles, a, b);
     else if (k)

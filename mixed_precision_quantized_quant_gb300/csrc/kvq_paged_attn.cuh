@@ -208,6 +208,17 @@ __device__ __forceinline__ void bulk_g2s_at(uint32_t dst, const void* src, uint3
       : "memory");
 }
 
+// Debug builds: row `row` of the output, and one partial result, lie in their buffers.
+template <typename T>
+__device__ __forceinline__ bool out_ok(const PagedAttnParams& p, int64_t row, int D) {
+  const T* out = reinterpret_cast<const T*>(p.out);
+  const int64_t rows = static_cast<int64_t>(p.batch.seqs) * p.hkv * p.gqa;
+  return in_range(out + row * D, D * sizeof(T), out, out + rows * D, p.pool.err);
+}
+__device__ __forceinline__ bool part_ok(const PagedAttnParams& p, const float* part, int D) {
+  return in_range(part, partial_floats(D) * 4, p.ws + p.ws_partials, p.ws_hi, p.pool.err);
+}
+
 // N words (1, 2 or 4) from shared memory in one load.
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -340,6 +351,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     cs = segs[0];
     if (cs.len == 0) {
       const int64_t row = static_cast<int64_t>(blockIdx.x) * p.gqa;
+      if (!out_ok<T>(p, row, D) || !out_ok<T>(p, row + p.gqa - 1, D)) return;
       for (int x = threadIdx.x; x < p.gqa * D; x += kThreads) reinterpret_cast<T*>(p.out)[row * D + x] = Num<T>::from(0.0f);
       if (p.lse && threadIdx.x < p.gqa) p.lse[row + threadIdx.x] = -INFINITY;
       return;
@@ -442,6 +454,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     if (qhead >= p.gqa) return;
     const T* src = reinterpret_cast<const T*>(p.q.data) + u.b * p.q.token_stride +
                    (u.h * p.gqa + qhead) * p.q.head_stride + qchunk * 8;
+    if (!rows_ok(p.q, src, 16, p.pool.err)) return;
     uint8_t* dst = qraw + (C::quant ? 0 : which * 16 * D);
     if (p.q_vec) {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -544,15 +557,15 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         if (n > 0) {
           const int e = (tok0 >> p.pool.page_shift) + piece;
           // a page wholly before the window is masked, and its entry may be gone
-          int page = ((e + 1) << p.pool.page_shift) <= ps.first
-                         ? 0
-                         : __ldg(p.batch.table + ps.b * p.batch.table_stride + e);
+          const int32_t* entry = p.batch.table + ps.b * p.batch.table_stride + e;
+          int page = ((e + 1) << p.pool.page_shift) <= ps.first || !table_ok(p.batch, entry, p.pool.err) ? 0 : __ldg(entry);
           if (page < 0 || page >= p.pool.num_pages) {
             atomicExch(p.pool.err, kErrBadPage);
             page = 0;
           }
           src = p.pool.pages + page * p.pool.page_stride + ps.h * p.pool.head_stride +
                 (ppc > 1 ? 0 : ((tok0 >> 4) & (tiles_page - 1)) * C::TB);
+          if (!pool_ok(p.pool, src, bytes)) src = p.pool.pages;  // (a barrier counts on the bytes)
         }
       }
       if (last < ps.i1) break;
@@ -909,7 +922,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         const int64_t last = (r0 + cs.hi - 1 - cs.cbase) / per;  // the CTA of the unit's last chunk
         Meta meta = {static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(ends ? 0 : last - blockIdx.x + 1),
                      cs.i0 > 0 ? 1 : 0, 0};
-        *reinterpret_cast<int4*>(p.ws + unit * sizeof(Meta)) = *reinterpret_cast<int4*>(&meta);
+        uint8_t* note = p.ws + unit * sizeof(Meta);
+        if (in_range(note, sizeof(Meta), p.ws, p.ws + p.ws_partials, p.pool.err))
+          *reinterpret_cast<int4*>(note) = *reinterpret_cast<int4*>(&meta);
       }
       if (starts && ends) {
 #pragma unroll
@@ -917,6 +932,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
           const int head = 2 * t + hd;
           if (head < p.gqa) {
             const int64_t row = unit * p.gqa + head;
+            if (!out_ok<T>(p, row, D)) continue;
             const float inv = sum[hd] == 0.0f ? 0.0f : 1.0f / sum[hd];
             T* out = reinterpret_cast<T*>(p.out) + row * D;
 #pragma unroll
@@ -933,7 +949,8 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
       } else {
         float* part = reinterpret_cast<float*>(p.ws + p.ws_partials) +
                       (2 * static_cast<int64_t>(blockIdx.x) + (cs.i0 > 0 ? 1 : 0)) * partial_floats(D);
-        if (g == 0 && warp == 0) {
+        const bool in = part_ok(p, part, D);
+        if (in && g == 0 && warp == 0) {
 #pragma unroll
           for (int hd = 0; hd < 2; ++hd) {
             part[2 * t + hd] = top[hd];
@@ -942,7 +959,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         }
         // [m-tile][lane][4]
 #pragma unroll
-        for (int q = 0; q < QT; ++q) *reinterpret_cast<float4*>(part + 16 + ((warp * QT + q) * 32 + lane) * 4) = r[q];
+        for (int q = 0; in && q < QT; ++q) *reinterpret_cast<float4*>(part + 16 + ((warp * QT + q) * 32 + lane) * 4) = r[q];
       }
     }
     if (cs.i1 >= range) break;
@@ -968,8 +985,11 @@ __global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
   const int64_t unit = blockIdx.x;
   const int b = static_cast<int>(unit / p.hkv);
   const int j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int4 raw = *reinterpret_cast<const int4*>(p.ws + unit * sizeof(Meta));  // (garbage where there is no token)
+  const uint8_t* note = p.ws + unit * sizeof(Meta);
+  if (!in_range(note, sizeof(Meta), p.ws, p.ws + p.ws_partials, p.pool.err)) return;
+  const int4 raw = *reinterpret_cast<const int4*>(note);  // (garbage where there is no token)
   if (seq_len(p, b) == 0) {
+    if (!out_ok<T>(p, unit * p.gqa, D) || !out_ok<T>(p, (unit + 1) * p.gqa - 1, D)) return;
     for (int x = threadIdx.x; x < p.gqa * D; x += 2 * D)
       reinterpret_cast<T*>(p.out)[unit * p.gqa * D + x] = Num<T>::from(0.0f);
     if (p.lse && threadIdx.x < p.gqa) p.lse[unit * p.gqa + threadIdx.x] = -INFINITY;
@@ -999,6 +1019,7 @@ __global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
       v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (i0 + u < count) {
         const float* x = part(i0 + u);
+        if (!part_ok(p, x, D)) continue;
         mi[u] = *reinterpret_cast<const float2*>(x + 2 * t);
         li[u] = *reinterpret_cast<const float2*>(x + 8 + 2 * t);
         v[u] = *reinterpret_cast<const float4*>(x + 16 + (j * 32 + lane) * 4);
@@ -1029,8 +1050,8 @@ __global__ void __launch_bounds__(2 * D) join_kernel(PagedAttnParams p) {
 #pragma unroll
   for (int hd = 0; hd < 2; ++hd) {
     const int head = 2 * t + hd;
-    if (head >= p.gqa) continue;
     const int64_t row = unit * p.gqa + head;
+    if (head >= p.gqa || !out_ok<T>(p, row, D)) continue;
     const float inv = sum[hd] == 0.0f ? 0.0f : 1.0f / sum[hd];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {

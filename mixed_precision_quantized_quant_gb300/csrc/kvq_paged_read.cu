@@ -67,6 +67,11 @@ __device__ __forceinline__ void read_rows(const PagedReadParams& p, const RowPla
         const RowPlace pl = places[r.tk];
         y[u] = reinterpret_cast<T*>(dst.data) + (row0 + r.tk) * dst.token_stride + head * dst.head_stride + 8 * j;
         const uint8_t* tile = p.pool.pages + pl.tile + head * p.pool.head_stride;
+        if (!pool_ok(p.pool, tile, p.pool.tile_bytes) || !rows_ok(dst, y[u], 32 * LPR - 16 * j, p.pool.err)) {
+          y[u] = nullptr;
+          r.next();
+          continue;
+        }
         if constexpr (BITS == 16) {
           tile += (VALUES ? 32 * D : 0) + pl.tok * 2 * D;
           a[u] = *reinterpret_cast<const uint4*>(tile + 16 * tile_chunk16(j, pl.tok));

@@ -70,7 +70,9 @@ __device__ __forceinline__ RowPlace find_places(const PagedBatch& b, const Paged
     atomicExch(pool.err, kErrBadState);
     return r;
   }
-  const int page = b.table[seq * b.table_stride + idx];
+  const int32_t* entry = b.table + seq * b.table_stride + idx;
+  if (!table_ok(b, entry, pool.err)) return r;
+  const int page = *entry;
   int rp = static_cast<int>(pos);
   if (rope) {
     if (positions) rp = positions[row];
