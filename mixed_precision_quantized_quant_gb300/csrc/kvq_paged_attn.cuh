@@ -238,12 +238,9 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
 // The thread column t of a key fragment owns D/4 channels: with 16-bit keys
 // the MMA's own (16 j + 8 i + 2t, + 1 for register 2j + i), with codes the
 // ones of its bytes, a run of D/4 (8 bits, D = 128: the runs of 16 channels at
-// 16t and 16t + 64).  Which of the run's channels are the two halves of
-// register r:
-template <int KB>
-__host__ __device__ constexpr int key_local(int r, int hi) {
-  return KB == 8 ? 2 * r + hi : KB == 4 ? 8 * (r / 4) + r % 4 + 4 * hi : 16 * (r / 8) + r % 8 + 8 * hi;
-}
+// 16t and 16t + 64).  Of the run's channels, register r holds 2r and 2r + 1 with
+// 8-bit codes, 8 (r / 4) + r % 4 and the fourth after it with 4-bit ones, 16 (r / 8) + r % 8
+// and the eighth after it with 2-bit ones (what split_codes leaves in its halves).
 // log2 of the power of two that the field of key register (value channel) r carries
 template <int B>
 __host__ __device__ constexpr int code_field(int r) {
@@ -493,7 +490,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
     e = mx < 1e-30f ? top : (e > 100 ? 100 : e);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + top - e) << 23);
     const float down = __uint_as_float(static_cast<uint32_t>(127 - top + e) << 23);
-    // channel 8 qchunk + i: thread column, register and half (see key_local)
+    // channel 8 qchunk + i: thread column, register and half (see codes, above)
     constexpr bool two_runs = KB == 8 && D == 128;
     const int col = two_runs ? qchunk / 2 % 4 : qchunk / (RC / 4);
     const int in_run = two_runs ? 16 * (qchunk / 8) + 8 * (qchunk % 2) : 8 * (qchunk % (RC / 4));
