@@ -13,7 +13,7 @@ static int64_t partials_at(int hkv, int seqs) {
 }
 
 size_t paged_attn_workspace(int D, int hkv, int seqs, int sms) {
-  return static_cast<size_t>(partials_at(hkv, seqs) + 2LL * 4 * sms * paged::partial_floats(D) * 4);
+  return static_cast<size_t>(partials_at(hkv, seqs) + 2LL * paged::kMostCtas * sms * paged::partial_floats(D) * 4);
 }
 
 static cudaError_t choose(const PagedAttnParams* p, int kb, int vb, int D, int dtype, int sms, cudaStream_t s) {

@@ -68,6 +68,8 @@ namespace paged {
 // were lost.
 constexpr float kRoom = 7.0f, kLazy = kRoom + 8.0f;
 
+constexpr int kMostCtas = 3;  // of an SM, in any shape: the workspace has room for their partial results
+
 template <int KB, int VB, int D>
 struct Shape {
   static constexpr bool quant = KB != 16;
@@ -75,9 +77,11 @@ struct Shape {
   // Tiles of a chunk, and CTAs per SM.  Codes: a chunk costs about 50
   // instructions beside its tiles (wait, maximum, next copy), so larger chunks
   // on 12 warps an SM beat smaller ones on 16 (K4V2, 8 x 32K tokens: 4 tiles on
-  // 3 CTAs 41.5 us, 2 on 3 45.3, 2 on 4 47.3, 4 on 2 43.6; K8V8, 32 sequences of
-  // up to 8K, window 4096: 2 tiles on 2 CTAs 29.7 us, 1 on 3 31.4).  16 bits: one
-  // tile, as many CTAs as leave a ring of three stages.
+  // 3 CTAs 48.3 us, 2 on 3 50.5, 2 on 4 53.8; K8V4, 16 x 4K: 2 tiles on 3 CTAs
+  // 21.7 us, on 2 22.5; K8V8, 32 sequences of up to 8K, window 4096: 2 tiles on 2
+  // CTAs 29.7 us, 1 on 3 32.2).  16 bits: one tile, and two CTAs, whose rings
+  // have room for three tiles (head_dim 128) or four (64: fp16, 4 x 16K tokens x
+  // 2 kv heads, 17.9 us on 2, 24.2 on 3, 27.4 on 4; 16 x 32K x 4, 66.4, 69.5, 67.7).
   static constexpr int S = !quant ? 1 : (TB > 1664 ? 2 : 4);  // tiles of a chunk
   static constexpr int stage = S * TB;
   static constexpr int W = 4;  // warps
@@ -87,7 +91,8 @@ struct Shape {
   // with 16 bits, 1.6 with K8V4, 2.9 with K4V2; 2 W was the best of 0, W, 2 W,
   // 3 W for all three: K8V4, 16 x 4K tokens, 21.7, 21.2, 20.8, 20.7 us.)
   static constexpr int E = 2 * W;
-  static constexpr int CPS = quant && TB <= 3200 ? 3 : (TB > 4096 ? 2 : 4);
+  static constexpr int CPS = quant && TB <= 3200 ? 3 : 2;
+  static_assert(CPS <= kMostCtas, "workspace");
   static constexpr int merge = (W - 1) * 32 * D;            // what each warp hands the others (D/4 fp32 a lane)
   static constexpr int queries = (quant ? 3 : 2) * 16 * D;  // rows of 8 heads (see fetch_q)
   static constexpr int extra = 1024;             // barriers, maxima and sums, q's factors, the search's sums
@@ -95,7 +100,7 @@ struct Shape {
   static constexpr int ring = ((228 / CPS - 1) * 1024 - head) / W;
   static constexpr int NST = ring / stage > 4 ? 4 : ring / stage;
   static constexpr int smem = head + W * NST * stage;
-  static_assert(NST >= 2, "ring");
+  static_assert(NST >= (quant ? 2 : 3), "ring");
 };
 
 // One partial result in the workspace: {m, l} of 8 heads, then the result in
