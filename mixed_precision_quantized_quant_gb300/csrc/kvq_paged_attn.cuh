@@ -36,18 +36,19 @@
 // sums by the exponent field, so that a sum of subnormals keeps fewer bits the
 // lower the field; fields are therefore moved to bit 4 or higher first (one
 // more shift for four codes).  At bits 0 .. 3 the scores of 4-bit keys were
-// 8.5e-6 off (rms) instead of 1.4e-6, those of 2-bit keys over 1e-5 of a short
-// sequence's, and outputs lost half the bits of fp16; the shifts cost 2 us of 42.
+// 8.5e-6 off (rms) instead of 1.4e-6, and those of 2-bit keys over 1e-5 of a
+// short sequence's; the shifts cost 2 us of 42 (with weights in one part).
 //
 // Measured (GB300, device time with the join, copy rate 6771 GB/s): 8 x 32K
-// tokens x 8 kv heads in fp16 119 us, 96% of the copy rate; K4V2 44 us, 53%;
-// 16 x 4K x 8 in bf16 38 us, 76%, K8V4 22 us, 53%; one sequence of 256 tokens
+// tokens x 8 kv heads in fp16 121 us, 95% of the copy rate; K4V2 48 us, 48%;
+// 16 x 4K x 8 in bf16 39 us, 76%, K8V4 22 us, 53%; one sequence of 256 tokens
 // 5 us.  About 9 us of each are the way to the first chunk (lengths, page
 // table, first copies: 3 dependent loads, 4.7 us), the uneven end of the CTAs
 // (2 to 4 us) and the join (3 us).  In between 16-bit rows stream at the copy
-// rate; narrow codes are bound by the ALU pipe and the issue slots (K4V2: 210
-// instructions a tile, 100 of them the masks, shifts and byte permutes that
-// make registers of two codes).
+// rate; narrow codes are bound by latency, at the 12 warps an SM that their
+// registers leave: K4V2 issues 240 instructions a tile, 100 of them the masks,
+// shifts and byte permutes that make registers of two codes, in 51% of the
+// issue slots, with the ALU pipe 41% and the tensor cores 34% busy.
 #pragma once
 
 #include <cfloat>
@@ -89,7 +90,7 @@ struct Shape {
   // What starting another unit costs a CTA (the merge, the drained pipeline), in
   // chunks: a unit counts that many more when the work is cut.  (Measured 1.2 us
   // with 16 bits, 1.6 with K8V4, 2.9 with K4V2; 2 W was the best of 0, W, 2 W,
-  // 3 W for all three: K8V4, 16 x 4K tokens, 21.7, 21.2, 20.8, 20.7 us.)
+  // 3 W for all three: K8V4, 16 x 4K tokens, then 21.7, 21.2, 20.8, 20.7 us.)
   static constexpr int E = 2 * W;
   static constexpr int CPS = quant && TB <= 3200 ? 3 : 2;
   static_assert(CPS <= kMostCtas, "workspace");
@@ -1075,10 +1076,10 @@ cudaError_t attn_as(const PagedAttnParams* pp, int sms, cudaStream_t s) {
   PagedAttnParams p = *pp;
   // Short tables are not split: a CTA for each unit, and no join.  Measured with
   // 1, 8 and 64 sequences x 8 kv heads, unsplit against split, us: fp16, 512
-  // tokens 7.0, 7.5, 26 against 7.7, 9.5, 30, 1024 tokens 10.6, 11.1, 44 against
-  // 9.6, 10.1, 50; K8V4, 512 tokens 6.5, 6.9, 17 against 7.5, 8.7, 19, 1024
-  // tokens 9.8, 10.1, 28 against 8.1, 10.3, 26; K4V2, 1024 tokens 8.1, 8.6, 21
-  // against 7.9, 9.7, 23, 2048 tokens 13.0, 13.7, 33 against 8.4, 11.8, 34.
+  // tokens 7.7, 8.0, 26 against 7.5, 9.7, 30, 1024 tokens 11.7, 12.0, 44 against
+  // 9.9, 10.5, 50; K8V4, 512 tokens 6.7, 6.9, 17 against 7.4, 9.1, 19, 1024
+  // tokens 9.9, 10.3, 28 against 7.9, 10.6, 27; K4V2, 1024 tokens 9.1, 9.6, 23
+  // against 8.2, 10.5, 25, 2048 tokens 14.7, 15.2, 38 against 8.7, 12.9, 38.
   // Otherwise one wave, or as many CTAs as the longest sequences that fit the
   // tables can fill.
   const int64_t tokens = static_cast<int64_t>(p.batch.max_pages) << p.pool.page_shift;
