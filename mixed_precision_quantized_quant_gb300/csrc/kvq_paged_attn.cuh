@@ -41,7 +41,7 @@
 //
 // Measured (GB300, device time with the join, copy rate 6771 GB/s): 8 x 32K
 // tokens x 8 kv heads in fp16 121 us, 95% of the copy rate; K4V2 48 us, 48%;
-// 16 x 4K x 8 in bf16 39 us, 76%, K8V4 22 us, 53%; one sequence of 256 tokens
+// 16 x 4K x 8 in bf16 39 us, 76%, K8V4 22 us, 52%; one sequence of 256 tokens
 // 5 us.  About 9 us of each are the way to the first chunk (lengths, page
 // table, first copies: 3 dependent loads, 4.7 us), the uneven end of the CTAs
 // (2 to 4 us) and the join (3 us).  In between 16-bit rows stream at the copy
@@ -705,7 +705,11 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
         constexpr int NW = rk / 16;  // words of a thread's part of a row
         constexpr int R = 16 / KB;   // registers of a word
         uint32_t wa[S][NW], wb[S][NW];
-        float acc[S][4] = {};
+        // Two sums for 8-bit keys: an MMA cuts each product at its sum's last bit, and theirs (19 bits) are
+        // longer than those of fewer bits.  In one sum the log-sum-exp of one token was 1.2e-6 off, in two 7e-7,
+        // as far as that of 4-bit keys in one (K8V4, 16 x 4K tokens, 22.4 instead of 22.2 us).
+        constexpr int CH = KB == 8 ? 2 : 1;
+        float acc[S][CH][4] = {};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           const uint8_t* kp = buf + s * C::TB + koff;
@@ -726,7 +730,7 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
             key_regs<KB>(wb[s][w], y);
 #pragma unroll
             for (int j = 0; j < R; j += 2)
-              mma_t<__half>(acc[s], x[j], y[j], x[j + 1], y[j + 1], qf[w * R + j], qf[w * R + j + 1]);
+              mma_t<__half>(acc[s][w % CH], x[j], y[j], x[j + 1], y[j + 1], qf[w * R + j], qf[w * R + j + 1]);
           }
 #pragma unroll
         for (int s = 0; s < S; ++s)
@@ -738,7 +742,9 @@ __global__ void __launch_bounds__(Shape<KB, VB, D>::threads, Shape<KB, VB, D>::C
             vz[s][i] = __high2float(u32_as_h2(raw.y));
 #pragma unroll
             for (int hd = 0; hd < 2; ++hd)
-              sc[s][2 * i + hd] = fmaf(ks * fac[hd], acc[s][2 * i + hd], kz * qs[hd]);
+              sc[s][2 * i + hd] =
+                  fmaf(ks * fac[hd], CH == 1 ? acc[s][0][2 * i + hd] : acc[s][0][2 * i + hd] + acc[s][CH - 1][2 * i + hd],
+                       kz * qs[hd]);
           }
         if (edge) {  // rows outside [first, len) may hold anything
           const int lo = cs.first - base - tile_row_token(g), hi = cs.len - base - tile_row_token(g);

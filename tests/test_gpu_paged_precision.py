@@ -153,3 +153,34 @@ def test_queries_below_fp16_steps(kb, below, d, width):
     o, tol, l, ltol, keys, value = _wide_queries(kb, below, d, width, lambda g, s: torch.randn(s, generator=g).clamp(-3, 3))
     r = 2.0 ** (-36 if kb == 2 else -40) * keys
     assert (l <= ltol + r).all() and (o <= tol + 3 * r * value).all() and r < 1e-2
+
+
+@pytest.mark.parametrize("width", [None, 100])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_score_of_8_bit_keys(d, width):
+    # One token a sequence, whose score is the log-sum-exp, with strong channels, so that the codes' part s q.c is
+    # R times the score and the zeros' part takes most of it off.  An MMA cuts 2^-24 of its sum off each product, in
+    # [0, 1) of that and of either sign: over d products in two chains of d / 2, whose sums are half of s q.c
+    # at the end and a quarter on the way, sqrt(d / 3) 2^-24 R / 4 of the score in the 2-norm; the zeros' part, its
+    # factor and the scale round by 2^-24 R / 3 each.  One chain has twice the first part.
+    S, g = 24, torch.Generator().manual_seed(9)
+    c = Case([1] * S, kb=8, vb=8, d=d, hq=32, hkv=8, fill=False, width=width)
+    mu, sigma, strong = torch.randn(8, d, generator=g) * 0.5, torch.exp(torch.randn(8, d, generator=g) * 0.5), torch.ones(8, d)
+    for h in range(8):
+        strong[h, torch.randperm(d, generator=g)[:4]] = 10.0
+    for b in range(S):
+        for h in range(8):
+            c.model.put(c.table[b, 0], 0, h, False, ((mu[h] + sigma[h] * torch.randn(d, generator=g)) * strong[h]).half().float())
+            c.model.put(c.table[b, 0], 0, h, True, torch.randn(d, generator=g).half().float())
+    c.upload()
+    q = c.rows(S, 32)
+    _, lse = c.cache.decode_attn(0, c.batch, q, return_lse=True)
+    score, codes = np.zeros((S, 32)), np.zeros((S, 32))
+    for b in range(S):
+        for h in range(8):
+            k, kc, _ = c.model.rows(c.table[b], 0, 1, h, False)
+            x = q[b, 4 * h:4 * h + 4].double().cpu().numpy() / math.sqrt(d)
+            score[b, 4 * h:4 * h + 4], codes[b, 4 * h:4 * h + 4] = x @ k[0], x @ kc[0]
+    R = np.linalg.norm(codes) / np.linalg.norm(score)
+    off = np.linalg.norm(lse.double().cpu().numpy() - score) / np.linalg.norm(score)
+    assert off <= 2.0 ** -24 * R * math.sqrt(d / 48 + 1 / 3), (off, R)
