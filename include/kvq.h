@@ -470,6 +470,32 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
                             const kvq_rows* V, const kvq_rows* q, const kvq_rows* q_out,
                             const kvq_rotation* rotation, int n_tokens, void* stream);
 
+/* A norm of every query and key head: the head's channels x_c become
+ * x_c * (1 / sqrt(mean of x_c^2 + eps)) * weight_c, in fp32.
+ *   q_weight, k_weight: device, the cache's type, 16-byte aligned; head h's
+ *     head_dim weights start at weight + h * stride elements, a multiple of 8
+ *     (0: one set for all heads).  NULL: all ones.
+ *   eps: finite, not negative (a head of zeros with eps 0 becomes NaN). */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  int64_t q_stride;
+  int64_t k_stride;
+  float eps;
+} kvq_head_norm;
+
+/* kvq_paged_append with `norm` (NULL: none) applied to queries and keys before
+ * their rotation, all in fp32 and rounded once; the values are taken as they
+ * are.  k_out: [n_tokens][num_kv_heads] rows or NULL, written with the keys as
+ * they are before they are stored (normed and turned, rounded to the cache's
+ * type, not quantized), as kvq_paged_prompt_attn takes them; k_out may be K
+ * itself, and overlaps nothing else, nor its rows one another.
+ * KVQ_ERR_ARG for an eps that is negative or not finite, or a stride that is
+ * no multiple of 8, KVQ_ERR_ALIGN for weights off 16 bytes. */
+kvq_status kvq_paged_append_norm(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K,
+                                 const kvq_rows* V, const kvq_rows* q, const kvq_rows* q_out, const kvq_rows* k_out,
+                                 const kvq_head_norm* norm, const kvq_rotation* rotation, int n_tokens, void* stream);
+
 /* Attention of one query token per sequence, the newest one, over its pages:
  * positions max(0, len - window) .. len - 1 (window 0: all of them).
  *   q: [num_seqs][num_q_heads] rows (cu_tokens is not looked at).
@@ -492,6 +518,48 @@ kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch*
 
 /* Bytes of the workspace above (0 if h is null or num_seqs < 1). */
 size_t kvq_paged_workspace_bytes(const kvq_paged* h, int num_seqs);
+
+/* Attention of the newest tokens of every sequence over its pages, causal:
+ * prompts taken in pieces, reused prefixes, drafted tokens to check.  Row i of
+ * sequence s (rows and cu_tokens as for an append, which comes first: seq_lens
+ * counts the rows) is the token at position p = seq_lens[s] - (its rows) + i
+ * and attends positions max(0, p - window + 1) .. p (window 0: 0 .. p).
+ *   q: [n_tokens][num_q_heads] rows.
+ *   out: [n_tokens][num_q_heads][head_dim] contiguous, 16-byte aligned, the
+ *     cache's type, overlapping no other argument.
+ *   lse: fp32 [n_tokens][num_q_heads] or NULL, as for kvq_paged_decode_attn.
+ *   scale: multiplies the scores; 0 means 1 / sqrt(head_dim).
+ *   n_tokens: rows of the tensors; without cu_tokens, equal to num_seqs.
+ *   workspace: device scratch of kvq_paged_chunk_workspace_bytes(h, num_seqs,
+ *     n_tokens) bytes, 256-byte aligned, whatever it holds; not shared with a
+ *     call in flight.
+ * A row with no score above -infinity gets 0, and -infinity.  Rows that belong
+ * to no sequence are not written, nor those of a sequence with fewer tokens
+ * than rows or more than its table holds.  What a row may not see does not
+ * reach it, whatever it holds; a NaN or an infinite value that it sees leaves
+ * NaN or infinity where it counts.
+ * KVQ_ERR_ARG for a negative window or a scale as kvq_paged_decode_attn
+ * refuses it; KVQ_ERR_CAPACITY for a small workspace; KVQ_ERR_UNSUPPORTED where
+ * the rows could make more than 2^31 - 1 tiles of queries, or n_tokens *
+ * num_q_heads is past 2^40. */
+kvq_status kvq_paged_chunk_attn(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* q, void* out,
+                                float* lse, float scale, int window, int n_tokens, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Attention of whole prompts over their own rows, causal, without the pages:
+ * the rows of sequence s (cu_tokens as for an append; the batch's table and
+ * lengths are not looked at) attend one another, row i the rows
+ * max(0, i - window + 1) .. i.  A quantized layer's prompt attends exact keys
+ * and values this way, as they were before they were stored (k_out of
+ * kvq_paged_append_norm); the cache's precision counts from the next token on.
+ * K, V: [n_tokens][num_kv_heads] rows; all else as for kvq_paged_chunk_attn. */
+kvq_status kvq_paged_prompt_attn(kvq_paged* h, const kvq_paged_batch* batch, const kvq_rows* q, const kvq_rows* K,
+                                 const kvq_rows* V, void* out, float* lse, float scale, int window, int n_tokens,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of the workspace of the two above (0 if h is null, num_seqs < 1 or
+ * n_tokens < 0). */
+size_t kvq_paged_chunk_workspace_bytes(const kvq_paged* h, int num_seqs, int n_tokens);
 
 /* Reads the newest rows of every sequence (cu_tokens as for an append) back as
  * the cache holds them: code * scale + zero in fp32, rounded once to the

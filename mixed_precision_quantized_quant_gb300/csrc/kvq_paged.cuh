@@ -55,6 +55,11 @@ struct PagedAppendParams {
   int n, hq, hkv;         // hq = 0: no queries
   int vec;                // every row is 16-byte aligned
   int tokens;             // tokens of a CTA (set at launch)
+  // of an append with a norm or with keys out, a kernel of its own
+  PagedRows ko;           // data null: none
+  const uint8_t *wq, *wk; // null: all ones
+  int64_t wq_stride, wk_stride;  // bytes between heads' weights
+  float eps;              // negative: no norm
 };
 
 struct PagedReadParams {
@@ -81,6 +86,22 @@ struct PagedAttnParams {
   const uint8_t* ws_hi;   // end of the workspace (checked in debug builds)
   int solo;               // a CTA for each unit, no join (set at launch)
   int ctas;               // of the attention kernel (set at launch)
+};
+
+// Attention of runs of new tokens: over the pages, or over rows of their own.
+struct PagedChunkParams {
+  PagedBatch batch;
+  PagedPool pool;         // for prompts only its error word
+  PagedRows q, k, v;      // k, v: of prompts
+  void* out;              // [n][hq][D]
+  float* lse;             // [n][hq] or null
+  float alpha;            // scale * log2(e)
+  int window;             // 0: all
+  int n, hkv, gqa;
+  int q_vec, kv_vec;      // every row of q / of k and v is 16-byte aligned
+  int prompt;
+  uint8_t* ws;
+  const uint8_t* ws_hi;   // end of the workspace (checked in debug builds)
 };
 
 // ---------------------------------------------------------------- debug checks
@@ -145,5 +166,7 @@ cudaError_t paged_read_launch(const PagedReadParams& p, int D, int dtype, int sm
 cudaError_t paged_attn_prepare(int kb, int vb, int D, int dtype);
 cudaError_t paged_attn_launch(PagedAttnParams p, int D, int dtype, int sms, cudaStream_t s);
 size_t paged_attn_workspace(int D, int hkv, int seqs, int sms);
+cudaError_t paged_chunk_launch(const PagedChunkParams& p, int D, int dtype, int sms, cudaStream_t s);
+size_t paged_chunk_workspace(int D, int hkv, int gqa, int seqs, int n, int sms);
 
 }  // namespace kvq

@@ -139,6 +139,98 @@ kvq_status take_rows(const kvq_rows* r, int n, int heads, int d, kvq::PagedRows*
   return KVQ_OK;
 }
 
+// An append, with a norm and keys out where they are given.
+kvq_status append(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K, const kvq_rows* V,
+                  const kvq_rows* q, const kvq_rows* q_out, const kvq_rows* k_out, const kvq_head_norm* norm,
+                  const kvq_rotation* rotation, int n_tokens, void* stream) {
+  kvq::PagedAppendParams p = {};
+  kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
+  if (st != KVQ_OK) return st;
+  if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!q != !q_out)) return KVQ_ERR_ARG;
+  if (n_tokens == 0) return KVQ_OK;
+  p.vec = 1;
+  const int hq = h->cfg.num_q_heads, hkv = h->cfg.num_kv_heads, d = h->cfg.head_dim;
+  if ((st = take_rows(K, n_tokens, hkv, d, &p.k, &p.vec)) != KVQ_OK ||
+      (st = take_rows(V, n_tokens, hkv, d, &p.v, &p.vec)) != KVQ_OK)
+    return st;
+  if (q && ((st = take_rows(q, n_tokens, hq, d, &p.q, &p.vec)) != KVQ_OK ||
+            (st = take_rows(q_out, n_tokens, hq, d, &p.qo, &p.vec)) != KVQ_OK))
+    return st;
+  if (rotation) {
+    if (!rotation->table || rotation->rows < 1 || rotation->dim < 16 || rotation->dim % 16 != 0 ||
+        rotation->dim > h->cfg.head_dim || (rotation->interleaved != 0 && rotation->interleaved != 1))
+      return KVQ_ERR_ARG;
+    if (!aligned16(rotation->table)) return KVQ_ERR_ALIGN;
+    p.rope = rotation->table;
+    p.positions = rotation->positions;
+    p.rope_rows = rotation->rows;
+    p.rope_dim = rotation->dim;
+    p.interleaved = rotation->interleaved;
+  }
+  if (k_out && (st = take_rows(k_out, n_tokens, hkv, d, &p.ko, &p.vec)) != KVQ_OK) return st;
+  p.eps = -1.0f;
+  if (norm) {
+    if (!std::isfinite(norm->eps) || norm->eps < 0.0f || norm->q_stride % 8 != 0 || norm->k_stride % 8 != 0)
+      return KVQ_ERR_ARG;
+    if (!aligned16(norm->q_weight) || !aligned16(norm->k_weight)) return KVQ_ERR_ALIGN;
+    p.wq = static_cast<const uint8_t*>(norm->q_weight);
+    p.wk = static_cast<const uint8_t*>(norm->k_weight);
+    p.wq_stride = 2 * norm->q_stride;
+    p.wk_stride = 2 * norm->k_stride;
+    p.eps = norm->eps;
+  }
+  p.n = n_tokens;
+  p.hq = q ? hq : 0;
+  p.hkv = hkv;
+  return kvq::paged_append_launch(p, d, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KVQ_OK
+             : KVQ_ERR_CUDA;
+}
+
+
+// Attention of runs of new tokens: over `layer`'s pages, or where K and V are
+// given over rows of their own.
+kvq_status attend(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* q, const kvq_rows* K,
+                  const kvq_rows* V, bool prompt, void* out, float* lse, float scale, int window, int n_tokens,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  kvq::PagedChunkParams p = {};
+  kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
+  if (st != KVQ_OK) return st;
+  if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs)) return KVQ_ERR_ARG;
+  if (window < 0 || !std::isfinite(scale)) return KVQ_ERR_ARG;
+  const int hq = h->cfg.num_q_heads, hkv = h->cfg.num_kv_heads, d = h->cfg.head_dim;
+  const double sc = scale == 0.0f ? 1.0 / std::sqrt(static_cast<double>(d)) : scale;
+  p.alpha = static_cast<float>(sc * 1.4426950408889634);
+  if (!std::isfinite(p.alpha)) return KVQ_ERR_ARG;  // scores are taken in base 2
+  if (n_tokens == 0) return KVQ_OK;
+  p.q_vec = p.kv_vec = 1;
+  if ((st = take_rows(q, n_tokens, hq, d, &p.q, &p.q_vec)) != KVQ_OK) return st;
+  if (prompt && ((st = take_rows(K, n_tokens, hkv, d, &p.k, &p.kv_vec)) != KVQ_OK ||
+                 (st = take_rows(V, n_tokens, hkv, d, &p.v, &p.kv_vec)) != KVQ_OK))
+    return st;
+  if (!out || !workspace) return KVQ_ERR_ARG;
+  if (!aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
+    return KVQ_ERR_ALIGN;
+  if (workspace_bytes < kvq_paged_chunk_workspace_bytes(h, batch->num_seqs, n_tokens)) return KVQ_ERR_CAPACITY;
+  // tiles of queries are counted in 32 bits
+  if (static_cast<int64_t>(n_tokens) * hq > int64_t{1} << 40 ||
+      (static_cast<int64_t>(n_tokens) * (hq / hkv) / 128 + batch->num_seqs) > INT_MAX / hkv)
+    return KVQ_ERR_UNSUPPORTED;
+  p.out = out;
+  p.lse = lse;
+  p.window = window;
+  p.n = n_tokens;
+  p.hkv = hkv;
+  p.gqa = hq / hkv;
+  p.prompt = prompt;
+  p.ws = static_cast<uint8_t*>(workspace);
+  p.ws_hi = p.ws + workspace_bytes;
+  return kvq::paged_chunk_launch(p, d, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KVQ_OK
+             : KVQ_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -192,36 +284,14 @@ kvq_status kvq_paged_append(kvq_paged* h, int layer, const kvq_paged_batch* batc
                             const kvq_rows* V, const kvq_rows* q, const kvq_rows* q_out,
                             const kvq_rotation* rotation, int n_tokens, void* stream) {
   Trace trace("kvq_paged_append");
-  kvq::PagedAppendParams p = {};
-  kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
-  if (st != KVQ_OK) return st;
-  if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs) || (!q != !q_out)) return KVQ_ERR_ARG;
-  if (n_tokens == 0) return KVQ_OK;
-  p.vec = 1;
-  const int hq = h->cfg.num_q_heads, hkv = h->cfg.num_kv_heads, d = h->cfg.head_dim;
-  if ((st = take_rows(K, n_tokens, hkv, d, &p.k, &p.vec)) != KVQ_OK ||
-      (st = take_rows(V, n_tokens, hkv, d, &p.v, &p.vec)) != KVQ_OK)
-    return st;
-  if (q && ((st = take_rows(q, n_tokens, hq, d, &p.q, &p.vec)) != KVQ_OK ||
-            (st = take_rows(q_out, n_tokens, hq, d, &p.qo, &p.vec)) != KVQ_OK))
-    return st;
-  if (rotation) {
-    if (!rotation->table || rotation->rows < 1 || rotation->dim < 16 || rotation->dim % 16 != 0 ||
-        rotation->dim > h->cfg.head_dim || (rotation->interleaved != 0 && rotation->interleaved != 1))
-      return KVQ_ERR_ARG;
-    if (!aligned16(rotation->table)) return KVQ_ERR_ALIGN;
-    p.rope = rotation->table;
-    p.positions = rotation->positions;
-    p.rope_rows = rotation->rows;
-    p.rope_dim = rotation->dim;
-    p.interleaved = rotation->interleaved;
-  }
-  p.n = n_tokens;
-  p.hq = q ? hq : 0;
-  p.hkv = hkv;
-  return kvq::paged_append_launch(p, d, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? KVQ_OK
-             : KVQ_ERR_CUDA;
+  return append(h, layer, batch, K, V, q, q_out, nullptr, nullptr, rotation, n_tokens, stream);
+}
+
+kvq_status kvq_paged_append_norm(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K,
+                                 const kvq_rows* V, const kvq_rows* q, const kvq_rows* q_out, const kvq_rows* k_out,
+                                 const kvq_head_norm* norm, const kvq_rotation* rotation, int n_tokens, void* stream) {
+  Trace trace("kvq_paged_append_norm");
+  return append(h, layer, batch, K, V, q, q_out, k_out, norm, rotation, n_tokens, stream);
 }
 
 size_t kvq_paged_workspace_bytes(const kvq_paged* h, int num_seqs) {
@@ -262,6 +332,27 @@ kvq_status kvq_paged_decode_attn(kvq_paged* h, int layer, const kvq_paged_batch*
                  cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_paged_chunk_attn(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* q, void* out,
+                                float* lse, float scale, int window, int n_tokens, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  Trace trace("kvq_paged_chunk_attn");
+  return attend(h, layer, batch, q, nullptr, nullptr, false, out, lse, scale, window, n_tokens, workspace,
+                workspace_bytes, stream);
+}
+
+kvq_status kvq_paged_prompt_attn(kvq_paged* h, const kvq_paged_batch* batch, const kvq_rows* q, const kvq_rows* K,
+                                 const kvq_rows* V, void* out, float* lse, float scale, int window, int n_tokens,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  Trace trace("kvq_paged_prompt_attn");
+  return attend(h, 0, batch, q, K, V, true, out, lse, scale, window, n_tokens, workspace, workspace_bytes, stream);
+}
+
+size_t kvq_paged_chunk_workspace_bytes(const kvq_paged* h, int num_seqs, int n_tokens) {
+  if (!h || num_seqs < 1 || n_tokens < 0) return 0;
+  return kvq::paged_chunk_workspace(h->cfg.head_dim, h->cfg.num_kv_heads, h->cfg.num_q_heads / h->cfg.num_kv_heads,
+                                    num_seqs, n_tokens, h->sms);
 }
 
 kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K, const kvq_rows* V,

@@ -48,8 +48,9 @@ struct AppendSmem {
   float angles[kRowTokens][128];                // the tokens' cosines and sines
 };
 
-// What is done with a row once its two chunks are in registers.
-template <typename T, int D, bool QUANT>
+// What is done with a row once its two chunks are in registers.  MORE: a norm
+// before the rotation, and keys written out, each where the call has it.
+template <typename T, int D, bool QUANT, bool MORE>
 struct RowWork {
   static constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes of a row, rows of a group
   const PagedAppendParams& p;
@@ -81,9 +82,13 @@ struct RowWork {
   __device__ __forceinline__ void one(int row, int head, const RowPlace& pl, const float* angles, uint4 a, uint4 b) const {
     f2 f[2][4];
     const bool turned = KIND != kValues && turns;
-    if (turned || (QUANT && KIND != kQueries)) {
+    const bool normed = MORE && KIND != kValues && p.eps >= 0.0f;
+    if (turned || normed || (QUANT && KIND != kQueries)) {
       unpack8<T>(a, f[0]);
       unpack8<T>(b, f[1]);
+    }
+    if constexpr (MORE && KIND != kValues) {
+      if (normed) norm<KIND>(f, head);
     }
     if (turned) {
       // angles of the half-split pairs, or of the lane's two chunks
@@ -107,9 +112,19 @@ struct RowWork {
             turn_within(f[h][i], c[i % 2], s[i % 2]);
           }
       }
-      if (!QUANT || KIND == kQueries) {
-        a = pack8<T>(f[0]);
-        b = pack8<T>(f[1]);
+    }
+    // (keys of a quantized layer are rounded for k_out alone)
+    if ((turned || normed) && (!QUANT || KIND == kQueries || (MORE && p.ko.data))) {
+      a = pack8<T>(f[0]);
+      b = pack8<T>(f[1]);
+    }
+    if constexpr (MORE && KIND == kKeys) {
+      if (p.ko.data && head < p.hkv) {
+        T* y = reinterpret_cast<T*>(p.ko.data) + row * p.ko.token_stride + head * p.ko.head_stride;
+        if (rows_ok(p.ko, y, 2 * D, p.pool.err)) {
+          store8(y + 8 * c0, p.vec, a);
+          store8(y + 8 * c1, p.vec, b);
+        }
       }
     }
     bool live = head < heads<KIND>();
@@ -134,6 +149,36 @@ struct RowWork {
       }
     } else {
       quantize<KIND>(f, head, live, pl);
+    }
+  }
+
+  // The row over the root of its mean square, times the head's weights.
+  template <int KIND>
+  __device__ __forceinline__ void norm(f2 (&f)[2][4], int head) const {
+    f2 sum = f2_of(0.0f, 0.0f);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum = fma2(f[x][i], f[x][i], sum);
+    float s0, s1;
+    f2_get(sum, s0, s1);
+    s0 += s1;
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    const float r = rsqrtf(fmaf(s0, 1.0f / D, p.eps));
+    const f2 r2 = f2_of(r, r);
+    const uint8_t* w = KIND == kQueries ? p.wq : p.wk;
+    const bool weighed = w != nullptr && head < heads<KIND>();
+    if (weighed) w += head * (KIND == kQueries ? p.wq_stride : p.wk_stride);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      f2 g[4];
+      if (weighed) unpack8<T>(__ldg(reinterpret_cast<const uint4*>(w) + (x ? c1 : c0)), g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[x][i] = mul2(f[x][i], r2);
+        if (weighed) f[x][i] = mul2(f[x][i], g[i]);
+      }
     }
   }
 
@@ -189,9 +234,9 @@ struct RowWork {
 };
 
 // Streams a warp's pairs: their rows are fetched kDepth pairs ahead.
-template <typename T, int D, bool QUANT>
+template <typename T, int D, bool QUANT, bool MORE>
 struct Appender {
-  using W = RowWork<T, D, QUANT>;
+  using W = RowWork<T, D, QUANT, MORE>;
   const W& w;
   AppendSmem& sm;
   int row0, count, lane, warp;
@@ -248,7 +293,7 @@ struct Appender {
 };
 
 // Many tokens: a CTA takes up to 32.
-template <typename T, int D, bool QUANT>
+template <typename T, int D, bool QUANT, bool MORE>
 __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   __shared__ __align__(16) AppendSmem sm;
   grid_dep_wait();
@@ -256,8 +301,8 @@ __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) paged_append_kernel
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row0 = blockIdx.x * p.tokens;  // (n is at most INT_MAX - 31)
   const int count = p.n - row0 < p.tokens ? p.n - row0 : p.tokens;
-  const RowWork<T, D, QUANT> work(p, lane);
-  Appender<T, D, QUANT> ap = {work, sm, row0, count, lane, warp, kQueries, Run(0, 1, 0)};
+  const RowWork<T, D, QUANT, MORE> work(p, lane);
+  Appender<T, D, QUANT, MORE> ap = {work, sm, row0, count, lane, warp, kQueries, Run(0, 1, 0)};
   ap.ahead = ap.run(kQueries);
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) ap.fetch(i);  // under way while the places are found
@@ -288,9 +333,9 @@ __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) paged_append_kernel
 // 256 rows 4.5 and 5.0, 456 rows 4.6 and 5.1, 912 rows 8.2 and 6.2; codes (K4V2,
 // with the read back): 1 row 4.8 and 6.2, 256 rows 7.5 and 9.1, 456 rows 10.6
 // and 9.3.
-template <typename T, int D, bool QUANT>
+template <typename T, int D, bool QUANT, bool MORE>
 __global__ void __launch_bounds__(1024) paged_append_few_kernel(const __grid_constant__ PagedAppendParams p) {
-  using W = RowWork<T, D, QUANT>;
+  using W = RowWork<T, D, QUANT, MORE>;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, row = blockIdx.x;
@@ -330,7 +375,7 @@ __global__ void __launch_bounds__(1024) paged_append_few_kernel(const __grid_con
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool MORE>
 cudaError_t append_as(PagedAppendParams p, int sms, cudaStream_t s) {
   p.tokens = cta_tokens(p.n, sms, kAppendPerSm);
   const dim3 grid(static_cast<unsigned>((p.n - 1) / p.tokens + 1));
@@ -338,18 +383,23 @@ cudaError_t append_as(PagedAppendParams p, int sms, cudaStream_t s) {
     constexpr int RPW = 32 / (D / 16);
     const int groups = (p.hq + RPW - 1) / RPW + 2 * ((p.hkv + RPW - 1) / RPW);
     const int threads = groups < 32 ? 32 * groups : 1024;
-    return p.pool.kb == 16 ? launch_pdl(paged_append_few_kernel<T, D, false>, p, grid, threads, s)
-                           : launch_pdl(paged_append_few_kernel<T, D, true>, p, grid, threads, s);
+    return p.pool.kb == 16 ? launch_pdl(paged_append_few_kernel<T, D, false, MORE>, p, grid, threads, s)
+                           : launch_pdl(paged_append_few_kernel<T, D, true, MORE>, p, grid, threads, s);
   }
-  return p.pool.kb == 16 ? launch_pdl(paged_append_kernel<T, D, false>, p, grid, kRowThreads, s)
-                         : launch_pdl(paged_append_kernel<T, D, true>, p, grid, kRowThreads, s);
+  return p.pool.kb == 16 ? launch_pdl(paged_append_kernel<T, D, false, MORE>, p, grid, kRowThreads, s)
+                         : launch_pdl(paged_append_kernel<T, D, true, MORE>, p, grid, kRowThreads, s);
 }
 
 }  // namespace
 
 cudaError_t paged_append_launch(const PagedAppendParams& p, int D, int dtype, int sms, cudaStream_t s) {
-  if (dtype == 0) return D == 64 ? append_as<__half, 64>(p, sms, s) : append_as<__half, 128>(p, sms, s);
-  return D == 64 ? append_as<__nv_bfloat16, 64>(p, sms, s) : append_as<__nv_bfloat16, 128>(p, sms, s);
+  const bool more = p.eps >= 0.0f || p.ko.data;
+  if (dtype == 0) {
+    if (more) return D == 64 ? append_as<__half, 64, true>(p, sms, s) : append_as<__half, 128, true>(p, sms, s);
+    return D == 64 ? append_as<__half, 64, false>(p, sms, s) : append_as<__half, 128, false>(p, sms, s);
+  }
+  if (more) return D == 64 ? append_as<__nv_bfloat16, 64, true>(p, sms, s) : append_as<__nv_bfloat16, 128, true>(p, sms, s);
+  return D == 64 ? append_as<__nv_bfloat16, 64, false>(p, sms, s) : append_as<__nv_bfloat16, 128, false>(p, sms, s);
 }
 
 }  // namespace kvq

@@ -30,6 +30,7 @@ EXPORTS = (
     "kvq_state_restore",
     "kvq_paged_bytes", "kvq_paged_create", "kvq_paged_append", "kvq_paged_decode_attn", "kvq_paged_workspace_bytes",
     "kvq_paged_read", "kvq_paged_view_get", "kvq_paged_device_error", "kvq_paged_destroy",
+    "kvq_paged_append_norm", "kvq_paged_chunk_attn", "kvq_paged_prompt_attn", "kvq_paged_chunk_workspace_bytes",
 )
 
 
@@ -68,6 +69,7 @@ class LayerView(ctypes.Structure):
 
 KVQ_FP16, KVQ_BF16 = 0, 1
 _FLT_MIN = 2.0 ** -126
+_FLT_MAX = (2.0 - 2.0 ** -23) * 2.0 ** 127
 
 
 class PagedLayerCfg(ctypes.Structure):
@@ -94,6 +96,11 @@ class PagedBatchArgs(ctypes.Structure):
 class RotationArgs(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rows", ctypes.c_int32),
                 ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class HeadNormArgs(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("eps", ctypes.c_float)]
 
 
 class Rows(ctypes.Structure):
@@ -170,6 +177,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.kvq_paged_device_error.restype = ctypes.c_int
     L.kvq_paged_destroy.argtypes = [vp]
     L.kvq_paged_destroy.restype = ctypes.c_int
+    L.kvq_paged_append_norm.argtypes = [vp, ctypes.c_int, batch, rows, rows, rows, rows, rows,
+                                        ctypes.POINTER(HeadNormArgs), ctypes.POINTER(RotationArgs), ctypes.c_int, vp]
+    L.kvq_paged_append_norm.restype = ctypes.c_int
+    L.kvq_paged_chunk_attn.argtypes = [vp, ctypes.c_int, batch, rows, vp, vp, ctypes.c_float, ctypes.c_int,
+                                       ctypes.c_int, vp, ctypes.c_size_t, vp]
+    L.kvq_paged_chunk_attn.restype = ctypes.c_int
+    L.kvq_paged_prompt_attn.argtypes = [vp, batch, rows, rows, rows, vp, vp, ctypes.c_float, ctypes.c_int,
+                                        ctypes.c_int, vp, ctypes.c_size_t, vp]
+    L.kvq_paged_prompt_attn.restype = ctypes.c_int
+    L.kvq_paged_chunk_workspace_bytes.argtypes = [vp, ctypes.c_int, ctypes.c_int]
+    L.kvq_paged_chunk_workspace_bytes.restype = ctypes.c_size_t
     _lib = L
     return L
 
@@ -311,6 +329,31 @@ def kvq_paged_decode_attn(h: int, layer: int, batch: PagedBatchArgs, q: Rows, ou
                           scale: float, window: int, workspace: int, workspace_bytes: int, stream: int) -> None:
     _check(load().kvq_paged_decode_attn(h, layer, batch, q, out, lse, scale, window, workspace, workspace_bytes,
                                         stream), "kvq_paged_decode_attn")
+
+
+def kvq_paged_append_norm(h: int, layer: int, batch: PagedBatchArgs, K: Rows, V: Rows, q: Optional[Rows],
+                          q_out: Optional[Rows], k_out: Optional[Rows], norm: Optional[HeadNormArgs],
+                          rotation: Optional[RotationArgs], n_tokens: int, stream: int) -> None:
+    _check(load().kvq_paged_append_norm(h, layer, batch, K, V, q, q_out, k_out, norm, rotation, n_tokens, stream),
+           "kvq_paged_append_norm")
+
+
+def kvq_paged_chunk_attn(h: int, layer: int, batch: PagedBatchArgs, q: Rows, out: int, lse: Optional[int],
+                         scale: float, window: int, n_tokens: int, workspace: int, workspace_bytes: int,
+                         stream: int) -> None:
+    _check(load().kvq_paged_chunk_attn(h, layer, batch, q, out, lse, scale, window, n_tokens, workspace,
+                                       workspace_bytes, stream), "kvq_paged_chunk_attn")
+
+
+def kvq_paged_prompt_attn(h: int, batch: PagedBatchArgs, q: Rows, K: Rows, V: Rows, out: int, lse: Optional[int],
+                          scale: float, window: int, n_tokens: int, workspace: int, workspace_bytes: int,
+                          stream: int) -> None:
+    _check(load().kvq_paged_prompt_attn(h, batch, q, K, V, out, lse, scale, window, n_tokens, workspace,
+                                        workspace_bytes, stream), "kvq_paged_prompt_attn")
+
+
+def kvq_paged_chunk_workspace_bytes(h: int, num_seqs: int, n_tokens: int) -> int:
+    return int(load().kvq_paged_chunk_workspace_bytes(h, num_seqs, n_tokens))
 
 
 def kvq_paged_workspace_bytes(h: int, num_seqs: int) -> int:
@@ -536,6 +579,41 @@ class Rotation:
                                  int(bool(interleaved)))
 
 
+class HeadNorm:
+    """The norm that an append gives every query and key head before its
+    rotation: x / sqrt(mean(x^2) + eps) * weight over the head's channels, in
+    fp32.  q_weight, k_weight: [head_dim] for all heads, or [heads, head_dim],
+    on the GPU in the cache's dtype, 16-byte aligned; None: all ones."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6):
+        if not 0.0 <= eps <= _FLT_MAX:
+            raise ValueError(f"eps must be finite and not negative, got {eps}")
+        self.weights = (q_weight, k_weight)
+        ptr, stride = [None, None], [0, 0]
+        for i, (w, name) in enumerate(zip(self.weights, ("q_weight", "k_weight"))):
+            if w is None:
+                continue
+            if w.device.type != "cuda":
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if w.dim() not in (1, 2) or w.stride(-1) != 1:
+                raise ValueError(f"{name} must be [head_dim] or [heads, head_dim] with contiguous channels")
+            ptr[i] = w.data_ptr()
+            if w.dim() == 2:
+                stride[i] = w.stride(0)
+            if ptr[i] % 16 or stride[i] % 8:
+                raise ValueError(f"{name}'s heads must be 16-byte aligned")
+        self.args = HeadNormArgs(ptr[0], ptr[1], stride[0], stride[1], eps)
+
+    def _check(self, device, dtype, hq: int, hkv: int, d: int) -> None:
+        for w, name, heads in zip(self.weights, ("q_weight", "k_weight"), (hq, hkv)):
+            if w is None:
+                continue
+            if w.dtype != dtype or w.device != device:
+                raise ValueError(f"{name} must be {dtype} on {device}, got {w.dtype} on {w.device}")
+            if tuple(w.shape) not in ((d,), (heads, d)):
+                raise ValueError(f"{name} has shape {tuple(w.shape)}, expected {(d,)} or {(heads, d)}")
+
+
 def rotation_table(rows: int, dim: int, base: float = 10000.0, device="cuda"):
     """Cosines and sines of p * base^(-2i/dim) for positions p < rows, in the
     form ``Rotation`` takes; the angles are formed in 64 bits (far positions
@@ -579,11 +657,13 @@ class KVQPagedCache:
             # the library writes its own bytes with the device idle behind it
             torch.cuda.current_stream().synchronize()
             self.h = kvq_paged_create(self.cfg, int(buffer.data_ptr()), buffer.numel())
-        self._ws = {}  # num_seqs -> workspace bytes
+        self._ws = {}  # num_seqs, or (num_seqs, rows) -> workspace bytes
         # a decode step makes two of these calls for every layer, so what a
         # call looks up is kept here
         lib = load()
         self._c_append, self._c_attn, self._c_read = lib.kvq_paged_append, lib.kvq_paged_decode_attn, lib.kvq_paged_read
+        self._c_norm, self._c_chunk, self._c_prompt = (lib.kvq_paged_append_norm, lib.kvq_paged_chunk_attn,
+                                                       lib.kvq_paged_prompt_attn)
         self._empty, self._f32, self._u8 = torch.empty, torch.float32, torch.uint8
         self._raw_stream, self._index = torch._C._cuda_getCurrentRawStream, self.device.index
         self._current_device, self._device_guard = torch._C._cuda_getDevice, torch.cuda.device
@@ -633,11 +713,13 @@ class KVQPagedCache:
             return fn(*args)
 
     def append(self, layer: int, batch: PagedBatch, K, V, q=None, rotation: Optional[Rotation] = None, q_out=None,
-               stream=None):
+               stream=None, norm: Optional[HeadNorm] = None, k_out=None):
         """Appends the newest rows of every sequence: K, V [n, Hkv, d]; returns
         q [n, Hq, d] turned by ``rotation`` (into ``q_out``, which may be q), or
-        None without q.  Rows of q_out that belong to no sequence are not
-        written."""
+        None without q.  ``norm`` is applied to queries and keys before they are
+        turned.  ``k_out`` [n, Hkv, d], which may be K, gets the keys as they
+        are before they are stored: what ``prompt_attn`` takes.  Rows of q_out
+        and k_out that belong to no sequence are not written."""
         n = K.shape[0]
         self._counts(layer, n, "kvq_paged_append")
         k, v = self._rows(K, "K", n, self.Hkv), self._rows(V, "V", n, self.Hkv)
@@ -658,8 +740,15 @@ class KVQPagedCache:
             qo = self._out_rows(q_out, "q_out", n, self.Hq)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        args = self.h, layer, b, k, v, qr, qo, r, n, self._stream(stream)
-        st = self._c_append(*args) if self._current_device() == self._index else self._on_device(self._c_append, *args)
+        if norm is None and k_out is None:
+            fn, args = self._c_append, (self.h, layer, b, k, v, qr, qo, r, n, self._stream(stream))
+        else:
+            if norm is not None:
+                norm._check(self.device, self.dtype, self.Hq, self.Hkv, self.D)
+            ko = None if k_out is None else self._out_rows(k_out, "k_out", n, self.Hkv)
+            fn, args = self._c_norm, (self.h, layer, b, k, v, qr, qo, ko, None if norm is None else norm.args, r, n,
+                                      self._stream(stream))
+        st = fn(*args) if self._current_device() == self._index else self._on_device(fn, *args)
         if st:
             raise KVQError(st, "kvq_paged_append")
         return q_out
@@ -692,6 +781,60 @@ class KVQPagedCache:
         st = self._c_attn(*args) if self._current_device() == self._index else self._on_device(self._c_attn, *args)
         if st:
             raise KVQError(st, "kvq_paged_decode_attn")
+        return (out, lse) if return_lse else out
+
+    def chunk_attn(self, layer: int, batch: PagedBatch, q, out=None, scale: float = 0.0, window: int = 0,
+                   return_lse: bool = False, stream=None):
+        """Causal attention of the newest rows of every sequence (cu_tokens and
+        seq_lens as for the append that came before) over its pages: q
+        [n, Hq, d] -> [n, Hq, d] in the cache's dtype, the token at position p
+        over positions max(0, p - window + 1) .. p (window 0: all up to p); with
+        return_lse (out, fp32 [n, Hq] log-sum-exp of the scaled scores).  Rows
+        that belong to no sequence are not written."""
+        self._counts(layer, window, "kvq_paged_chunk_attn")
+        return self._attend("kvq_paged_chunk_attn", self._c_chunk, (self.h, layer), batch, q, (), out, scale, window,
+                            return_lse, stream)
+
+    def prompt_attn(self, batch: PagedBatch, q, K, V, out=None, scale: float = 0.0, window: int = 0,
+                    return_lse: bool = False, stream=None):
+        """Causal attention of whole prompts over their own rows, not the
+        pages': q [n, Hq, d], K, V [n, Hkv, d], the rows of sequence s as
+        batch.cu_tokens has them (its table and lengths are not looked at).
+        Returns as ``chunk_attn`` does."""
+        self._counts(0, window, "kvq_paged_prompt_attn")
+        return self._attend("kvq_paged_prompt_attn", self._c_prompt, (self.h,), batch, q, ((K, "K"), (V, "V")), out,
+                            scale, window, return_lse, stream)
+
+    def _attend(self, name, fn, first, batch, q, kv, out, scale, window, return_lse, stream):
+        """The call that chunk_attn and prompt_attn share."""
+        n = q.shape[0]
+        self._counts(0, n, name)
+        b = self._batch(batch)
+        qr = self._rows(q, "q", n, self.Hq)
+        rows = [self._rows(x, label, n, self.Hkv) for x, label in kv]
+        if b.cu_tokens is None and n != batch.num_seqs:
+            raise ValueError(f"q has {n} rows, expected one for each of {batch.num_seqs} sequences")
+        if out is None:
+            out = self._new(stream, (n, self.Hq, self.D), self.dtype)
+        elif out.dtype != self.dtype or out.device != self.device or tuple(out.shape) != (n, self.Hq, self.D) or \
+                not out.is_contiguous():
+            raise ValueError(f"out must be contiguous {self.dtype} of shape {(n, self.Hq, self.D)} on {self.device}")
+        lse = self._new(stream, (n, self.Hq), self._f32) if return_lse else None
+        if scale and -_FLT_MIN < scale < _FLT_MIN:  # as a C float it could be 0, which means another scale
+            raise ValueError(f"scale must be 0 or at least {_FLT_MIN} in magnitude, got {scale}")
+        key = batch.num_seqs, n
+        nws = self._ws.get(key)
+        if nws is None:
+            nws = kvq_paged_chunk_workspace_bytes(self.h, *key)
+            if len(self._ws) < 4096:  # prompts come in any number of rows
+                self._ws[key] = nws
+        # as for decode_attn: a workspace of its own for every call
+        ws = self._new(stream, nws, self._u8)
+        args = (*first, b, qr, *rows, out.data_ptr(), lse.data_ptr() if return_lse else None, scale, window, n,
+                ws.data_ptr(), nws, self._stream(stream))
+        st = fn(*args) if self._current_device() == self._index else self._on_device(fn, *args)
+        if st:
+            raise KVQError(st, name)
         return (out, lse) if return_lse else out
 
     def read(self, layer: int, batch: PagedBatch, n: int, K=None, V=None, stream=None):
