@@ -2,6 +2,7 @@
 // (16 consecutive tokens of one kv head), shared by append, read and attention.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -166,7 +167,11 @@ cudaError_t paged_read_launch(const PagedReadParams& p, int D, int dtype, int sm
 cudaError_t paged_attn_prepare(int kb, int vb, int D, int dtype);
 cudaError_t paged_attn_launch(PagedAttnParams p, int D, int dtype, int sms, cudaStream_t s);
 size_t paged_attn_workspace(int D, int hkv, int seqs, int sms);
-cudaError_t paged_chunk_launch(const PagedChunkParams& p, int D, int dtype, int sms, cudaStream_t s);
-size_t paged_chunk_workspace(int D, int hkv, int gqa, int seqs, int n, int sms);
+typedef decltype(&cuTensorMapEncodeTiled) TensorMapEncode;
+// `pages`: the layer's map (16-bit layers).
+cudaError_t paged_chunk_launch(const PagedChunkParams& p, const CUtensorMap* pages, TensorMapEncode enc, int D, int dtype,
+                               int sms, cudaStream_t s);
+size_t paged_chunk_workspace(int D, int hkv, int gqa, int n, int sms);
+bool paged_chunk_map(CUtensorMap* m, TensorMapEncode enc, void* pages, int64_t tiles, int page_size, int D, int dtype);
 
 }  // namespace kvq

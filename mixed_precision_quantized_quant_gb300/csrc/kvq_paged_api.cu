@@ -29,6 +29,7 @@ constexpr int kMaxLayers = 1 << 16, kMaxHeads = 1 << 16;
 struct PagedLayer {
   int kb, vb, tile_bytes;
   int64_t head_stride, page_stride, off;
+  CUtensorMap map;  // of 16-bit rows
 };
 
 bool shape_ok(const kvq_paged_config* c) {
@@ -85,6 +86,7 @@ struct kvq_paged {
   uint8_t* base = nullptr;
   int32_t* err = nullptr;
   int device = 0, sms = 0;
+  kvq::TensorMapEncode encode = nullptr;  // the driver's
   std::mutex taking;  // of the error word: err[1] is one call's at a time
   int64_t checked_bytes = INT64_MAX;  // debug builds: where the checks take a layer's pages to end at the latest
 };
@@ -226,7 +228,8 @@ kvq_status attend(kvq_paged* h, int layer, const kvq_paged_batch* batch, const k
   p.prompt = prompt;
   p.ws = static_cast<uint8_t*>(workspace);
   p.ws_hi = p.ws + workspace_bytes;
-  return kvq::paged_chunk_launch(p, d, h->cfg.dtype, h->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return kvq::paged_chunk_launch(p, &h->layers[layer].map, h->encode, d, h->cfg.dtype, h->sms,
+                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }
@@ -252,6 +255,14 @@ kvq_status kvq_paged_create(const kvq_paged_config* cfg, void* dev_buf, size_t b
   if (bytes < static_cast<size_t>(need)) return KVQ_ERR_CAPACITY;
   kvq_paged* h = new (std::nothrow) kvq_paged;
   if (!h) return KVQ_ERR_ARG;
+  void* encode = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &encode, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess) {
+    delete h;
+    return KVQ_ERR_CUDA;
+  }
+  h->encode = reinterpret_cast<kvq::TensorMapEncode>(encode);
   try {
     h->layers.resize(static_cast<size_t>(cfg->num_layers));
   } catch (...) {
@@ -264,7 +275,11 @@ kvq_status kvq_paged_create(const kvq_paged_config* cfg, void* dev_buf, size_t b
   int64_t off = 0;
   for (int l = 0; l < cfg->num_layers; ++l) {
     layer_plan(cfg, l, off, &h->layers[l], &off);
-    if (kvq::paged_attn_prepare(h->layers[l].kb, h->layers[l].vb, cfg->head_dim, cfg->dtype) != cudaSuccess) {
+    PagedLayer& lay = h->layers[l];
+    if (kvq::paged_attn_prepare(lay.kb, lay.vb, cfg->head_dim, cfg->dtype) != cudaSuccess ||
+        (lay.kb == 16 && !kvq::paged_chunk_map(&lay.map, h->encode, h->base + lay.off,
+                                               lay.page_stride / lay.tile_bytes * cfg->num_pages, cfg->page_size,
+                                               cfg->head_dim, cfg->dtype))) {
       delete h;
       return KVQ_ERR_CUDA;
     }
@@ -352,7 +367,7 @@ kvq_status kvq_paged_prompt_attn(kvq_paged* h, const kvq_paged_batch* batch, con
 size_t kvq_paged_chunk_workspace_bytes(const kvq_paged* h, int num_seqs, int n_tokens) {
   if (!h || num_seqs < 1 || n_tokens < 0) return 0;
   return kvq::paged_chunk_workspace(h->cfg.head_dim, h->cfg.num_kv_heads, h->cfg.num_q_heads / h->cfg.num_kv_heads,
-                                    num_seqs, n_tokens, h->sms);
+                                    n_tokens, h->sms);
 }
 
 kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K, const kvq_rows* V,
