@@ -153,6 +153,8 @@ struct Shape {
 
 struct Ctl {
   uint64_t full[8], empty[8];   // ring stages
+  // one for each query tile, or where there is one for each of its score tiles, of which a role may be a tile ahead of
+  // another: a wait tells a phase from the one before only
   uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
   uint64_t group[2];            // a group's warps have read its results
   uint64_t looked[8];           // masked values of the stage have been looked through
@@ -447,7 +449,11 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
       mbar_init(&ctl.o_done[g], 1);
       mbar_init(&ctl.group[g], 4);
     }
-    if (NQ == 1) mbar_init(&ctl.s_full[1], 1);
+    if (NQ == 1) {
+      mbar_init(&ctl.s_full[1], 1);
+      mbar_init(&ctl.p_full[1], 4);
+      mbar_init(&ctl.o_done[1], 1);
+    }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
       mbar_init(&ctl.seg_empty[i], W0 + 3);
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
       const uint32_t idS = idesc_f16_f32(kM, kTokens) | f | (p.alpha < 0.0f ? 1u << 13 : 0u);  // -q for a scale below 0
       const uint32_t sq = smem_u32(sm + S::q), sr = smem_u32(sm + S::ring);
       Stage st = {0, 0}, slot = {0, 0};
-      uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, lookph = 0;
+      uint32_t qph[2] = {0, 0}, pph = 0, lookph = 0;
       bool ok = true;
       auto scores = [&](int g, int buf, int stage) {
         const uint64_t dq = smem_desc_sw128(sq + g * S::tile, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
@@ -667,12 +673,13 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
 #pragma unroll
           for (int g = 0; g < NQ; ++g) {
             if (i >= ng[g]) continue;
-            ok = ok && wait(&ctl.p_full[g], pph[g], err, quit);
-            pph[g] ^= 1;
+            const int buf = NQ == 1 ? i & 1 : g;
+            ok = ok && wait(&ctl.p_full[buf], pph >> buf & 1, err, quit);
+            pph ^= 1u << buf;
             if (!ok) break;
             tc_fence_after_sync();
-            outputs(g, NQ == 1 ? i & 1 : g, v.i, i == 0);
-            if (NQ == 1 || i + 1 == ng[g]) umma_commit(&ctl.o_done[g]);
+            outputs(g, buf, v.i, i == 0);
+            if (NQ == 1 || i + 1 == ng[g]) umma_commit(&ctl.o_done[buf]);
             if (NQ > 1 && i + 1 < ng[g]) {
               if (!have) {
                 ok = wait(&ctl.full[st.i], st.phase, err, quit);
@@ -834,7 +841,7 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
               l *= f;
               if (i > 0) {
                 if (NQ == 1) {  // the product of the tile before (for two tiles s_full says so)
-                  ok = __all_sync(0xffffffffu, wait(&ctl.o_done[0], oph ^ 1, err, quit));
+                  ok = __all_sync(0xffffffffu, wait(&ctl.o_done[buf ^ 1], (oph >> (buf ^ 1) & 1) ^ 1, err, quit));
                   if (!ok) break;
                   tc_fence_after_sync();
                 }
@@ -849,7 +856,7 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
                 }
               }
             }
-            if (NQ == 1) oph ^= 1;
+            if (NQ == 1) oph ^= 1u << buf;
             const float nm = Fmt<T>::room - (m == -INFINITY ? 0.0f : m);
             const f2 nm2 = f2_of(nm, nm);
             f2 sum[2] = {f2_of(0.0f, 0.0f), f2_of(0.0f, 0.0f)};
@@ -876,11 +883,12 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.p_full[g]);
+            if (lane == 0) mbar_arrive(&ctl.p_full[buf]);
           }
           if (!ok) break;
           if (NQ == 1) {
-            ok = wait(&ctl.o_done[0], oph ^ 1, err, quit);
+            const int buf = (nt - 1) & 1;
+            ok = wait(&ctl.o_done[buf], (oph >> buf & 1) ^ 1, err, quit);
           } else {
             ok = wait(&ctl.o_done[g], oph, err, quit);
             oph ^= 1;
