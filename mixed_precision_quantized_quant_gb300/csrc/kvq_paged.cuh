@@ -171,7 +171,7 @@ typedef decltype(&cuTensorMapEncodeTiled) TensorMapEncode;
 // `pages`: the layer's map (16-bit layers).
 cudaError_t paged_chunk_launch(const PagedChunkParams& p, const CUtensorMap* pages, TensorMapEncode enc, int D, int dtype,
                                int sms, cudaStream_t s);
-size_t paged_chunk_workspace(int D, int hkv, int gqa, int n, int sms);
+size_t paged_chunk_workspace(int D, int hkv, int gqa, int seqs, int n, int sms);
 bool paged_chunk_map(CUtensorMap* m, TensorMapEncode enc, void* pages, int64_t tiles, int page_size, int D, int dtype);
 
 }  // namespace kvq

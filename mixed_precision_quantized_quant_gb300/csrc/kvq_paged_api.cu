@@ -367,7 +367,7 @@ kvq_status kvq_paged_prompt_attn(kvq_paged* h, const kvq_paged_batch* batch, con
 size_t kvq_paged_chunk_workspace_bytes(const kvq_paged* h, int num_seqs, int n_tokens) {
   if (!h || num_seqs < 1 || n_tokens < 0) return 0;
   return kvq::paged_chunk_workspace(h->cfg.head_dim, h->cfg.num_kv_heads, h->cfg.num_q_heads / h->cfg.num_kv_heads,
-                                    n_tokens, h->sms);
+                                    num_seqs, n_tokens, h->sms);
 }
 
 kvq_status kvq_paged_read(kvq_paged* h, int layer, const kvq_paged_batch* batch, const kvq_rows* K, const kvq_rows* V,

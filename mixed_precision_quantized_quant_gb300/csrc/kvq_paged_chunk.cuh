@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kvq_paged_rows.cuh"
 #include "kvq_tc.cuh"
 
@@ -17,10 +19,10 @@ using rows::f2_of;
 using rows::fma2;
 
 constexpr int kTokens = 128;  // tokens of a key or value tile
-constexpr int kM = 128;       // rows of a query tile: (token, query head) pairs of one kv head
+constexpr int kM = 128;       // rows of a query tile: the (token, query head) pairs of kM / gqa tokens of one kv head
 constexpr int kStart = 2;     // what starting an item counts, in tiles
 constexpr int kPlan = 1024;   // entries of the plan in shared memory
-constexpr int kMostBad = 8;   // masked tiles of a segment (6 at the most: see Seg::masked)
+constexpr int kMostBad = 8;   // masked tiles of a segment (see masked_tile)
 constexpr int kSlots = 2;     // segments under way
 
 // Weights are taken 2^room above the power of two that a running maximum stands
@@ -66,28 +68,19 @@ __device__ __forceinline__ Span read_span(const PagedChunkParams& p, int s, bool
   return r;
 }
 
-// Item j of a sequence and kv head: rows j R .. of its (token, head) pairs.
+// Item j of a sequence and kv head: tokens j T .. of its m.
 struct Item {
-  int tok, rem;    // first token; row 0 is its head `rem`
-  int rows;
-  int last;        // last token
-  int t0, t1;      // tiles that its rows see: t0 .. t1 - 1
+  int tok, tokens;
+  int t0, t1;      // tiles of keys that its rows see: t0 .. t1 - 1
 };
 
-__device__ __forceinline__ int items_of(int m, int gqa, int R) {
-  return static_cast<int>((static_cast<int64_t>(m) * gqa + R - 1) / R);
-}
-
-__device__ __forceinline__ Item item_of(const Span& s, int64_t j, int gqa, int R, int window) {
+__device__ __forceinline__ Item item_of(const Span& s, int j, int T, int window) {
   Item it;
-  const int64_t x = j * R, total = static_cast<int64_t>(s.m) * gqa;
-  it.tok = static_cast<int>(x / gqa);
-  it.rem = static_cast<int>(x - static_cast<int64_t>(it.tok) * gqa);
-  it.rows = static_cast<int>(total - x < R ? total - x : R);
-  it.last = it.tok + (it.rem + it.rows - 1) / gqa;
+  it.tok = j * T;
+  it.tokens = s.m - it.tok < T ? s.m - it.tok : T;
   const int first = s.pos0 + it.tok;
   it.t0 = window && first >= window ? (first - window + 1) / kTokens : 0;
-  it.t1 = (s.pos0 + it.last) / kTokens + 1;
+  it.t1 = (first + it.tokens - 1) / kTokens + 1;
   return it;
 }
 
@@ -97,30 +90,30 @@ struct Seg {
   const int32_t* table;  // the sequence's pages
   int done;              // 1: no more
   int row, pos;          // tensor row and position of the item's first token
-  int rem, rows;
+  int tokens;
   int kvh;
   int t0, t1;
   int lo, hi;            // positions that any of the item's rows sees: lo .. hi - 1
   int whole;             // the item has no other segments
   int slot;              // else: where the partial result goes
-  int bad_tiles;         // tiles with infinite or NaN values among the masked ones
+  int dirty;             // 1: there are infinite or NaN values in masked tiles
+  int bad_tiles;         // masked tiles
   int bad_tile[kMostBad];
-  uint32_t bad[kMostBad][4];  // their tokens
+  uint32_t bad[kMostBad][4];  // their tokens with such values
 };
 
-// Whether some row of the rows first .. (positions) to last sees only a part of
-// tile t.  Those are the tiles of the last rows' positions and of the window's
-// lower ends, at most three each: rows first .. last are 256 tokens at the most.
+// Whether some row of positions first .. last sees only a part of tile t.  Those
+// are the tiles of the rows' positions and of their windows' lower ends, at most
+// three each: first .. last are 256 tokens at the most.
 __device__ __forceinline__ bool masked_tile(int t, int first, int last, int window) {
   return t * kTokens + kTokens - 1 > first || (window && t * kTokens <= last - window);
 }
 
 // A CTA's note for the join.
 struct Note {
-  int rows;       // of the item whose first piece this CTA left in its slot 1; 0: none
-  int row, rem, kvh;
+  int tokens;     // of the item whose first piece this CTA left in its slot 1; 0: none
+  int row, kvh;
   int cont;       // 1: its slot 0 continues the item of the CTA before, 2: and ends it
-  int pad[3];
 };
 
 // Where a boundary at weight b cuts an item of nt tiles that starts at x: not
@@ -134,40 +127,58 @@ __device__ __forceinline__ int cut_at(int64_t b, int64_t x, int nt, int tol) {
 
 // ---------------------------------------------------------------- shape
 
-template <int D, int NQ>
+template <int D, int NQ, bool QUANT>
 struct Shape {
-  static constexpr int R = NQ * kM;
   static constexpr int H = D / 64;                 // 128-byte halves of a row
   static constexpr int half = kTokens * 128;       // bytes of a tile's half
   static constexpr int tile = H * half;
   static constexpr int softmax = NQ * 128;         // threads
-  static constexpr int threads = softmax + 128;    // and the warps that load, multiply and look (two)
-  static constexpr int NST = D == 128 ? (NQ == 2 ? 5 : 6) : 8;
+  // Beside them: for codes four warps that unpack, for 16 bits two that look
+  // through masked values; one that loads and one that multiplies (with two idle
+  // ones a warpgroup, where registers are shared out anew).
+  static constexpr int helpers = QUANT ? 4 : 2;
+  static constexpr int W0 = NQ * 4;                // first helper
+  static constexpr int WL = W0 + helpers;          // loads; WL + 1 multiplies
+  static constexpr bool split = QUANT && NQ == 2;
+  static constexpr int threads = (WL + (split ? 4 : 2)) * 32;
+  // Registers of a thread where four warpgroups have 128 each at launch: their sum is 4 x 128 again.
+  static constexpr int regs_softmax = 168, regs_others = 88;
+  static_assert(!split || (threads == 512 && 2 * regs_softmax + 2 * regs_others <= 512), "registers");
+  static constexpr int NST = QUANT ? 4 : D == 128 ? (NQ == 2 ? 5 : 6) : 8;  // key and value tiles, in turn
   static constexpr int q = 0;
   static constexpr int ring = NQ * tile;           // (a query tile is as large as a key tile)
-  static constexpr int ctl = ring + NST * tile;
-  static constexpr int smem = ctl + 2048;
-  static_assert(smem <= 227 * 1024 && NST * tile >= kPlan * 8, "shared memory");
+  static constexpr int raw = ring + NST * tile;    // codes: tiles of 16 tokens as they are stored
+  static constexpr int extra = QUANT ? 2 * kTokens * 8 + NQ * kM * 8 : 0;  // key scales of two tiles, rows' factors
+  static constexpr int most = 227 * 1024;
+  static constexpr int raw_bytes = QUANT ? (most - raw - extra - 2560) / 128 * 128 : 0;
+  static constexpr int scales = raw + raw_bytes;
+  static constexpr int factors = scales + (QUANT ? 2 * kTokens * 8 : 0);
+  static constexpr int ctl = raw + raw_bytes + extra;
+  static constexpr int smem = ctl + 2560;
+  static_assert(smem <= most && NST * tile >= kPlan * 8, "shared memory");
+  static_assert(!QUANT || raw_bytes >= 4 * paged_tile_bytes(D, 8, 8), "stored tiles");
   static constexpr int tS = 0, tO = 2 * kTokens;   // columns: two score tiles, then the outputs
 };
 
+constexpr int kMostRaw = 32;  // stored tiles under way
+
 struct Ctl {
   uint64_t full[8], empty[8];   // ring stages
-  // one for each query tile, or where there is one for each of its score tiles, of which a role may be a tile ahead of
-  // another: a wait tells a phase from the one before only
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
-  uint64_t group[2];            // a group's warps have read its results
   uint64_t looked[8];           // masked values of the stage have been looked through
+  uint64_t raw_full[kMostRaw], raw_empty[kMostRaw];
+  // one for each query tile, or where there is one for each of its score tiles, of which a role may be a tile ahead of
+  // another: a wait tells a phase from the one before only.  Weights are ready in two halves.
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2];
   uint64_t seg_full[kSlots], seg_empty[kSlots];
   uint64_t fin;
   uint32_t tmem;
   int quit;
   Seg seg[kSlots];
 };
-static_assert(sizeof(Ctl) <= 2048, "control");
+static_assert(sizeof(Ctl) <= 2560, "control");
 
 // A bounded wait that ends when another of the CTA's waits gave up.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t phase, int32_t* err, volatile int* quit) {
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t phase, int32_t* err, volatile int* quit) {
   for (int i = 0; i < 1 << 12; ++i) {
     const uint32_t addr = smem_u32(bar);
     for (int k = 0; k < 1 << 10; ++k) {
@@ -246,20 +257,28 @@ __device__ __forceinline__ uint32_t pack2(__nv_bfloat16*, float x, float y) {
 
 struct Launch {
   PagedChunkParams p;
+  CUtensorMap qm;       // queries, where q_tma
   CUtensorMap km, vm;   // pages: km alone; prompts: keys, values
+  int q_tma;
+  int bf16;             // of codes, whose kernels know no type: q and out are bf16
+  int T;                // tokens of a query tile: kM / gqa
+  int raw_slots;        // codes: stored tiles that fit the ring
   int grid;
   int slot_rows;        // rows of a partial result
+  float room;           // of the weights (see Fmt)
   int64_t partials;     // bytes of the workspace before them
 };
 
 // ---------------------------------------------------------------- planning
 
 // Weight (tiles, and kStart an item) of a sequence's items of one kv head, by a warp.
-__device__ __forceinline__ int64_t span_weight(const Span& s, int gqa, int R, int window, int lane) {
-  const int q = items_of(s.m, gqa, R);
+__device__ __forceinline__ int items_of(int m, int T) { return m ? (m - 1) / T + 1 : 0; }
+
+__device__ __forceinline__ int64_t span_weight(const Span& s, int T, int window, int lane) {
+  const int q = items_of(s.m, T);
   int64_t w = 0;
   for (int j = lane; j < q; j += 32) {
-    const Item it = item_of(s, j, gqa, R, window);
+    const Item it = item_of(s, j, T, window);
     w += it.t1 - it.t0 + kStart;
   }
   for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -267,7 +286,7 @@ __device__ __forceinline__ int64_t span_weight(const Span& s, int gqa, int R, in
 }
 
 // Entry e of the plan: the weight of sequences e k .. e k + k - 1, all kv heads.
-__device__ __forceinline__ void plan_entries(const PagedChunkParams& p, int R, int64_t* plan, int entries, int k,
+__device__ __forceinline__ void plan_entries(const PagedChunkParams& p, int T, int64_t* plan, int entries, int k,
                                              int warp, int warps, int lane) {
   for (int e0 = warp * 32; e0 < entries; e0 += warps * 32) {
     const int e = e0 + lane;
@@ -277,10 +296,10 @@ __device__ __forceinline__ void plan_entries(const PagedChunkParams& p, int R, i
       Span sp = {0, 0, 0};
       if (e < entries && s < p.batch.seqs) sp = read_span(p, static_cast<int>(s), blockIdx.x == 0);
       // few items: by the lane itself; many: by the warp
-      const int q = items_of(sp.m, p.gqa, R);
+      const int q = items_of(sp.m, T);
       if (q <= 4)
         for (int j = 0; j < q; ++j) {
-          const Item it = item_of(sp, j, p.gqa, R, p.window);
+          const Item it = item_of(sp, j, T, p.window);
           w += it.t1 - it.t0 + kStart;
         }
       uint32_t big = __ballot_sync(0xffffffffu, q > 4);
@@ -289,7 +308,7 @@ __device__ __forceinline__ void plan_entries(const PagedChunkParams& p, int R, i
         big &= big - 1;
         const Span o = {__shfl_sync(0xffffffffu, sp.row0, l), __shfl_sync(0xffffffffu, sp.m, l),
                         __shfl_sync(0xffffffffu, sp.pos0, l)};
-        const int64_t x = span_weight(o, p.gqa, R, p.window, lane);
+        const int64_t x = span_weight(o, T, p.window, lane);
         if (lane == l) w += x;
       }
     }
@@ -306,7 +325,7 @@ struct Walk {
   int tol;
 };
 
-__device__ __forceinline__ void walk_start(const PagedChunkParams& p, int R, const int64_t* plan, int entries, int k,
+__device__ __forceinline__ void walk_start(const PagedChunkParams& p, int T, const int64_t* plan, int entries, int k,
                                            int cta, int grid, int lane, Walk& w) {
   // each lane has a run of entries
   const int per = (entries + 31) / 32;
@@ -338,7 +357,7 @@ __device__ __forceinline__ void walk_start(const PagedChunkParams& p, int R, con
   int64_t s = static_cast<int64_t>(e) * k;
   for (; s < p.batch.seqs; ++s) {
     w.sp = read_span(p, static_cast<int>(s), false);
-    const int64_t one = span_weight(w.sp, p.gqa, R, p.window, lane), all = one * p.hkv;
+    const int64_t one = span_weight(w.sp, T, p.window, lane), all = one * p.hkv;
     if (all > 0 && x + all > w.b0) {
       w.kvh = static_cast<int>((w.b0 - x) / one);
       x += one * w.kvh;
@@ -348,11 +367,11 @@ __device__ __forceinline__ void walk_start(const PagedChunkParams& p, int R, con
   }
   if (s >= p.batch.seqs) return;
   w.s = static_cast<int>(s);
-  w.q = items_of(w.sp.m, p.gqa, R);
+  w.q = items_of(w.sp.m, T);
   for (int j0 = 0; j0 < w.q; j0 += 32) {
     int64_t wt = 0;
     if (j0 + lane < w.q) {
-      const Item it = item_of(w.sp, j0 + lane, p.gqa, R, p.window);
+      const Item it = item_of(w.sp, j0 + lane, T, p.window);
       wt = it.t1 - it.t0 + kStart;
     }
     int64_t e2 = wt;
@@ -373,7 +392,7 @@ __device__ __forceinline__ void walk_start(const PagedChunkParams& p, int R, con
 }
 
 // To the next item; false where there is none.
-__device__ __forceinline__ bool walk_next(const PagedChunkParams& p, int R, int tiles, Walk& w) {
+__device__ __forceinline__ bool walk_next(const PagedChunkParams& p, int T, int tiles, Walk& w) {
   w.x += tiles + kStart;
   if (++w.j < w.q) return true;
   w.j = 0;
@@ -381,7 +400,7 @@ __device__ __forceinline__ bool walk_next(const PagedChunkParams& p, int R, int 
   w.kvh = 0;
   while (++w.s < p.batch.seqs) {
     w.sp = read_span(p, w.s, false);
-    w.q = items_of(w.sp.m, p.gqa, R);
+    w.q = items_of(w.sp.m, T);
     if (w.q) return true;
   }
   return false;
@@ -389,8 +408,9 @@ __device__ __forceinline__ bool walk_next(const PagedChunkParams& p, int R, int 
 
 // ---------------------------------------------------------------- values that are no numbers
 
-template <typename T, int D, bool PROMPT>
-__device__ __forceinline__ const uint8_t* value_row(const PagedChunkParams& p, const Seg& sg, int t) {
+// The tile that holds position t's rows, or for prompts the value row itself.
+template <bool PROMPT>
+__device__ __forceinline__ const uint8_t* value_at(const PagedChunkParams& p, const Seg& sg, int t) {
   if (PROMPT)
     return p.v.data + 2 * ((static_cast<int64_t>(sg.row) - sg.pos + t) * p.v.token_stride + sg.kvh * p.v.head_stride);
   const int page = sg.table[t >> p.pool.page_shift];
@@ -403,17 +423,26 @@ __device__ __forceinline__ const uint8_t* value_row(const PagedChunkParams& p, c
 
 // The masked tiles' values that are not finite were left out of the products
 // (times a weight of 0 they would be NaN); the rows that see them get them here.
-template <typename T, int D, bool PROMPT>
+// A quantized row whose scale or zero is no number is none in all channels.
+template <typename T, int D, bool PROMPT, bool QUANT>
 __device__ __forceinline__ void add_bad(const PagedChunkParams& p, const Seg& sg, int first, int last, int c0, float (&o)[32]) {
   for (int i = 0; i < sg.bad_tiles && i < kMostBad; ++i)
     for (int b = 0; b < kTokens; ++b) {
+      if (!sg.bad[i][b / 32]) {
+        b |= 31;
+        continue;
+      }
       const int t = sg.bad_tile[i] * kTokens + b;
       if (!(sg.bad[i][b / 32] >> (b % 32) & 1) || t < first || t > last) continue;
-      const uint8_t* v = value_row<T, D, PROMPT>(p, sg, t);
-      if (!v) continue;
+      const uint8_t* v = QUANT ? nullptr : value_at<PROMPT>(p, sg, t);
+      if (!QUANT && !v) continue;
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         const int ch = c0 + c;
+        if (QUANT) {
+          o[c] = __int_as_float(0x7fffffff);
+          continue;
+        }
         const T* x = PROMPT ? reinterpret_cast<const T*>(v) + ch
                             : reinterpret_cast<const T*>(v + 32 * D + (t % kTile) * 2 * D +
                                                          16 * tile_chunk16(ch / 8, t % kTile) + ch % 8 * 2);
@@ -423,336 +452,717 @@ __device__ __forceinline__ void add_bad(const PagedChunkParams& p, const Seg& sg
     }
 }
 
+// ---------------------------------------------------------------- codes
+
+// Sixteen codes of one token (an aligned run of channels) as fp16 numbers less
+// `mid`, exact, in the order that the fields come out in: pair j holds channels
+//   8 bits: 4 (j / 2) + j % 2 and two further,
+//   4 bits: 8 (j / 4) + j % 4 and four further,
+//   2 bits: j and eight further.
+// An AND leaves two fields in the mantissas of 1024 (times their place), one
+// multiply-add takes both out; keys and queries, and outputs where they are
+// written, follow that order.
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t mask, int k, float mid) {
+  const __half2 e = u32_as_h2(and_or(x, mask << k, 0x64006400u));
+  const float sc = 1.0f / static_cast<float>(1 << k);
+  return h2_as_u32(__hfma2(e, __float2half2_rn(sc), __float2half2_rn(-1024.0f * sc - mid)));
+}
+template <int BITS>
+__device__ __forceinline__ void unpack16(const uint8_t* src, float mid, uint32_t (&h)[8]) {
+  if constexpr (BITS == 8) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[2 * i] = code_pair(w[i], 0x00ff00ffu, 0, mid);
+      h[2 * i + 1] = code_pair(w[i] >> 8, 0x00ff00ffu, 0, mid);
+    }
+  } else if constexpr (BITS == 4) {
+    const uint2 x = *reinterpret_cast<const uint2*>(src);
+    const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      h[4 * i] = code_pair(w[i], 0x000f000fu, 0, mid);
+      h[4 * i + 1] = code_pair(w[i], 0x000f000fu, 4, mid);
+      h[4 * i + 2] = code_pair(w[i] >> 8, 0x000f000fu, 0, mid);
+      h[4 * i + 3] = code_pair(w[i] >> 8, 0x000f000fu, 4, mid);
+    }
+  } else {
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(src), y = x >> 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = code_pair(x, 0x00030003u, 2 * i, mid);
+      h[4 + i] = code_pair(y, 0x00030003u, 2 * i, mid);
+    }
+  }
+}
+// Channel of place i (of 16) in that order.
+__host__ __device__ constexpr int code_channel(int bits, int i) {
+  const int j = i / 2, k = i % 2;
+  return bits == 8 ? 4 * (j / 2) + j % 2 + 2 * k : bits == 4 ? 8 * (j / 4) + j % 4 + 4 * k : j + 8 * k;
+}
+
+// Stores the two 16-byte chunks of a run of 16 channels (run u of row `row`) at
+// their swizzled places; the order keeps a warp's lanes, eight runs of a row,
+// on different banks.
+template <int HALF>
+__device__ __forceinline__ void store_run(uint8_t* tile, int row, int u, const uint32_t (&h)[8]) {
+  uint8_t* at = tile + (u / 4) * HALF + row * 128;
+  const int c = 2 * (u % 4), x = row & 7, odd = u / 4;
+  const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+  *reinterpret_cast<uint4*>(at + (((c + odd) ^ x) << 4)) = odd ? b : a;
+  *reinterpret_cast<uint4*>(at + (((c + 1 - odd) ^ x) << 4)) = odd ? a : b;
+}
+
+// One stored tile of 16 tokens (tokens t16 .. of the 128-token tile) into the
+// key and the value operand: keys as codes less their middle, the scales and
+// what they are to be added as fp32; values as numbers, rounded to fp16 once.
+// Tokens outside lo .. hi, and in masked tiles those whose scale or zero is no
+// number, get values of 0.
+template <int D, int KB, int VB>
+__device__ __forceinline__ void unpack_tile(const uint8_t* raw, uint8_t* kt, uint8_t* vt, float4* scales, int t16, int pos,
+                                            const Seg& sg, bool masked, int nth, int tid, int* dirty, uint32_t* bad) {
+  constexpr int U = D / 16, rk = D / 8 * KB, rv = D / 8 * VB, HALF = kTokens * 128;
+  const int u = tid % U, i = tid / U % 16;  // D = 64: half of the threads take keys, half values
+  const uint8_t* sz = raw + 16 * (rk + rv) + tile_key_row(i) * 8;
+  const bool keys = D == 128 || tid < 16 * U, values = D == 128 || tid >= 16 * U;
+  uint32_t h[8];
+  if (keys) {
+    constexpr float mid = KB == 8 ? 128.0f : KB == 4 ? 8.0f : 2.0f;
+    const int r = tile_key_row(i);
+    unpack16<KB>(raw + r * rk + ((u * 2 * KB) ^ tile_key_xor(rk, r)), mid, h);
+    store_run<HALF>(kt, t16 + i, u, h);
+    if (u == 0) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(sz));
+      float* to = reinterpret_cast<float*>(scales + (t16 + i) / 2) + (i & 1);
+      to[0] = f.x;
+      to[2] = fmaf(f.x, mid, f.y);
+    }
+  }
+  if (values) {
+    constexpr float mid = VB == 8 ? 128.0f : VB == 4 ? 8.0f : 2.0f;
+    __half2 f = *reinterpret_cast<const __half2*>(sz + 4);
+    const bool in = pos + i >= sg.lo && pos + i < sg.hi;
+    const uint32_t e = h2_as_u32(f);
+    const bool fine = ((e & 0x7c00u) != 0x7c00u) && ((e & 0x7c000000u) != 0x7c000000u);
+    if (!in || (masked && !fine)) {
+      if (in && u == 0) {
+        *dirty = 1;
+        if (nth < kMostBad) atomicOr(bad + (t16 + i) / 32, 1u << ((t16 + i) % 32));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = 0;
+    } else {
+      unpack16<VB>(raw + 16 * rk + i * rv + ((u * 2 * VB) ^ tile_val_xor(rv, i)), 0.0f, h);
+      (void)mid;
+      const __half2 s = __low2half2(f), z = __high2half2(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hfma2(u32_as_h2(h[j]), s, z));
+      // a last step past the greatest fp16 (a scale rounded up) stays finite
+      const float top = fabsf(__low2float(f)) * ((1 << VB) - 1) + fabsf(__high2float(f));
+      if (top > 65504.0f) {
+        const __half2 lim = __floats2half2_rn(65504.0f, 65504.0f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hmax2_nan(__hmin2_nan(u32_as_h2(h[j]), lim), __hneg2(lim)));
+      }
+    }
+    store_run<HALF>(vt, t16 + i, u, h);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void unpack_any(int kb, int vb, const uint8_t* raw, uint8_t* kt, uint8_t* vt, float4* scales, int t16,
+                                           int pos, const Seg& sg, bool masked, int nth, int tid, int* dirty, uint32_t* bad) {
+  const auto with = [&](auto k, auto v) {
+    unpack_tile<D, decltype(k)::value, decltype(v)::value>(raw, kt, vt, scales, t16, pos, sg, masked, nth, tid, dirty, bad);
+  };
+  using two = std::integral_constant<int, 2>;
+  using four = std::integral_constant<int, 4>;
+  using eight = std::integral_constant<int, 8>;
+  const auto value = [&](auto k) {
+    if (vb == 8)
+      with(k, eight{});
+    else if (vb == 4)
+      with(k, four{});
+    else
+      with(k, two{});
+  };
+  if (kb == 8)
+    value(eight{});
+  else if (kb == 4)
+    value(four{});
+  else
+    value(two{});
+}
+
+// Query rows of a group as operand rows, by `n` threads.  16 bits: as they are
+// (where a tensor map cannot describe them).  Codes: in fp16, times a power of
+// two that takes the row's largest near 2^14 (exact down to 2^-29 of it, in bf16
+// 2^-32), channels in the keys' order; the factor and the row's sum beside them.
+template <typename T, int D, bool QUANT>
+__device__ __forceinline__ void stage_queries(const Launch& a, const Seg& sg, int g, int rows, uint8_t* qs, float2* factors,
+                                              int me, int n) {
+  const PagedChunkParams& p = a.p;
+  constexpr int U = D / 16, HALF = kTokens * 128;
+  const int u = me % U, per = n / U;
+#pragma unroll (QUANT ? 2 : 4)
+  for (int r0 = 0; r0 < kM; r0 += per) {
+    const int row = r0 + me / U;
+    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (row < rows) {
+      const int tk = row / p.gqa, hh = row - tk * p.gqa;
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q.data) +
+                            (static_cast<int64_t>(sg.row) + g * a.T + tk) * p.q.token_stride +
+                            (sg.kvh * p.gqa + hh) * p.q.head_stride + 16 * u;
+      if (rows_ok(p.q, src, 32, p.pool.err)) {
+        rows::load8(src, p.q_vec, x[0]);
+        rows::load8(src + 8, p.q_vec, x[1]);
+      }
+    }
+    uint32_t h[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    if constexpr (QUANT) {
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 v = a.bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h[j])) : __half22float2(u32_as_h2(h[j]));
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(f[j]));
+#pragma unroll
+      for (int o = 1; o < U; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      int e = top > 0.0f && top < INFINITY ? 14 - ilogbf(top) : 0;
+      e = e > 126 ? 126 : e;
+      const float up = __int_as_float((127 + e) << 23) * (p.alpha < 0.0f ? -1.0f : 1.0f);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        f[j] = __half2float(__float2half_rn(f[j] * up));
+        sum += f[j];
+      }
+#pragma unroll
+      for (int o = 1; o < U; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (u == 0 && row < kM) factors[row] = make_float2(__int_as_float((127 - e) << 23), sum);
+      const auto order = [&](auto bits) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          h[j] = h2_as_u32(__floats2half2_rn(f[code_channel(decltype(bits)::value, 2 * j)], f[code_channel(decltype(bits)::value, 2 * j + 1)]));
+      };
+      if (p.pool.kb == 8)
+        order(std::integral_constant<int, 8>{});
+      else if (p.pool.kb == 4)
+        order(std::integral_constant<int, 4>{});
+      else
+        order(std::integral_constant<int, 2>{});
+    }
+    if (row < kM) store_run<HALF>(qs, row, u, h);
+  }
+}
+
+// 32 bytes at once
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* q = reinterpret_cast<uint4*>(p);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// 32 columns of outputs, in the values' order, as channels.
+template <bool QUANT>
+__device__ __forceinline__ void to_channels(int vb, float (&y)[32]) {
+  if constexpr (QUANT) {
+    float z[32];
+    const auto order = [&](auto bits) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i / 16 * 16 + code_channel(decltype(bits)::value, i % 16)] = y[i];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) y[i] = z[i];
+    };
+    if (vb == 8)
+      order(std::integral_constant<int, 8>{});
+    else if (vb == 4)
+      order(std::integral_constant<int, 4>{});
+    else
+      order(std::integral_constant<int, 2>{});
+  }
+}
+
+// (A kernel that shares its registers out anew may call no function: the compiler finds no registers for it.)
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- the kernel
 
-template <typename T, int D, int NQ, bool PROMPT>
-__global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(const __grid_constant__ Launch a) {
-  using S = Shape<D, NQ>;
+// QUANT: T is __half, the type of the products; q and out are in a.bf16's.
+template <typename T, int D, int NQ, bool PROMPT, bool QUANT>
+__global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_kernel(const __grid_constant__ Launch a) {
+  using S = Shape<D, NQ, QUANT>;
   extern __shared__ __align__(1024) uint8_t sm[];
   Ctl& ctl = *reinterpret_cast<Ctl*>(sm + S::ctl);
   const PagedChunkParams& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int W0 = S::softmax / 32;  // the loading warp; W0 + 1 multiplies, W0 + 2 and W0 + 3 look
+  const int items_T = NQ * a.T;  // tokens of an item
   int32_t* err = p.pool.err;
   int* quit = &ctl.quit;
+  const bool q_tma = !QUANT && a.q_tma;
 
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
-      mbar_init(&ctl.full[i], 1);
-      mbar_init(&ctl.empty[i], 3);  // the products have read it, and the two warps that look have passed it
-      mbar_init(&ctl.looked[i], 2);
+      mbar_init(&ctl.full[i], QUANT ? S::helpers : 1);
+      // the products have read it, and (16 bits) the two warps that look have passed it
+      mbar_init(&ctl.empty[i], QUANT ? 1 : 1 + S::helpers);
+      mbar_init(&ctl.looked[i], S::helpers);
     }
-    for (int g = 0; g < NQ; ++g) {
-      mbar_init(&ctl.q_full[g], 4);
+    if (QUANT)
+      for (int i = 0; i < kMostRaw; ++i) {
+        mbar_init(&ctl.raw_full[i], 1);
+        mbar_init(&ctl.raw_empty[i], S::helpers);
+      }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&ctl.q_full[g], q_tma ? 1 : S::helpers);
+      mbar_init(&ctl.q_empty[g], QUANT ? 5 : 1);  // the products, and the warps that have the rows' factors
       mbar_init(&ctl.s_full[g], 1);
-      mbar_init(&ctl.p_full[g], 4);
+      mbar_init(&ctl.p_full[g][0], 4);
+      mbar_init(&ctl.p_full[g][1], 4);
       mbar_init(&ctl.o_done[g], 1);
-      mbar_init(&ctl.group[g], 4);
-    }
-    if (NQ == 1) {
-      mbar_init(&ctl.s_full[1], 1);
-      mbar_init(&ctl.p_full[1], 4);
-      mbar_init(&ctl.o_done[1], 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
-      mbar_init(&ctl.seg_empty[i], W0 + 3);
+      mbar_init(&ctl.seg_empty[i], S::W0 + S::helpers + 1);
     }
     mbar_init(&ctl.fin, 1);
     ctl.quit = 0;
     fence_mbar_init();
   }
-  if (warp == W0 + 1) tmem_alloc(&ctl.tmem, 512);
+  if (warp == S::WL + 1) tmem_alloc(&ctl.tmem, 512);
   grid_dep_wait();
   grid_dep_launch();
   const int per_entry = (p.batch.seqs - 1) / kPlan + 1, entries = (p.batch.seqs - 1) / per_entry + 1;
   int64_t* plan = reinterpret_cast<int64_t*>(sm + S::ring);
-  plan_entries(p, S::R, plan, entries, per_entry, warp, S::threads / 32, lane);
+  plan_entries(p, items_T, plan, entries, per_entry, warp, S::threads / 32, lane);
+  fence_proxy_async_smem();  // the plan's bytes become the ring's
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tm = ctl.tmem;
+  // tiles, from t0 on, that query tile g of a segment sees: up to that of its last token's position
+  const auto tiles_of = [&](const Seg& sg, int g) {
+    const int left = sg.tokens - g * a.T;
+    if (left <= 0) return 0;
+    const int end = (sg.pos + g * a.T + (left < a.T ? left : a.T) - 1) / kTokens + 1;
+    return (end < sg.t1 ? end : sg.t1) - sg.t0;
+  };
 
-  if (warp == W0) {
-    // ================= plans, and loads keys and values
-    Walk w;
-    walk_start(p, S::R, plan, entries, per_entry, blockIdx.x, a.grid, lane, w);
-    __syncwarp();
-    fence_proxy_async_smem();  // the plan's bytes become the ring's
-    Note note = {};
-    Stage st = {0, 0}, slot = {0, 0};
-    int issued = 0;
-    bool ok = true;
-    bool more = w.s < p.batch.seqs;
-    while (more && ok && w.x < w.b1) {
-      const Item it = item_of(w.sp, w.j, p.gqa, S::R, p.window);
-      const int nt = it.t1 - it.t0;
-      const int from = w.x < w.b0 ? cut_at(w.b0, w.x, nt, w.tol) : 0;
-      const int to = w.x + nt + kStart > w.b1 ? cut_at(w.b1, w.x, nt, w.tol) : nt;
-      if (from < to) {
-        ok = wait(&ctl.seg_empty[slot.i], slot.phase ^ 1, err, quit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int pos = w.sp.pos0 + it.tok, hi = w.sp.pos0 + it.last + 1;
-        const int lo = p.window && pos >= p.window ? pos - p.window + 1 : 0;
-        const int32_t* table = PROMPT ? nullptr : p.batch.table + w.s * p.batch.table_stride;
-        if (lane == 0) {
+  if (warp >= S::WL) {
+    if constexpr (S::split) fewer_registers<S::regs_others>();
+    if (warp == S::WL) {
+      // ================= plans, and loads keys and values (and queries)
+      Walk w;
+      walk_start(p, items_T, plan, entries, per_entry, blockIdx.x, a.grid, lane, w);
+      __syncwarp();
+      Note note = {};
+      Stage st = {0, 0}, slot = {0, 0}, rw = {0, 0};
+      uint32_t qph = 0;
+      int issued = 0;
+      bool ok = true;
+      bool more = w.s < p.batch.seqs;
+      while (more && ok && w.x < w.b1) {
+        const Item it = item_of(w.sp, w.j, items_T, p.window);
+        const int nt = it.t1 - it.t0;
+        const int from = w.x < w.b0 ? cut_at(w.b0, w.x, nt, w.tol) : 0;
+        const int to = w.x + nt + kStart > w.b1 ? cut_at(w.b1, w.x, nt, w.tol) : nt;
+        if (from < to) {
+          ok = __all_sync(0xffffffffu, wait(&ctl.seg_empty[slot.i], slot.phase ^ 1, err, quit));
+          if (!ok) break;
+          const int pos = w.sp.pos0 + it.tok, hi = pos + it.tokens;
+          const int lo = p.window && pos >= p.window ? pos - p.window + 1 : 0;
+          const int32_t* table = PROMPT ? nullptr : p.batch.table + w.s * p.batch.table_stride;
           Seg& sg = ctl.seg[slot.i];
-          sg.table = table;
-          sg.done = 0;
-          sg.row = w.sp.row0 + it.tok;
-          sg.pos = pos;
-          sg.rem = it.rem;
-          sg.rows = it.rows;
-          sg.kvh = w.kvh;
-          sg.t0 = it.t0 + from;
-          sg.t1 = it.t0 + to;
-          sg.lo = lo;
-          sg.hi = hi;
-          sg.whole = from == 0 && to == nt;
-          sg.slot = 2 * blockIdx.x + (from == 0);
-          sg.bad_tiles = 0;
-          for (int i = 0; i < kMostBad; ++i)
-            for (int k = 0; k < 4; ++k) sg.bad[i][k] = 0;
-          mbar_arrive(&ctl.seg_full[slot.i]);
-        }
-        slot.next<kSlots>();
-        if (from > 0) {
-          note.cont = to == nt ? 2 : 1;
-        } else if (to < nt) {
-          note.rows = it.rows;
-          note.row = w.sp.row0 + it.tok;
-          note.rem = it.rem;
-          note.kvh = w.kvh;
-        }
-        for (int t = it.t0 + from; t < it.t0 + to && ok; ++t) {
-          // a lane's page (of both, where rows have two halves), the same for keys and values
-          int page = -1;
-          const int pages = kTokens >> p.pool.page_shift;
-          const int at = t * kTokens + ((lane / S::H) << p.pool.page_shift);
-          if (!PROMPT) {
-            if (lane < pages * S::H && at < hi && at + (1 << p.pool.page_shift) > lo) {
-              const int32_t* entry = table + (at >> p.pool.page_shift);
-              if (table_ok(p.batch, entry, err)) {
-                page = *entry;
-                if (page < 0 || page >= p.pool.num_pages) {
-                  atomicExch(err, kErrBadPage);
-                  page = -1;
-                } else if (!pool_ok(p.pool, p.pool.pages + page * p.pool.page_stride + w.kvh * p.pool.head_stride,
-                                    p.pool.head_stride)) {
-                  page = -1;
+          if (lane == 0) {
+            sg.table = table;
+            sg.done = 0;
+            sg.row = w.sp.row0 + it.tok;
+            sg.pos = pos;
+            sg.tokens = it.tokens;
+            sg.kvh = w.kvh;
+            sg.t0 = it.t0 + from;
+            sg.t1 = it.t0 + to;
+            sg.lo = lo;
+            sg.hi = hi;
+            sg.whole = from == 0 && to == nt;
+            sg.slot = 2 * blockIdx.x + (from == 0);
+            sg.dirty = sg.bad_tiles = 0;
+            for (int i = 0; i < kMostBad; ++i)
+              for (int k = 0; k < 4; ++k) sg.bad[i][k] = 0;
+            mbar_arrive(&ctl.seg_full[slot.i]);
+          }
+          __syncwarp();
+          slot.next<kSlots>();
+          if (from > 0) {
+            note.cont = to == nt ? 2 : 1;
+          } else if (to < nt) {
+            note.tokens = it.tokens;
+            note.row = w.sp.row0 + it.tok;
+            note.kvh = w.kvh;
+          }
+          if (q_tma) {
+            for (int g = 0; g < NQ; ++g) {
+              if (tiles_of(sg, g) <= 0) continue;
+              ok = ok && __all_sync(0xffffffffu, wait(&ctl.q_empty[g], (qph >> g & 1) ^ 1, err, quit));
+              qph ^= 1u << g;
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&ctl.q_full[g], S::H * 128 * a.T * p.gqa);
+              __syncwarp();
+              if (lane < S::H)
+                tma4(sm + S::q + g * S::tile + lane * S::half, &a.qm, w.kvh * p.gqa, w.sp.row0 + it.tok + g * a.T, lane,
+                     &ctl.q_full[g]);
+            }
+          }
+          for (int t = it.t0 + from; t < it.t0 + to && ok; ++t) {
+            // a lane's page (codes: stored tile; rows of two halves: of both), the same for keys and values
+            int page = -1;
+            const int shift = QUANT ? 4 : p.pool.page_shift;
+            const int at = t * kTokens + ((lane / (QUANT ? 1 : S::H)) << shift);
+            if (!PROMPT) {
+              if (lane < (kTokens >> shift) * (QUANT ? 1 : S::H) && at < hi && at + (1 << shift) > lo) {
+                const int32_t* entry = table + (at >> p.pool.page_shift);
+                if (table_ok(p.batch, entry, err)) {
+                  page = *entry;
+                  if (page < 0 || page >= p.pool.num_pages) {
+                    atomicExch(err, kErrBadPage);
+                    page = -1;
+                  } else if (!pool_ok(p.pool, p.pool.pages + page * p.pool.page_stride + w.kvh * p.pool.head_stride,
+                                      p.pool.head_stride)) {
+                    page = -1;
+                  }
                 }
               }
             }
-          }
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            if (ok) ok = wait(&ctl.empty[st.i], st.phase ^ 1, err, quit);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            uint8_t* dst = sm + S::ring + st.i * S::tile;
-            uint64_t* bar = &ctl.full[st.i];
-            if (PROMPT) {
-              if (lane == 0) mbar_arrive_expect_tx(bar, S::tile);
-              __syncwarp();
-              if (lane < S::H)
-                tma4(dst + lane * S::half, kv ? &a.vm : &a.km, w.sp.row0 + t * kTokens, lane, w.kvh, bar);
-            } else {
-              const uint32_t bytes = 128u << p.pool.page_shift;  // of a page's half
-              const int count = __popc(__ballot_sync(0xffffffffu, page >= 0));
-              if (lane == 0) {
-                if (count)
-                  mbar_arrive_expect_tx(bar, count * bytes);
-                else
-                  mbar_arrive(bar);
+            if constexpr (QUANT) {
+              // eight stored tiles, a lane each, four at a time: no lane waits for a slot that another of its
+              // four fills first
+#pragma unroll 1
+              for (int r = 0; r < 8; r += 4) {
+                if (lane >= r && lane < r + 4) {
+                  const int n = rw.i + lane, wraps = n / a.raw_slots, slot_i = n - wraps * a.raw_slots;
+                  ok = ok && wait(&ctl.raw_empty[slot_i], (rw.phase ^ (wraps & 1)) ^ 1, err, quit);
+                  if (ok) {
+                    uint64_t* bar = &ctl.raw_full[slot_i];
+                    if (page >= 0) {
+                      const int in = at & ((1 << p.pool.page_shift) - 1);
+                      const uint8_t* src = p.pool.pages + page * p.pool.page_stride + w.kvh * p.pool.head_stride +
+                                           static_cast<int64_t>(in / kTile) * p.pool.tile_bytes;
+                      mbar_arrive_expect_tx(bar, p.pool.tile_bytes);
+                      bulk_g2s(sm + S::raw + slot_i * p.pool.tile_bytes, src, p.pool.tile_bytes, bar);
+                    } else {
+                      mbar_arrive(bar);
+                    }
+                  }
+                }
+                ok = __all_sync(0xffffffffu, ok);
               }
-              __syncwarp();
-              if (page >= 0) {
-                const int tiles = 1 << (p.pool.page_shift - 4);
-                tma5(dst + (lane % S::H) * S::half + (lane / S::H) * bytes, &a.km, 0, (page * p.hkv + w.kvh) * tiles,
-                     lane % S::H, kv, bar);
+              rw.i += 8;
+              while (rw.i >= a.raw_slots) {
+                rw.i -= a.raw_slots;
+                rw.phase ^= 1;
+              }
+              issued = issued + 8 < a.raw_slots ? issued + 8 : a.raw_slots;
+            } else {
+#pragma unroll
+              for (int kv = 0; kv < 2; ++kv) {
+                ok = __all_sync(0xffffffffu, ok && wait(&ctl.empty[st.i], st.phase ^ 1, err, quit));
+                if (!ok) break;
+                uint8_t* dst = sm + S::ring + st.i * S::tile;
+                uint64_t* bar = &ctl.full[st.i];
+                if (PROMPT) {
+                  if (lane == 0) mbar_arrive_expect_tx(bar, S::tile);
+                  __syncwarp();
+                  if (lane < S::H)
+                    tma4(dst + lane * S::half, kv ? &a.vm : &a.km, w.sp.row0 + t * kTokens, lane, w.kvh, bar);
+                } else {
+                  const uint32_t bytes = 128u << p.pool.page_shift;  // of a page's half
+                  const int count = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                  if (lane == 0) {
+                    if (count)
+                      mbar_arrive_expect_tx(bar, count * bytes);
+                    else
+                      mbar_arrive(bar);
+                  }
+                  __syncwarp();
+                  if (page >= 0)
+                    tma5(dst + (lane % S::H) * S::half + (lane / S::H) * bytes, &a.km, 0,
+                         (page * p.hkv + w.kvh) << (p.pool.page_shift - 4), lane % S::H, kv, bar);
+                }
+                st.next<S::NST>();
+                if (issued < S::NST) ++issued;
               }
             }
-            st.next<S::NST>();
-            if (issued < S::NST) ++issued;
           }
         }
+        more = walk_next(p, items_T, nt, w);
       }
-      more = walk_next(p, S::R, nt, w);
-    }
-    // no more segments
-    if (ok) ok = wait(&ctl.seg_empty[slot.i], slot.phase ^ 1, err, quit);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok && lane == 0) {
-      ctl.seg[slot.i].done = 1;
-      mbar_arrive(&ctl.seg_full[slot.i]);
-    }
-    if (lane == 0) {
-      Note* notes = reinterpret_cast<Note*>(p.ws);
-      if (in_range(notes + blockIdx.x, sizeof(Note), p.ws, p.ws_hi, err)) notes[blockIdx.x] = note;
-    }
-    // every copy has landed before the CTA ends
-    for (int i = 0; i < issued; ++i) {
-      st.i = st.i ? st.i - 1 : S::NST - 1;
-      if (st.i == S::NST - 1) st.phase ^= 1;
-      mbar_wait(&ctl.full[st.i], st.phase, err, 1u << 16);
-    }
-  } else if (warp == W0 + 1) {
-    // ================= multiplies: scores into columns tS, weights times values into tO
-    if (lane == 0) {
-      constexpr uint32_t f = Fmt<T>::code << 7 | Fmt<T>::code << 10;
-      constexpr uint32_t idO = idesc_f16_f32(kM, D) | f | 1u << 16;  // values run along channels
-      const uint32_t idS = idesc_f16_f32(kM, kTokens) | f | (p.alpha < 0.0f ? 1u << 13 : 0u);  // -q for a scale below 0
-      const uint32_t sq = smem_u32(sm + S::q), sr = smem_u32(sm + S::ring);
-      Stage st = {0, 0}, slot = {0, 0};
-      uint32_t qph[2] = {0, 0}, pph = 0, lookph = 0;
-      bool ok = true;
-      auto scores = [&](int g, int buf, int stage) {
-        const uint64_t dq = smem_desc_sw128(sq + g * S::tile, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = ((k / 4) * S::half + (k % 4) * 32) >> 4;
-          umma_f16(tm + S::tS + kTokens * buf, dq + off, dk + off, idS, k > 0);
-        }
-        umma_commit(&ctl.s_full[buf]);
-      };
-      auto outputs = [&](int g, int buf, int stage, bool first) {
-        const uint64_t dv = smem_desc_sw128(sr + stage * S::tile, S::half, 1024);
-#pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k)
-          umma_f16_ts(tm + S::tO + D * g, tm + S::tS + kTokens * buf + 8 * k, dv + ((2048 * k) >> 4), idO, !first || k > 0);
-      };
-      while (ok) {
-        ok = wait(&ctl.seg_full[slot.i], slot.phase, err, quit);
-        if (!ok) break;
-        const Seg& sg = ctl.seg[slot.i];
-        if (sg.done) break;
-        const int t0 = sg.t0, nt = sg.t1 - t0, pos = sg.pos, rem = sg.rem, rows = sg.rows, hi = sg.hi;
-        int ng[NQ];  // tiles of each query tile
-#pragma unroll
-        for (int g = 0; g < NQ; ++g) {
-          const int r = rows < kM * (g + 1) ? rows : kM * (g + 1);
-          const int end = (pos + (rem + r - 1) / p.gqa) / kTokens + 1;
-          ng[g] = kM * g >= rows ? 0 : (end < sg.t1 ? end : sg.t1) - t0;
-          if (ng[g] > 0) {
-            ok = ok && wait(&ctl.q_full[g], qph[g], err, quit);
-            qph[g] ^= 1;
-          }
-        }
-        mbar_arrive(&ctl.seg_empty[slot.i]);
-        slot.next<kSlots>();
-        ok = ok && wait(&ctl.full[st.i], st.phase, err, quit);
-        if (!ok) break;
-        tc_fence_after_sync();
-        int kst = st.i;  // the stage of the keys in hand
-#pragma unroll
-        for (int g = 0; g < NQ; ++g)
-          if (ng[g] > 0) scores(g, NQ == 1 ? 0 : g, kst);
-        umma_commit(&ctl.empty[kst]);
-        st.next<S::NST>();
-        for (int i = 0; i < nt && ok; ++i) {
-          const Stage v = st;
-          st.next<S::NST>();
-          const bool next = i + 1 < nt;
-          if (NQ == 1 && next) {
-            ok = wait(&ctl.full[st.i], st.phase, err, quit);
-            if (!ok) break;
-            tc_fence_after_sync();
-            scores(0, (i + 1) & 1, st.i);
-            umma_commit(&ctl.empty[st.i]);
-          }
-          if (masked_tile(t0 + i, pos, hi - 1, p.window)) {
-            ok = wait(&ctl.looked[v.i], lookph >> v.i & 1, err, quit);
-            lookph ^= 1u << v.i;
+      // no more segments
+      ok = __all_sync(0xffffffffu, ok && wait(&ctl.seg_empty[slot.i], slot.phase ^ 1, err, quit));
+      if (ok && lane == 0) {
+        ctl.seg[slot.i].done = 1;
+        mbar_arrive(&ctl.seg_full[slot.i]);
+      }
+      if (lane == 0) {
+        Note* notes = reinterpret_cast<Note*>(p.ws);
+        if (in_range(notes + blockIdx.x, sizeof(Note), p.ws, p.ws_hi, err)) notes[blockIdx.x] = note;
+        // every copy has landed before the CTA ends
+        for (int i = 0; i < issued; ++i) {
+          if (QUANT) {
+            rw.i = rw.i ? rw.i - 1 : a.raw_slots - 1;
+            if (rw.i == a.raw_slots - 1) rw.phase ^= 1;
+            mbar_wait(&ctl.raw_full[rw.i], rw.phase, err, 1u << 16);
           } else {
-            ok = wait(&ctl.full[v.i], v.phase, err, quit);
+            st.i = st.i ? st.i - 1 : S::NST - 1;
+            if (st.i == S::NST - 1) st.phase ^= 1;
+            mbar_wait(&ctl.full[st.i], st.phase, err, 1u << 16);
           }
-          if (!ok) break;
-          tc_fence_after_sync();
-          bool have = false;
+        }
+        if (q_tma)
+          for (int g = 0; g < NQ; ++g)
+            if (!ok) mbar_wait(&ctl.q_full[g], (qph >> g & 1) ^ 1, err, 1u << 16);
+      }
+      __syncwarp();
+    } else if (warp == S::WL + 1) {
+      // ================= multiplies: scores into columns tS, weights times values into tO
+      if (lane == 0) {
+        constexpr uint32_t f = Fmt<T>::code << 7 | Fmt<T>::code << 10;
+        constexpr uint32_t idO = idesc_f16_f32(kM, D) | f | 1u << 16;  // values run along channels
+        // -q for a scale below 0 (queries of codes have the sign already)
+        const uint32_t idS = idesc_f16_f32(kM, kTokens) | f | (!QUANT && p.alpha < 0.0f ? 1u << 13 : 0u);
+        const uint32_t sq = smem_u32(sm + S::q), sr = smem_u32(sm + S::ring);
+        Stage st = {0, 0}, slot = {0, 0};
+        uint32_t qph = 0, pph = 0, lookph = 0;
+        bool ok = true;
+        const auto scores = [&](int g, int buf, int stage, bool last) {
+          const uint64_t dq = smem_desc_sw128(sq + g * S::tile, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
 #pragma unroll
-          for (int g = 0; g < NQ; ++g) {
-            if (i >= ng[g]) continue;
-            const int buf = NQ == 1 ? i & 1 : g;
-            ok = ok && wait(&ctl.p_full[buf], pph >> buf & 1, err, quit);
-            pph ^= 1u << buf;
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = ((k / 4) * S::half + (k % 4) * 32) >> 4;
+            umma_f16(tm + S::tS + kTokens * buf, dq + off, dk + off, idS, k > 0);
+          }
+          umma_commit(&ctl.s_full[buf]);
+          if (last) umma_commit(&ctl.q_empty[g]);
+        };
+        const auto outputs = [&](int g, int buf, int stage, int part, bool first) {
+          const uint64_t dv = smem_desc_sw128(sr + stage * S::tile, S::half, 1024);
+#pragma unroll
+          for (int k = 0; k < kTokens / 32; ++k) {
+            const int kk = part * (kTokens / 32) + k;
+            umma_f16_ts(tm + S::tO + D * g, tm + S::tS + kTokens * buf + 8 * kk, dv + ((2048 * kk) >> 4), idO, !first || kk > 0);
+          }
+        };
+        while (ok) {
+          ok = wait(&ctl.seg_full[slot.i], slot.phase, err, quit);
+          if (!ok) break;
+          const Seg& sg = ctl.seg[slot.i];
+          if (sg.done) break;
+          const int t0 = sg.t0, nt = sg.t1 - t0, pos = sg.pos, hi = sg.hi;
+          int ng[NQ];  // tiles of each query tile
+#pragma unroll
+          for (int g = 0; g < NQ; ++g) ng[g] = tiles_of(sg, g);
+          mbar_arrive(&ctl.seg_empty[slot.i]);
+          slot.next<kSlots>();
+          ok = wait(&ctl.full[st.i], st.phase, err, quit);
+          if (!ok) break;
+          const int kst = st.i;
+#pragma unroll
+          for (int g = 0; g < NQ; ++g)
+            if (ng[g] > 0) {
+              ok = ok && wait(&ctl.q_full[g], qph >> g & 1, err, quit);
+              qph ^= 1u << g;
+              if (!ok) break;
+              tc_fence_after_sync();
+              scores(g, NQ == 1 ? 0 : g, kst, ng[g] == 1);
+            }
+          if (!ok) break;
+          umma_commit(&ctl.empty[kst]);
+          st.next<S::NST>();
+          for (int i = 0; i < nt && ok; ++i) {
+            const Stage v = st;
+            st.next<S::NST>();
+            const bool next = i + 1 < nt;
+            if (NQ == 1 && next) {
+              ok = wait(&ctl.full[st.i], st.phase, err, quit);
+              if (!ok) break;
+              tc_fence_after_sync();
+              scores(0, (i + 1) & 1, st.i, i + 2 == nt);
+              umma_commit(&ctl.empty[st.i]);
+            }
+            if (!QUANT && masked_tile(t0 + i, pos, hi - 1, p.window)) {
+              ok = wait(&ctl.looked[v.i], lookph >> v.i & 1, err, quit);
+              lookph ^= 1u << v.i;
+            } else {
+              ok = wait(&ctl.full[v.i], v.phase, err, quit);
+            }
             if (!ok) break;
             tc_fence_after_sync();
-            outputs(g, buf, v.i, i == 0);
-            if (NQ == 1 || i + 1 == ng[g]) umma_commit(&ctl.o_done[buf]);
-            if (NQ > 1 && i + 1 < ng[g]) {
-              if (!have) {
-                ok = wait(&ctl.full[st.i], st.phase, err, quit);
-                have = true;
+            bool have = false;
+#pragma unroll
+            for (int g = 0; g < NQ; ++g) {
+              if (i >= ng[g]) continue;
+              const int buf = NQ == 1 ? i & 1 : g;
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                ok = ok && wait(&ctl.p_full[buf][part], pph >> buf & 1, err, quit);
                 if (!ok) break;
                 tc_fence_after_sync();
+                outputs(g, buf, v.i, part, i == 0);
               }
-              scores(g, g, st.i);
+              if (!ok) break;
+              pph ^= 1u << buf;
+              if (NQ == 1 || i + 1 == ng[g]) umma_commit(&ctl.o_done[buf]);
+              if (NQ > 1 && i + 1 < ng[g]) {
+                if (!have) {
+                  ok = wait(&ctl.full[st.i], st.phase, err, quit);
+                  have = true;
+                  if (!ok) break;
+                  tc_fence_after_sync();
+                }
+                scores(g, g, st.i, i + 2 == ng[g]);
+              }
+            }
+            if (!ok) break;
+            umma_commit(&ctl.empty[v.i]);
+            if (next) {
+              if (NQ > 1) umma_commit(&ctl.empty[st.i]);
+              st.next<S::NST>();
             }
           }
-          if (!ok) break;
-          umma_commit(&ctl.empty[v.i]);
-          if (next) {
-            if (NQ > 1) umma_commit(&ctl.empty[st.i]);
-            st.next<S::NST>();
-          }
         }
+        umma_commit(&ctl.fin);  // nothing is under way when the columns are given back
+        mbar_wait(&ctl.fin, 0, err, 1u << 20);
       }
-      umma_commit(&ctl.fin);  // nothing is under way when the columns are given back
-      mbar_wait(&ctl.fin, 0, err, 1u << 20);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp > W0) {
-    // ================= look through the values of masked tiles
-    Stage st = {0, 0}, slot = {0, 0};
+  } else if (warp >= S::W0) {
+    // ================= helpers: stage queries where they are not copied; codes: unpack; 16 bits: look
+    // through the values of masked tiles
+    if constexpr (S::split) fewer_registers<S::regs_others>();
+    const int me = tid - S::W0 * 32;
+    Stage st = {0, 0}, slot = {0, 0}, rw = {0, 0};
+    uint32_t qph = 0;
     bool ok = true;
     while (ok) {
       ok = __all_sync(0xffffffffu, wait(&ctl.seg_full[slot.i], slot.phase, err, quit));
       if (!ok) break;
       Seg& sg = ctl.seg[slot.i];
       if (sg.done) break;
+      if (!q_tma) {
+        for (int g = 0; g < NQ; ++g) {
+          if (tiles_of(sg, g) <= 0) continue;
+          ok = __all_sync(0xffffffffu, ok && wait(&ctl.q_empty[g], (qph >> g & 1) ^ 1, err, quit));
+          qph ^= 1u << g;
+          if (!ok) break;
+          const int left = sg.tokens - g * a.T, rows = (left < a.T ? left : a.T) * p.gqa;
+          stage_queries<T, D, QUANT>(a, sg, g, rows, sm + S::q + g * S::tile,
+                                     reinterpret_cast<float2*>(sm + S::factors) + g * kM, me, 32 * S::helpers);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.q_full[g]);
+        }
+      }
       int seen = 0;
       for (int t = sg.t0; t < sg.t1 && ok; ++t) {
-        // every stage in turn, so that none is mistaken for its last use
-        ok = __all_sync(0xffffffffu, wait(&ctl.full[st.i], st.phase, err, quit));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(&ctl.empty[st.i]);
-        st.next<S::NST>();
-        const Stage v = st;
-        st.next<S::NST>();
-        ok = __all_sync(0xffffffffu, wait(&ctl.full[v.i], v.phase, err, quit));
-        if (!ok) break;
-        if (!masked_tile(t, sg.pos, sg.hi - 1, p.window)) {
-          if (lane == 0) mbar_arrive(&ctl.empty[v.i]);
-          continue;
-        }
-        uint8_t* tile = sm + S::ring + v.i * S::tile;
-        const int me = tid - (W0 + 2) * 32;
-#pragma unroll 8
-        for (int i = me; i < S::tile / 16; i += 64) {
-          uint4* at = reinterpret_cast<uint4*>(tile) + i;
-          uint4 x = *at;
-          constexpr uint32_t E = Fmt<T>::expo, C = Fmt<T>::carry;
-          uint32_t any = ((x.x & E) + C) | ((x.y & E) + C) | ((x.z & E) + C) | ((x.w & E) + C);
-          if (any & 0x80008000u) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            for (int k = 0; k < 4; ++k) {
-              if (((w[k] & E) + C) & 0x8000u) w[k] &= 0xffff0000u;
-              if (((w[k] & E) + C) & 0x80000000u) w[k] &= 0xffffu;
+        const bool masked = masked_tile(t, sg.pos, sg.hi - 1, p.window);
+        if constexpr (QUANT) {
+          // both of the tile's stages
+          const Stage k = st;
+          st.next<S::NST>();
+          const Stage v = st;
+          st.next<S::NST>();
+          ok = wait(&ctl.empty[k.i], k.phase ^ 1, err, quit);
+          ok = __all_sync(0xffffffffu, ok && wait(&ctl.empty[v.i], v.phase ^ 1, err, quit));
+          if (!ok) break;
+          uint8_t *kt = sm + S::ring + k.i * S::tile, *vt = sm + S::ring + v.i * S::tile;
+          float4* scales = reinterpret_cast<float4*>(sm + S::scales) + (k.i / 2) * (kTokens / 2);
+          for (int c = 0; c < 8; ++c) {
+            ok = __all_sync(0xffffffffu, ok && wait(&ctl.raw_full[rw.i], rw.phase, err, quit));
+            if (!ok) break;
+            unpack_any<D>(p.pool.kb, p.pool.vb, sm + S::raw + rw.i * p.pool.tile_bytes, kt, vt, scales, c * 16,
+                          t * kTokens + c * 16, sg, masked, seen, me, &sg.dirty, sg.bad[seen < kMostBad ? seen : 0]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.raw_empty[rw.i]);
+            if (++rw.i == a.raw_slots) {
+              rw.i = 0;
+              rw.phase ^= 1;
             }
-            *at = x;
-            const int tok = (i * 16 % S::half) / 128;
-            if (seen < kMostBad) atomicOr(&sg.bad[seen][tok / 32], 1u << (tok % 32));
           }
-        }
-        if (me == 0 && seen < kMostBad) sg.bad_tile[seen] = t;
-        if (me == 0) sg.bad_tiles = seen + 1;
-        ++seen;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl.looked[v.i]);
-          mbar_arrive(&ctl.empty[v.i]);
+          if (!ok) break;
+          if (masked) {
+            if (me == 0 && seen < kMostBad) {
+              sg.bad_tile[seen] = t;
+              sg.bad_tiles = seen + 1;
+            }
+            ++seen;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl.full[k.i]);
+            mbar_arrive(&ctl.full[v.i]);
+          }
+        } else {
+          // every stage in turn, so that none is mistaken for its last use
+          ok = __all_sync(0xffffffffu, wait(&ctl.full[st.i], st.phase, err, quit));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&ctl.empty[st.i]);
+          st.next<S::NST>();
+          const Stage v = st;
+          st.next<S::NST>();
+          ok = __all_sync(0xffffffffu, wait(&ctl.full[v.i], v.phase, err, quit));
+          if (!ok) break;
+          if (!masked) {
+            if (lane == 0) mbar_arrive(&ctl.empty[v.i]);
+            continue;
+          }
+          uint8_t* tile = sm + S::ring + v.i * S::tile;
+#pragma unroll 8
+          for (int i = me; i < S::tile / 16; i += 32 * S::helpers) {
+            uint4* at = reinterpret_cast<uint4*>(tile) + i;
+            uint4 x = *at;
+            constexpr uint32_t E = Fmt<T>::expo, C = Fmt<T>::carry;
+            const uint32_t any = ((x.x & E) + C) | ((x.y & E) + C) | ((x.z & E) + C) | ((x.w & E) + C);
+            if (any & 0x80008000u) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+              for (int k = 0; k < 4; ++k) {
+                if (((w[k] & E) + C) & 0x8000u) w[k] &= 0xffff0000u;
+                if (((w[k] & E) + C) & 0x80000000u) w[k] &= 0xffffu;
+              }
+              *at = x;
+              const int tok = (i * 16 % S::half) / 128;
+              sg.dirty = 1;
+              if (seen < kMostBad) atomicOr(&sg.bad[seen][tok / 32], 1u << (tok % 32));
+            }
+          }
+          if (me == 0 && seen < kMostBad) {
+            sg.bad_tile[seen] = t;
+            sg.bad_tiles = seen + 1;
+          }
+          ++seen;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl.looked[v.i]);
+            mbar_arrive(&ctl.empty[v.i]);
+          }
         }
       }
       if (!ok) break;
@@ -762,51 +1172,45 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
     }
   } else {
     // ================= softmax: a thread a row
+    if constexpr (S::split) more_registers<S::regs_softmax>();
     const int g = NQ == 1 ? 0 : warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t tO = tm + S::tO + D * g + lanes;
-    uint8_t* qs = sm + S::q + g * S::tile;
-    const float alpha = fabsf(p.alpha);
-    const f2 alpha2 = f2_of(alpha, alpha);
+    const int my_tok = r / p.gqa, my_head = r - my_tok * p.gqa;
+    const bool wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     Stage slot = {0, 0};
-    uint32_t sph[2] = {0, 0}, oph = 0, gph = 0;  // phases
+    uint32_t sph = 0, oph = 0, qph = 0, kst = 0;  // phases; tiles so far: the key scales' stage
     bool ok = true;
     while (ok) {
       ok = __all_sync(0xffffffffu, wait(&ctl.seg_full[slot.i], slot.phase, err, quit));
       if (!ok) break;
       const Seg& sg = ctl.seg[slot.i];
       if (sg.done) break;
-      const int rows = sg.rows - kM * g < kM ? sg.rows - kM * g : kM;
-      if (rows > 0) {
-        const int x0 = sg.rem + kM * g;  // row r is head (x0 + r) % gqa of token (x0 + r) / gqa
-        const int pos = sg.pos, t0 = sg.t0;
-        const int first_lim = pos + x0 / p.gqa, last_lim = pos + (x0 + rows - 1) / p.gqa;
-        const int end = last_lim / kTokens + 1;
-        const int nt = (end < sg.t1 ? end : sg.t1) - t0;
-        const int lim = r < rows ? pos + (x0 + r) / p.gqa : last_lim;
+      const int left = sg.tokens - g * a.T, tokens = left < a.T ? left : a.T;
+      if (tokens > 0) {
+        const int t0 = sg.t0, nt = tiles_of(sg, g);
+        const int first_lim = sg.pos + g * a.T, last_lim = first_lim + tokens - 1;
+        const bool live = my_tok < tokens;
+        const int lim = live ? first_lim + my_tok : last_lim;
         const int low = p.window ? lim - p.window + 1 : 0;
         float m = -INFINITY, l = 0.0f;
         if (nt > 0) {
-          // ---- query rows into shared memory
-#pragma unroll 4
-          for (int i = r; i < kM * (D / 8); i += 128) {
-            const int row = i / (D / 8), ch = i % (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < rows) {
-              const int tk = (x0 + row) / p.gqa, hh = x0 + row - tk * p.gqa;
-              const T* src = reinterpret_cast<const T*>(p.q.data) + (static_cast<int64_t>(sg.row) + tk) * p.q.token_stride +
-                             (sg.kvh * p.gqa + hh) * p.q.head_stride + 8 * ch;
-              if (rows_ok(p.q, src, 16, err)) rows::load8(src, p.q_vec, v);
-            }
-            *reinterpret_cast<uint4*>(qs + (ch / 8) * S::half + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+          float alpha = fabsf(p.alpha), qsum = 0.0f;
+          if (QUANT) {
+            ok = __all_sync(0xffffffffu, wait(&ctl.q_full[g], qph, err, quit));
+            qph ^= 1;
+            if (!ok) break;
+            const float2 fq = reinterpret_cast<const float2*>(sm + S::factors)[g * kM + r];
+            alpha *= fq.x;
+            qsum = fq.y;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.q_empty[g]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.q_full[g]);
+          const f2 alpha2 = f2_of(alpha, alpha), qsum2 = f2_of(qsum, qsum);
           for (int i = 0; i < nt; ++i) {
             const int buf = NQ == 1 ? i & 1 : g;
-            ok = __all_sync(0xffffffffu, wait(&ctl.s_full[buf], sph[NQ == 1 ? buf : 0], err, quit));
-            sph[NQ == 1 ? buf : 0] ^= 1;
+            ok = __all_sync(0xffffffffu, wait(&ctl.s_full[buf], sph >> buf & 1, err, quit));
+            sph ^= 1u << buf;
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t tS = tm + S::tS + kTokens * buf + lanes;
@@ -815,6 +1219,24 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
             for (int k = 0; k < 4; ++k) tmem_ld32(tS + 32 * k, x[k]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_ld_wait(x[k]);
+            if constexpr (QUANT) {  // s (q.c) + z sum(q)
+              // (complete since before the scores; it makes the scales visible here)
+              ok = __all_sync(0xffffffffu, wait(&ctl.full[2 * (kst & 1)], kst >> 1 & 1, err, quit));
+              if (!ok) break;
+              const float4* sc = reinterpret_cast<const float4*>(sm + S::scales) + (kst & 1) * (kTokens / 2);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  const float4 z = sc[16 * k + c];
+                  const f2 y = fma2(f2_of(__uint_as_float(x[k][2 * c]), __uint_as_float(x[k][2 * c + 1])), f2_of(z.x, z.y),
+                                    rows::mul2(f2_of(z.z, z.w), qsum2));
+                  float u, v;
+                  f2_get(y, u, v);
+                  x[k][2 * c] = __float_as_uint(u);
+                  x[k][2 * c + 1] = __float_as_uint(v);
+                }
+            }
             const int tb = (t0 + i) * kTokens;
             if (tb + kTokens - 1 > first_lim || (p.window && tb <= last_lim - p.window)) {
               const int a0 = low - tb, a1 = lim - tb;  // columns a0 .. a1 are seen
@@ -862,28 +1284,30 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
             f2 sum[2] = {f2_of(0.0f, 0.0f), f2_of(0.0f, 0.0f)};
             T* const type = nullptr;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[32];
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[16];
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const uint32_t *xx = &x[2 * h + c / 16][2 * (c % 16)];
+              for (int c = 0; c < 16; ++c) {
                 float u, v;
-                f2_get(fma2(f2_of(__uint_as_float(xx[0]), __uint_as_float(xx[1])), alpha2, nm2), u, v);
+                f2_get(fma2(f2_of(__uint_as_float(x[k][2 * c]), __uint_as_float(x[k][2 * c + 1])), alpha2, nm2), u, v);
                 u = ex2(u);
                 v = ex2(v);
                 sum[c & 1] = add2(sum[c & 1], f2_of(u, v));
                 w[c] = pack2(type, u, v);
               }
-              tmem_st32(tS + 32 * h, w);
+              tmem_st16(tS + 16 * k, w);
+              if (k & 1) {
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_full[buf][k / 2]);
+              }
             }
             float s0, s1, s2, s3;
             f2_get(sum[0], s0, s1);
             f2_get(sum[1], s2, s3);
             l += (s0 + s1) + (s2 + s3);
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.p_full[buf]);
+            ++kst;
           }
           if (!ok) break;
           if (NQ == 1) {
@@ -897,11 +1321,13 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
           if (!ok) break;
           tc_fence_after_sync();
         }
+        // tiles that only the other query tile saw
+        if (QUANT) kst += sg.t1 - t0 - (nt > 0 ? nt : 0);
         // ---- the rows' results
-        const int tk = (x0 + r) / p.gqa, head = sg.kvh * p.gqa + x0 + r - tk * p.gqa;
-        const int64_t at = (static_cast<int64_t>(sg.row) + tk) * p.hkv * p.gqa + head;
+        const int64_t at = (static_cast<int64_t>(sg.row) + g * a.T + my_tok) * p.hkv * p.gqa + sg.kvh * p.gqa + my_head;
         if (sg.whole) {
           const float inv = l != 0.0f ? __fdividef(1.0f, l) : 0.0f;
+          uint8_t* dst = static_cast<uint8_t*>(p.out) + at * D * 2;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -910,23 +1336,30 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
             float y[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) y[k] = l != 0.0f ? __uint_as_float(o[k]) * inv : 0.0f;
-            if (sg.bad_tiles && l != 0.0f) add_bad<T, D, PROMPT>(p, sg, low, lim, c, y);
-            if (r < rows) {
-              T* const type = nullptr;
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * D + c);
+            to_channels<QUANT>(p.pool.vb, y);
+            if (sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
+            uint32_t w[2][8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                dst[k] = make_uint4(pack2(type, y[8 * k], y[8 * k + 1]), pack2(type, y[8 * k + 2], y[8 * k + 3]),
-                                    pack2(type, y[8 * k + 4], y[8 * k + 5]), pack2(type, y[8 * k + 6], y[8 * k + 7]));
+            for (int k = 0; k < 16; ++k) {
+              if (QUANT)
+                w[k / 8][k % 8] = a.bf16 ? pack2(static_cast<__nv_bfloat16*>(nullptr), y[2 * k], y[2 * k + 1])
+                                         : pack2(static_cast<__half*>(nullptr), y[2 * k], y[2 * k + 1]);
+              else
+                w[k / 8][k % 8] = pack2(static_cast<T*>(nullptr), y[2 * k], y[2 * k + 1]);
+            }
+            if (live) {
+              store32(dst + 2 * c, wide_out, w[0]);
+              store32(dst + 2 * c + 32, wide_out, w[1]);
             }
           }
-          if (p.lse && r < rows)
+          if (p.lse && live)
             p.lse[at] = l == 0.0f ? -INFINITY : ((m - Fmt<T>::room) + log2f(l)) * 0.69314718055994531f;
         } else {
           // m, l of every row, then the outputs, four channels of all rows together
           float* part = reinterpret_cast<float*>(p.ws + a.partials) + static_cast<int64_t>(sg.slot) * a.slot_rows * (D + 2);
           const int rr = kM * g + r;
-          if (rr < a.slot_rows && in_range(part, a.slot_rows * (D + 2) * 4, p.ws, p.ws_hi, err)) {
+          const bool fits = rr < a.slot_rows && in_range(part, a.slot_rows * (D + 2) * 4, p.ws, p.ws_hi, err);
+          if (fits) {
             part[rr] = m;
             part[a.slot_rows + rr] = l;
           }
@@ -939,8 +1372,9 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
               float y[32];
 #pragma unroll
               for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]);
-              if (sg.bad_tiles && l != 0.0f) add_bad<T, D, PROMPT>(p, sg, low, lim, c, y);
-              if (rr < a.slot_rows) {
+              to_channels<QUANT>(p.pool.vb, y);
+              if (sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
+              if (fits) {
                 float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows) + rr;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -950,13 +1384,8 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
           }
         }
         tc_fence_before_sync();
-        // the query rows of the next segment are written by all of the group's threads
-        // (a bounded wait: a warp whose wait gave up does not come)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.group[g]);
-        ok = __all_sync(0xffffffffu, wait(&ctl.group[g], gph, err, quit));
-        gph ^= 1;
-        if (!ok) break;
+      } else if (QUANT) {
+        kst += sg.t1 - sg.t0;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.seg_empty[slot.i]);
@@ -965,7 +1394,7 @@ __global__ void __launch_bounds__(Shape<D, NQ>::threads, 1) paged_chunk_kernel(c
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == W0 + 1) {
+  if (warp == S::WL + 1) {
     tc_fence_after_sync();
     tmem_dealloc(tm, 512);
   }
@@ -991,14 +1420,15 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ 
 
 // Joins the pieces of the items that several CTAs shared: block (i, y) takes 32
 // rows of the item whose first piece is CTA i's.
-template <typename T, int D>
+template <bool BF16, int D>
 __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const __grid_constant__ Launch a) {
   grid_dep_wait();
   const PagedChunkParams& p = a.p;
   const Note* notes = reinterpret_cast<const Note*>(p.ws);
   const Note n = notes[blockIdx.x];
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), c0 = (threadIdx.x >> 5) * (D / 8);
-  if (n.rows <= 0 || r >= n.rows || r >= a.slot_rows) return;
+  const int tk = r % kM / p.gqa, token = r / kM * a.T + tk;
+  if (r % kM >= a.T * p.gqa || token >= n.tokens || r >= a.slot_rows) return;
   const float* parts = reinterpret_cast<const float*>(p.ws + a.partials);
   const int64_t size = static_cast<int64_t>(a.slot_rows) * (D + 2);
   int last = blockIdx.x;
@@ -1030,17 +1460,18 @@ __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const __grid_cons
       o[4 * c + 3] = fmaf(v.w, w, o[4 * c + 3]);
     }
   }
-  const int tk = (n.rem + r) / p.gqa, head = n.kvh * p.gqa + n.rem + r - tk * p.gqa;
-  const int64_t row = static_cast<int64_t>(n.row) + tk;
+  const int head = n.kvh * p.gqa + r % kM - tk * p.gqa;
+  const int64_t row = static_cast<int64_t>(n.row) + token;
   if (n.row < 0 || row >= p.n || head < 0 || head >= p.hkv * p.gqa) return;
   const int64_t at = row * p.hkv * p.gqa + head;
   const float inv = 1.0f / l;
+  using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
   T* const type = nullptr;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + at * D + c0);
 #pragma unroll
   for (int c = 0; c < D / 8; c += 2)
     dst[c / 2] = l == 0.0f ? 0u : pack2(type, o[c] * inv, o[c + 1] * inv);
-  if (p.lse && c0 == 0) p.lse[at] = l == 0.0f ? -INFINITY : ((top - Fmt<T>::room) + log2f(l)) * 0.69314718055994531f;
+  if (p.lse && c0 == 0) p.lse[at] = l == 0.0f ? -INFINITY : ((top - a.room) + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace chunk
