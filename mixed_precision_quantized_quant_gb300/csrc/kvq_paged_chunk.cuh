@@ -468,34 +468,45 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t mask, int k, 
   return h2_as_u32(__hfma2(e, __float2half2_rn(sc), __float2half2_rn(-1024.0f * sc - mid)));
 }
 template <int BITS>
-__device__ __forceinline__ void unpack16(const uint8_t* src, float mid, uint32_t (&h)[8]) {
-  if constexpr (BITS == 8) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[2 * i] = code_pair(w[i], 0x00ff00ffu, 0, mid);
-      h[2 * i + 1] = code_pair(w[i] >> 8, 0x00ff00ffu, 0, mid);
-    }
-  } else if constexpr (BITS == 4) {
-    const uint2 x = *reinterpret_cast<const uint2*>(src);
-    const uint32_t w[2] = {x.x, x.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      h[4 * i] = code_pair(w[i], 0x000f000fu, 0, mid);
-      h[4 * i + 1] = code_pair(w[i], 0x000f000fu, 4, mid);
-      h[4 * i + 2] = code_pair(w[i] >> 8, 0x000f000fu, 0, mid);
-      h[4 * i + 3] = code_pair(w[i] >> 8, 0x000f000fu, 4, mid);
-    }
-  } else {
-    const uint32_t x = *reinterpret_cast<const uint32_t*>(src), y = x >> 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = code_pair(x, 0x00030003u, 2 * i, mid);
-      h[4 + i] = code_pair(y, 0x00030003u, 2 * i, mid);
+struct Codes {  // sixteen as they are stored
+  static constexpr int N = BITS / 2;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const uint8_t* src) {
+    if constexpr (N == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(src);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (N == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      w[0] = x.x, w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(src);
     }
   }
-}
+  __device__ __forceinline__ void unpack(float mid, uint32_t (&h)[8]) const {
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[2 * i] = code_pair(w[i], 0x00ff00ffu, 0, mid);
+        h[2 * i + 1] = code_pair(w[i] >> 8, 0x00ff00ffu, 0, mid);
+      }
+    } else if constexpr (BITS == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        h[4 * i] = code_pair(w[i], 0x000f000fu, 0, mid);
+        h[4 * i + 1] = code_pair(w[i], 0x000f000fu, 4, mid);
+        h[4 * i + 2] = code_pair(w[i] >> 8, 0x000f000fu, 0, mid);
+        h[4 * i + 3] = code_pair(w[i] >> 8, 0x000f000fu, 4, mid);
+      }
+    } else {
+      const uint32_t y = w[0] >> 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[i] = code_pair(w[0], 0x00030003u, 2 * i, mid);
+        h[4 + i] = code_pair(y, 0x00030003u, 2 * i, mid);
+      }
+    }
+  }
+};
 // Channel of place i (of 16) in that order.
 __host__ __device__ constexpr int code_channel(int bits, int i) {
   const int j = i / 2, k = i % 2;
@@ -514,50 +525,59 @@ __device__ __forceinline__ void store_run(uint8_t* tile, int row, int u, const u
   *reinterpret_cast<uint4*>(at + (((c + 1 - odd) ^ x) << 4)) = odd ? a : b;
 }
 
-// One stored tile of 16 tokens (tokens t16 .. of the 128-token tile) into the
-// key and the value operand: keys as codes less their middle, the scales and
-// what they are to be added as fp32; values as numbers, rounded to fp16 once.
-// Tokens outside lo .. hi, and in masked tiles those whose scale or zero is no
-// number, get values of 0.
+// Four stored tiles of 16 tokens (tokens t16 .. of the 128-token tile, positions
+// pos ..) into the key and the value operand: keys as codes less their middle,
+// the scales and what they are to be added as fp32; values as numbers, rounded
+// to fp16 once.  Tokens outside lo .. hi, and in masked tiles those whose scale
+// or zero is no number, get values of 0.  All is read before anything is worked
+// on: one tile after another took 500 ns each, hardly any of them at work.
 template <int D, int KB, int VB>
-__device__ __forceinline__ void unpack_tile(const uint8_t* raw, uint8_t* kt, uint8_t* vt, float4* scales, int t16, int pos,
-                                            const Seg& sg, bool masked, int nth, int tid, int* dirty, uint32_t* bad) {
+__device__ __forceinline__ void unpack_four(const uint8_t* raw, int tile_bytes, const int (&slots)[4], uint64_t* freed, uint8_t* kt,
+                                            uint8_t* vt, float4* scales, int t16, int pos, Seg& sg, bool masked, int nth, int tid) {
   constexpr int U = D / 16, rk = D / 8 * KB, rv = D / 8 * VB, HALF = kTokens * 128;
-  const int u = tid % U, i = tid / U % 16;  // D = 64: half of the threads take keys, half values
-  const uint8_t* sz = raw + 16 * (rk + rv) + tile_key_row(i) * 8;
+  constexpr float mid = KB == 8 ? 128.0f : KB == 4 ? 8.0f : 2.0f;
+  const int u = tid % U, i = tid / U % 16, r = tile_key_row(i);
+  // D = 64: half of the threads take keys, half values
   const bool keys = D == 128 || tid < 16 * U, values = D == 128 || tid >= 16 * U;
-  uint32_t h[8];
-  if (keys) {
-    constexpr float mid = KB == 8 ? 128.0f : KB == 4 ? 8.0f : 2.0f;
-    const int r = tile_key_row(i);
-    unpack16<KB>(raw + r * rk + ((u * 2 * KB) ^ tile_key_xor(rk, r)), mid, h);
-    store_run<HALF>(kt, t16 + i, u, h);
-    if (u == 0) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(sz));
-      float* to = reinterpret_cast<float*>(scales + (t16 + i) / 2) + (i & 1);
-      to[0] = f.x;
-      to[2] = fmaf(f.x, mid, f.y);
-    }
-  }
-  if (values) {
-    constexpr float mid = VB == 8 ? 128.0f : VB == 4 ? 8.0f : 2.0f;
-    __half2 f = *reinterpret_cast<const __half2*>(sz + 4);
-    const bool in = pos + i >= sg.lo && pos + i < sg.hi;
-    const uint32_t e = h2_as_u32(f);
-    const bool fine = ((e & 0x7c00u) != 0x7c00u) && ((e & 0x7c000000u) != 0x7c000000u);
-    if (!in || (masked && !fine)) {
-      if (in && u == 0) {
-        *dirty = 1;
-        if (nth < kMostBad) atomicOr(bad + (t16 + i) / 32, 1u << ((t16 + i) % 32));
-      }
+  const int k_at = r * rk + ((u * 2 * KB) ^ tile_key_xor(rk, r)), v_at = 16 * rk + i * rv + ((u * 2 * VB) ^ tile_val_xor(rv, i));
+  Codes<KB> kc[4];
+  Codes<VB> vc[4];
+  uint2 sz[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = 0;
-    } else {
-      unpack16<VB>(raw + 16 * rk + i * rv + ((u * 2 * VB) ^ tile_val_xor(rv, i)), 0.0f, h);
-      (void)mid;
+  for (int c = 0; c < 4; ++c) {
+    const uint8_t* t = raw + slots[c] * tile_bytes;
+    sz[c] = *reinterpret_cast<const uint2*>(t + 16 * (rk + rv) + r * 8);
+    if (keys) kc[c].load(t + k_at);
+    if (values) vc[c].load(t + v_at);
+  }
+  __syncwarp();
+  if ((tid & 31) == 0)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mbar_arrive(freed + slots[c]);
+  const int lo = sg.lo, hi = sg.hi;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t h[8];
+    const int at = t16 + 16 * c + i;
+    if (keys) {
+      kc[c].unpack(mid, h);
+      store_run<HALF>(kt, at, u, h);
+      if (u == 0) {
+        const float2 f = __half22float2(u32_as_h2(sz[c].x));
+        float* to = reinterpret_cast<float*>(scales + at / 2) + (at & 1);
+        to[0] = f.x;
+        to[2] = fmaf(f.x, mid, f.y);
+      }
+    }
+    if (values) {
+      const __half2 f = u32_as_h2(sz[c].y);
+      const bool in = pos + 16 * c + i >= lo && pos + 16 * c + i < hi;
+      const bool fine = (sz[c].y & 0x7c00u) != 0x7c00u && (sz[c].y & 0x7c000000u) != 0x7c000000u;
+      const bool none = !in || (masked && !fine);
+      vc[c].unpack(0.0f, h);
       const __half2 s = __low2half2(f), z = __high2half2(f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hfma2(u32_as_h2(h[j]), s, z));
+      for (int j = 0; j < 8; ++j) h[j] = none ? 0u : h2_as_u32(__hfma2(u32_as_h2(h[j]), s, z));
       // a last step past the greatest fp16 (a scale rounded up) stays finite
       const float top = fabsf(__low2float(f)) * ((1 << VB) - 1) + fabsf(__high2float(f));
       if (top > 65504.0f) {
@@ -565,16 +585,21 @@ __device__ __forceinline__ void unpack_tile(const uint8_t* raw, uint8_t* kt, uin
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hmax2_nan(__hmin2_nan(u32_as_h2(h[j]), lim), __hneg2(lim)));
       }
+      if (in && none && u == 0) {
+        sg.dirty = 1;
+        if (nth < kMostBad) atomicOr(&sg.bad[nth][at / 32], 1u << (at % 32));
+      }
+      store_run<HALF>(vt, at, u, h);
     }
-    store_run<HALF>(vt, t16 + i, u, h);
   }
 }
 
 template <int D>
-__device__ __forceinline__ void unpack_any(int kb, int vb, const uint8_t* raw, uint8_t* kt, uint8_t* vt, float4* scales, int t16,
-                                           int pos, const Seg& sg, bool masked, int nth, int tid, int* dirty, uint32_t* bad) {
+__device__ __forceinline__ void unpack_any(int kb, int vb, const uint8_t* raw, int tile_bytes, const int (&slots)[4], uint64_t* freed,
+                                           uint8_t* kt, uint8_t* vt, float4* scales, int t16, int pos, Seg& sg, bool masked, int nth,
+                                           int tid) {
   const auto with = [&](auto k, auto v) {
-    unpack_tile<D, decltype(k)::value, decltype(v)::value>(raw, kt, vt, scales, t16, pos, sg, masked, nth, tid, dirty, bad);
+    unpack_four<D, decltype(k)::value, decltype(v)::value>(raw, tile_bytes, slots, freed, kt, vt, scales, t16, pos, sg, masked, nth, tid);
   };
   using two = std::integral_constant<int, 2>;
   using four = std::integral_constant<int, 4>;
@@ -605,20 +630,31 @@ __device__ __forceinline__ void stage_queries(const Launch& a, const Seg& sg, in
   const PagedChunkParams& p = a.p;
   constexpr int U = D / 16, HALF = kTokens * 128;
   const int u = me % U, per = n / U;
-#pragma unroll (QUANT ? 2 : 4)
-  for (int r0 = 0; r0 < kM; r0 += per) {
-    const int row = r0 + me / U;
-    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (row < rows) {
-      const int tk = row / p.gqa, hh = row - tk * p.gqa;
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q.data) +
-                            (static_cast<int64_t>(sg.row) + g * a.T + tk) * p.q.token_stride +
-                            (sg.kvh * p.gqa + hh) * p.q.head_stride + 16 * u;
-      if (rows_ok(p.q, src, 32, p.pool.err)) {
-        rows::load8(src, p.q_vec, x[0]);
-        rows::load8(src + 8, p.q_vec, x[1]);
+  if (QUANT)
+    for (int r = rows + me; r < kM; r += n) factors[r] = make_float2(1.0f, 0.0f);
+  constexpr int AHEAD = 4;  // passes whose rows are asked for together
+#pragma unroll 1
+  for (int r1 = 0; r1 < rows; r1 += AHEAD * per) {
+    uint4 xs[AHEAD][2];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int row = r1 + k * per + me / U;
+      xs[k][0] = xs[k][1] = make_uint4(0, 0, 0, 0);
+      if (row < rows) {
+        const int tk = row / p.gqa, hh = row - tk * p.gqa;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q.data) +
+                              (static_cast<int64_t>(sg.row) + g * a.T + tk) * p.q.token_stride +
+                              (sg.kvh * p.gqa + hh) * p.q.head_stride + 16 * u;
+        if (rows_ok(p.q, src, 32, p.pool.err)) {
+          rows::load8(src, p.q_vec, xs[k][0]);
+          rows::load8(src + 8, p.q_vec, xs[k][1]);
+        }
       }
     }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+    const int row = r1 + k * per + me / U;
+    const uint4* x = xs[k];
     uint32_t h[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     if constexpr (QUANT) {
       float f[16];
@@ -644,7 +680,7 @@ __device__ __forceinline__ void stage_queries(const Launch& a, const Seg& sg, in
       }
 #pragma unroll
       for (int o = 1; o < U; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (u == 0 && row < kM) factors[row] = make_float2(__int_as_float((127 - e) << 23), sum);
+      if (u == 0 && row < rows) factors[row] = make_float2(__int_as_float((127 - e) << 23), sum);
       const auto order = [&](auto bits) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -657,7 +693,8 @@ __device__ __forceinline__ void stage_queries(const Launch& a, const Seg& sg, in
       else
         order(std::integral_constant<int, 2>{});
     }
-    if (row < kM) store_run<HALF>(qs, row, u, h);
+    if (row < rows) store_run<HALF>(qs, row, u, h);
+    }
   }
 }
 
@@ -941,8 +978,11 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
       }
       __syncwarp();
     } else if (warp == S::WL + 1) {
-      // ================= multiplies: scores into columns tS, weights times values into tO
-      if (lane == 0) {
+      // ================= multiplies: scores into columns tS, weights times values into tO.  The whole warp
+      // waits and one lane, always the same, issues: addresses and descriptors then stay in uniform registers.
+      // With one lane in a branch of its own an issue took 44 clocks instead of 17, a wait that is already over
+      // 100 instead of 30 (beside the softmax warps 90 and 250: more than the products, 64 each).
+      {
         constexpr uint32_t f = Fmt<T>::code << 7 | Fmt<T>::code << 10;
         constexpr uint32_t idO = idesc_f16_f32(kM, D) | f | 1u << 16;  // values run along channels
         // -q for a scale below 0 (queries of codes have the sign already)
@@ -953,24 +993,32 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
         bool ok = true;
         const auto scores = [&](int g, int buf, int stage, bool last) {
           const uint64_t dq = smem_desc_sw128(sq + g * S::tile, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = ((k / 4) * S::half + (k % 4) * 32) >> 4;
-            umma_f16(tm + S::tS + kTokens * buf, dq + off, dk + off, idS, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = ((k / 4) * S::half + (k % 4) * 32) >> 4;
+              umma_f16(tm + S::tS + kTokens * buf, dq + off, dk + off, idS, k > 0);
+            }
+            umma_commit(&ctl.s_full[buf]);
+            if (last) umma_commit(&ctl.q_empty[g]);
           }
-          umma_commit(&ctl.s_full[buf]);
-          if (last) umma_commit(&ctl.q_empty[g]);
         };
         const auto outputs = [&](int g, int buf, int stage, int part, bool first) {
           const uint64_t dv = smem_desc_sw128(sr + stage * S::tile, S::half, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTokens / 32; ++k) {
-            const int kk = part * (kTokens / 32) + k;
-            umma_f16_ts(tm + S::tO + D * g, tm + S::tS + kTokens * buf + 8 * kk, dv + ((2048 * kk) >> 4), idO, !first || kk > 0);
+            for (int k = 0; k < kTokens / 32; ++k) {
+              const int kk = part * (kTokens / 32) + k;
+              umma_f16_ts(tm + S::tO + D * g, tm + S::tS + kTokens * buf + 8 * kk, dv + ((2048 * kk) >> 4), idO, !first || kk > 0);
+            }
           }
         };
+        const auto commit = [&](uint64_t* bar) {
+          if (elect_one()) umma_commit(bar);
+        };
+        const auto ready = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase, err, quit)) != 0; };
         while (ok) {
-          ok = wait(&ctl.seg_full[slot.i], slot.phase, err, quit);
+          ok = ready(&ctl.seg_full[slot.i], slot.phase);
           if (!ok) break;
           const Seg& sg = ctl.seg[slot.i];
           if (sg.done) break;
@@ -978,39 +1026,40 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           int ng[NQ];  // tiles of each query tile
 #pragma unroll
           for (int g = 0; g < NQ; ++g) ng[g] = tiles_of(sg, g);
-          mbar_arrive(&ctl.seg_empty[slot.i]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.seg_empty[slot.i]);
           slot.next<kSlots>();
-          ok = wait(&ctl.full[st.i], st.phase, err, quit);
+          ok = ready(&ctl.full[st.i], st.phase);
           if (!ok) break;
           const int kst = st.i;
 #pragma unroll
           for (int g = 0; g < NQ; ++g)
             if (ng[g] > 0) {
-              ok = ok && wait(&ctl.q_full[g], qph >> g & 1, err, quit);
+              ok = ok && ready(&ctl.q_full[g], qph >> g & 1);
               qph ^= 1u << g;
               if (!ok) break;
               tc_fence_after_sync();
               scores(g, NQ == 1 ? 0 : g, kst, ng[g] == 1);
             }
           if (!ok) break;
-          umma_commit(&ctl.empty[kst]);
+          commit(&ctl.empty[kst]);
           st.next<S::NST>();
           for (int i = 0; i < nt && ok; ++i) {
             const Stage v = st;
             st.next<S::NST>();
             const bool next = i + 1 < nt;
             if (NQ == 1 && next) {
-              ok = wait(&ctl.full[st.i], st.phase, err, quit);
+              ok = ready(&ctl.full[st.i], st.phase);
               if (!ok) break;
               tc_fence_after_sync();
               scores(0, (i + 1) & 1, st.i, i + 2 == nt);
-              umma_commit(&ctl.empty[st.i]);
+              commit(&ctl.empty[st.i]);
             }
             if (!QUANT && masked_tile(t0 + i, pos, hi - 1, p.window)) {
-              ok = wait(&ctl.looked[v.i], lookph >> v.i & 1, err, quit);
+              ok = ready(&ctl.looked[v.i], lookph >> v.i & 1);
               lookph ^= 1u << v.i;
             } else {
-              ok = wait(&ctl.full[v.i], v.phase, err, quit);
+              ok = ready(&ctl.full[v.i], v.phase);
             }
             if (!ok) break;
             tc_fence_after_sync();
@@ -1021,17 +1070,17 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               const int buf = NQ == 1 ? i & 1 : g;
 #pragma unroll
               for (int part = 0; part < 2; ++part) {
-                ok = ok && wait(&ctl.p_full[buf][part], pph >> buf & 1, err, quit);
+                ok = ok && ready(&ctl.p_full[buf][part], pph >> buf & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 outputs(g, buf, v.i, part, i == 0);
               }
               if (!ok) break;
               pph ^= 1u << buf;
-              if (NQ == 1 || i + 1 == ng[g]) umma_commit(&ctl.o_done[buf]);
+              if (NQ == 1 || i + 1 == ng[g]) commit(&ctl.o_done[buf]);
               if (NQ > 1 && i + 1 < ng[g]) {
                 if (!have) {
-                  ok = wait(&ctl.full[st.i], st.phase, err, quit);
+                  ok = ready(&ctl.full[st.i], st.phase);
                   have = true;
                   if (!ok) break;
                   tc_fence_after_sync();
@@ -1040,14 +1089,14 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               }
             }
             if (!ok) break;
-            umma_commit(&ctl.empty[v.i]);
+            commit(&ctl.empty[v.i]);
             if (next) {
-              if (NQ > 1) umma_commit(&ctl.empty[st.i]);
+              if (NQ > 1) commit(&ctl.empty[st.i]);
               st.next<S::NST>();
             }
           }
         }
-        umma_commit(&ctl.fin);  // nothing is under way when the columns are given back
+        commit(&ctl.fin);  // nothing is under way when the columns are given back
         mbar_wait(&ctl.fin, 0, err, 1u << 20);
       }
       __syncwarp();
@@ -1093,17 +1142,22 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           if (!ok) break;
           uint8_t *kt = sm + S::ring + k.i * S::tile, *vt = sm + S::ring + v.i * S::tile;
           float4* scales = reinterpret_cast<float4*>(sm + S::scales) + (k.i / 2) * (kTokens / 2);
-          for (int c = 0; c < 8; ++c) {
-            ok = __all_sync(0xffffffffu, ok && wait(&ctl.raw_full[rw.i], rw.phase, err, quit));
-            if (!ok) break;
-            unpack_any<D>(p.pool.kb, p.pool.vb, sm + S::raw + rw.i * p.pool.tile_bytes, kt, vt, scales, c * 16,
-                          t * kTokens + c * 16, sg, masked, seen, me, &sg.dirty, sg.bad[seen < kMostBad ? seen : 0]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.raw_empty[rw.i]);
-            if (++rw.i == a.raw_slots) {
-              rw.i = 0;
-              rw.phase ^= 1;
+#pragma unroll 1
+          for (int c = 0; c < 8; c += 4) {
+            int slots[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              ok = ok && wait(&ctl.raw_full[rw.i], rw.phase, err, quit);
+              slots[k] = rw.i;
+              if (++rw.i == a.raw_slots) {
+                rw.i = 0;
+                rw.phase ^= 1;
+              }
             }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            unpack_any<D>(p.pool.kb, p.pool.vb, sm + S::raw, p.pool.tile_bytes, slots, ctl.raw_empty, kt, vt, scales, c * 16,
+                          t * kTokens + c * 16, sg, masked, seen, me);
           }
           if (!ok) break;
           if (masked) {
