@@ -133,17 +133,12 @@ struct Shape {
   static constexpr int half = kTokens * 128;       // bytes of a tile's half
   static constexpr int tile = H * half;
   static constexpr int softmax = NQ * 128;         // threads
-  // Beside them: for codes four warps that unpack, for 16 bits two that look
-  // through masked values; one that loads and one that multiplies (with two idle
-  // ones a warpgroup, where registers are shared out anew).
-  static constexpr int helpers = QUANT ? 4 : 2;
+  // Beside them: for codes four warps that unpack, for 16 bits one that looks
+  // through masked values; one that loads; one that multiplies for each query tile.
+  static constexpr int helpers = QUANT ? 4 : 1;
   static constexpr int W0 = NQ * 4;                // first helper
-  static constexpr int WL = W0 + helpers;          // loads; WL + 1 multiplies
-  static constexpr bool split = QUANT && NQ == 2;
-  static constexpr int threads = (WL + (split ? 4 : 2)) * 32;
-  // Registers of a thread where four warpgroups have 128 each at launch: their sum is 4 x 128 again.
-  static constexpr int regs_softmax = 168, regs_others = 88;
-  static_assert(!split || (threads == 512 && 2 * regs_softmax + 2 * regs_others <= 512), "registers");
+  static constexpr int WL = W0 + helpers;          // loads; from WL + 1 on: multiply
+  static constexpr int threads = (WL + 1 + NQ) * 32;
   static constexpr int NST = QUANT ? 4 : D == 128 ? (NQ == 2 ? 5 : 6) : 8;  // key and value tiles, in turn
   static constexpr int q = 0;
   static constexpr int ring = NQ * tile;           // (a query tile is as large as a key tile)
@@ -178,36 +173,24 @@ struct Ctl {
 static_assert(sizeof(Ctl) <= 2560, "control");
 
 // A bounded wait that ends when another of the CTA's waits gave up.
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t phase, int32_t* err, volatile int* quit) {
-  for (int i = 0; i < 1 << 12; ++i) {
-    const uint32_t addr = smem_u32(bar);
-    for (int k = 0; k < 1 << 10; ++k) {
-      uint32_t done;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(addr), "r"(phase)
-          : "memory");
-      if (done) return true;
-    }
-    if (*quit) return false;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, int32_t* err, volatile int* quit) {
+  const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(phase)
+        : "memory");
+    if (done) return true;
+    if (i % 1024 == 0 && (*quit || i >= kWaitLimit)) break;
   }
-  atomicExch(err, kErrWaitTimeout);
+  if (!*quit) atomicExch(err, kErrWaitTimeout);
   *quit = 1;
   return false;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, int32_t* err, int* quit) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(phase)
-      : "memory");
-  return done || wait_slow(bar, phase, err, quit);
 }
 
 __device__ __forceinline__ void tma5(void* dst, const CUtensorMap* map, int c1, int c2, int c3, int c4, uint64_t* bar) {
@@ -731,15 +714,6 @@ __device__ __forceinline__ void to_channels(int vb, float (&y)[32]) {
   }
 }
 
-// (A kernel that shares its registers out anew may call no function: the compiler finds no registers for it.)
-template <int N>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 // ---------------------------------------------------------------- the kernel
 
@@ -759,8 +733,8 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&ctl.full[i], QUANT ? S::helpers : 1);
-      // the products have read it, and (16 bits) the two warps that look have passed it
-      mbar_init(&ctl.empty[i], QUANT ? 1 : 1 + S::helpers);
+      // the products of each query tile have read it, and (16 bits) the warp that looks has passed it
+      mbar_init(&ctl.empty[i], QUANT ? NQ : NQ + S::helpers);
       mbar_init(&ctl.looked[i], S::helpers);
     }
     if (QUANT)
@@ -778,9 +752,9 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
-      mbar_init(&ctl.seg_empty[i], S::W0 + S::helpers + 1);
+      mbar_init(&ctl.seg_empty[i], S::W0 + S::helpers + NQ);
     }
-    mbar_init(&ctl.fin, 1);
+    mbar_init(&ctl.fin, NQ);
     ctl.quit = 0;
     fence_mbar_init();
   }
@@ -804,7 +778,6 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
   };
 
   if (warp >= S::WL) {
-    if constexpr (S::split) fewer_registers<S::regs_others>();
     if (warp == S::WL) {
       // ================= plans, and loads keys and values (and queries)
       Walk w;
@@ -977,134 +950,129 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             if (!ok) mbar_wait(&ctl.q_full[g], (qph >> g & 1) ^ 1, err, 1u << 16);
       }
       __syncwarp();
-    } else if (warp == S::WL + 1) {
-      // ================= multiplies: scores into columns tS, weights times values into tO.  The whole warp
-      // waits and one lane, always the same, issues: addresses and descriptors then stay in uniform registers.
-      // With one lane in a branch of its own an issue took 44 clocks instead of 17, a wait that is already over
-      // 100 instead of 30 (beside the softmax warps 90 and 250: more than the products, 64 each).
-      {
-        constexpr uint32_t f = Fmt<T>::code << 7 | Fmt<T>::code << 10;
-        constexpr uint32_t idO = idesc_f16_f32(kM, D) | f | 1u << 16;  // values run along channels
-        // -q for a scale below 0 (queries of codes have the sign already)
-        const uint32_t idS = idesc_f16_f32(kM, kTokens) | f | (!QUANT && p.alpha < 0.0f ? 1u << 13 : 0u);
-        const uint32_t sq = smem_u32(sm + S::q), sr = smem_u32(sm + S::ring);
-        Stage st = {0, 0}, slot = {0, 0};
-        uint32_t qph = 0, pph = 0, lookph = 0;
-        bool ok = true;
-        const auto scores = [&](int g, int buf, int stage, bool last) {
-          const uint64_t dq = smem_desc_sw128(sq + g * S::tile, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
-          if (elect_one()) {
+    } else {
+      // ================= multiply, a warp a query tile: scores into columns tS, weights times values into
+      // tO.  The whole warp waits and one lane, always the same, issues: addresses and descriptors then stay in
+      // uniform registers.  With one lane in a branch of its own an issue took 44 clocks instead of 17, a wait
+      // that is already over 100 instead of 30 (beside the softmax warps 90 and 250: more than the products, 64
+      // each).  The weights of a tile and the next scores, which take their columns, are issued in this order
+      // by one lane and done in it.
+      constexpr uint32_t f = Fmt<T>::code << 7 | Fmt<T>::code << 10;
+      constexpr uint32_t idO = idesc_f16_f32(kM, D) | f | 1u << 16;  // values run along channels
+      // -q for a scale below 0 (queries of codes have the sign already)
+      const uint32_t idS = idesc_f16_f32(kM, kTokens) | f | (!QUANT && p.alpha < 0.0f ? 1u << 13 : 0u);
+      const int g = warp - S::WL - 1;
+      const uint32_t sq = smem_u32(sm + S::q) + g * S::tile, sr = smem_u32(sm + S::ring);
+      Stage st = {0, 0}, slot = {0, 0};
+      uint32_t qph = 0, pph = 0, lookph = 0;
+      bool ok = true;
+      const auto scores = [&](int buf, int stage, bool last) {
+        const uint64_t dq = smem_desc_sw128(sq, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t off = ((k / 4) * S::half + (k % 4) * 32) >> 4;
-              umma_f16(tm + S::tS + kTokens * buf, dq + off, dk + off, idS, k > 0);
-            }
-            umma_commit(&ctl.s_full[buf]);
-            if (last) umma_commit(&ctl.q_empty[g]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = ((k / 4) * S::half + (k % 4) * 32) >> 4;
+            umma_f16(tm + S::tS + kTokens * buf, dq + off, dk + off, idS, k > 0);
           }
-        };
-        const auto outputs = [&](int g, int buf, int stage, int part, bool first) {
-          const uint64_t dv = smem_desc_sw128(sr + stage * S::tile, S::half, 1024);
-          if (elect_one()) {
+          umma_commit(&ctl.s_full[buf]);
+          umma_commit(&ctl.empty[stage]);
+          if (last) umma_commit(&ctl.q_empty[g]);
+        }
+      };
+      const auto outputs = [&](int buf, int stage, int part, bool first) {
+        const uint64_t dv = smem_desc_sw128(sr + stage * S::tile + part * (kTokens / 2) * 128, S::half, 1024);
+        const uint32_t pt = tm + S::tS + kTokens * buf + part * (kTokens / 4);
+        if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTokens / 32; ++k) {
-              const int kk = part * (kTokens / 32) + k;
-              umma_f16_ts(tm + S::tO + D * g, tm + S::tS + kTokens * buf + 8 * kk, dv + ((2048 * kk) >> 4), idO, !first || kk > 0);
-            }
-          }
-        };
-        const auto commit = [&](uint64_t* bar) {
-          if (elect_one()) umma_commit(bar);
-        };
-        const auto ready = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase, err, quit)) != 0; };
-        while (ok) {
-          ok = ready(&ctl.seg_full[slot.i], slot.phase);
+          for (int k = 0; k < kTokens / 32; ++k)
+            umma_f16_ts(tm + S::tO + D * g, pt + 8 * k, dv + ((2048 * k) >> 4), idO, !first || part > 0 || k > 0);
+        }
+      };
+      const auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+      };
+      const auto ready = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase, err, quit)) != 0; };
+      // passes a stage that only the other query tile has a use for
+      const auto pass = [&](const Stage& x) {
+        const bool r = ready(&ctl.full[x.i], x.phase);
+        if (r && lane == 0) mbar_arrive(&ctl.empty[x.i]);
+        return r;
+      };
+      while (ok) {
+        ok = ready(&ctl.seg_full[slot.i], slot.phase);
+        if (!ok) break;
+        const Seg& sg = ctl.seg[slot.i];
+        if (sg.done) break;
+        const int t0 = sg.t0, nt = sg.t1 - t0, pos = sg.pos, last = sg.hi - 1, ng = tiles_of(sg, g);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.seg_empty[slot.i]);
+        slot.next<kSlots>();
+        Stage key = st;
+        st.next<S::NST>();
+        if (ng > 0) {
+          ok = ready(&ctl.full[key.i], key.phase) && ready(&ctl.q_full[g], qph);
+          qph ^= 1;
           if (!ok) break;
-          const Seg& sg = ctl.seg[slot.i];
-          if (sg.done) break;
-          const int t0 = sg.t0, nt = sg.t1 - t0, pos = sg.pos, hi = sg.hi;
-          int ng[NQ];  // tiles of each query tile
-#pragma unroll
-          for (int g = 0; g < NQ; ++g) ng[g] = tiles_of(sg, g);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.seg_empty[slot.i]);
-          slot.next<kSlots>();
-          ok = ready(&ctl.full[st.i], st.phase);
+          tc_fence_after_sync();
+          scores(NQ == 1 ? 0 : g, key.i, ng == 1);
+        } else {
+          ok = pass(key);
           if (!ok) break;
-          const int kst = st.i;
-#pragma unroll
-          for (int g = 0; g < NQ; ++g)
-            if (ng[g] > 0) {
-              ok = ok && ready(&ctl.q_full[g], qph >> g & 1);
-              qph ^= 1u << g;
-              if (!ok) break;
-              tc_fence_after_sync();
-              scores(g, NQ == 1 ? 0 : g, kst, ng[g] == 1);
-            }
-          if (!ok) break;
-          commit(&ctl.empty[kst]);
+        }
+        for (int i = 0; i < nt && ok; ++i) {
+          const Stage v = st;
           st.next<S::NST>();
-          for (int i = 0; i < nt && ok; ++i) {
-            const Stage v = st;
-            st.next<S::NST>();
-            const bool next = i + 1 < nt;
-            if (NQ == 1 && next) {
-              ok = ready(&ctl.full[st.i], st.phase);
-              if (!ok) break;
-              tc_fence_after_sync();
-              scores(0, (i + 1) & 1, st.i, i + 2 == nt);
-              commit(&ctl.empty[st.i]);
-            }
-            if (!QUANT && masked_tile(t0 + i, pos, hi - 1, p.window)) {
-              ok = ready(&ctl.looked[v.i], lookph >> v.i & 1);
-              lookph ^= 1u << v.i;
-            } else {
-              ok = ready(&ctl.full[v.i], v.phase);
-            }
+          key = st;
+          const bool next = i + 1 < nt;
+          if (next) st.next<S::NST>();
+          if (NQ == 1 && next) {
+            ok = ready(&ctl.full[key.i], key.phase);
             if (!ok) break;
             tc_fence_after_sync();
-            bool have = false;
-#pragma unroll
-            for (int g = 0; g < NQ; ++g) {
-              if (i >= ng[g]) continue;
-              const int buf = NQ == 1 ? i & 1 : g;
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                ok = ok && ready(&ctl.p_full[buf][part], pph >> buf & 1);
-                if (!ok) break;
-                tc_fence_after_sync();
-                outputs(g, buf, v.i, part, i == 0);
-              }
+            scores((i + 1) & 1, key.i, i + 2 == nt);
+          }
+          if (!QUANT && masked_tile(t0 + i, pos, last, p.window)) {
+            ok = ready(&ctl.looked[v.i], lookph >> v.i & 1);
+            lookph ^= 1u << v.i;
+          } else {
+            ok = ready(&ctl.full[v.i], v.phase);
+          }
+          if (!ok) break;
+          if (i < ng) {
+            const int buf = NQ == 1 ? i & 1 : g;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+              ok = ok && ready(&ctl.p_full[buf][part], pph >> buf & 1);
               if (!ok) break;
-              pph ^= 1u << buf;
-              if (NQ == 1 || i + 1 == ng[g]) commit(&ctl.o_done[buf]);
-              if (NQ > 1 && i + 1 < ng[g]) {
-                if (!have) {
-                  ok = ready(&ctl.full[st.i], st.phase);
-                  have = true;
-                  if (!ok) break;
-                  tc_fence_after_sync();
-                }
-                scores(g, g, st.i, i + 2 == ng[g]);
-              }
+              tc_fence_after_sync();
+              outputs(buf, v.i, part, i == 0);
             }
             if (!ok) break;
+            pph ^= 1u << buf;
+            if (NQ == 1 || i + 1 == ng) commit(&ctl.o_done[buf]);
             commit(&ctl.empty[v.i]);
-            if (next) {
-              if (NQ > 1) commit(&ctl.empty[st.i]);
-              st.next<S::NST>();
+          } else if (lane == 0) {
+            mbar_arrive(&ctl.empty[v.i]);
+          }
+          if (NQ > 1 && next) {
+            if (i + 1 < ng) {
+              ok = ready(&ctl.full[key.i], key.phase);
+              if (!ok) break;
+              tc_fence_after_sync();
+              scores(g, key.i, i + 2 == ng);
+            } else {
+              ok = pass(key);
             }
           }
         }
-        commit(&ctl.fin);  // nothing is under way when the columns are given back
-        mbar_wait(&ctl.fin, 0, err, 1u << 20);
       }
+      commit(&ctl.fin);  // nothing is under way when the columns are given back
+      mbar_wait(&ctl.fin, 0, err, 1u << 20);
       __syncwarp();
     }
   } else if (warp >= S::W0) {
     // ================= helpers: stage queries where they are not copied; codes: unpack; 16 bits: look
     // through the values of masked tiles
-    if constexpr (S::split) fewer_registers<S::regs_others>();
     const int me = tid - S::W0 * 32;
     Stage st = {0, 0}, slot = {0, 0}, rw = {0, 0};
     uint32_t qph = 0;
@@ -1226,7 +1194,6 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
     }
   } else {
     // ================= softmax: a thread a row
-    if constexpr (S::split) more_registers<S::regs_softmax>();
     const int g = NQ == 1 ? 0 : warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t tO = tm + S::tO + D * g + lanes;
@@ -1268,45 +1235,70 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t tS = tm + S::tS + kTokens * buf + lanes;
-            uint32_t x[4][32];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tmem_ld32(tS + 32 * k, x[k]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tmem_ld_wait(x[k]);
-            if constexpr (QUANT) {  // s (q.c) + z sum(q)
-              // (complete since before the scores; it makes the scales visible here)
+            // The scores are read twice, 64 columns at a time, for their maximum and for the weights: held in
+            // registers the loops would be unrolled over all 128, and the instructions of all roles no longer
+            // fit the instruction cache (a quarter to a half of the time went into that).
+            const int tb = (t0 + i) * kTokens;
+            const bool masked = tb + kTokens - 1 > first_lim || (p.window && tb <= last_lim - p.window);
+            const int a0 = low - tb, a1 = lim - tb;  // columns a0 .. a1 are seen
+            const float4* sc = reinterpret_cast<const float4*>(sm + S::scales) + (kst & 1) * (kTokens / 2);
+            if (QUANT) {  // (complete since before the scores; it makes the scales visible here)
               ok = __all_sync(0xffffffffu, wait(&ctl.full[2 * (kst & 1)], kst >> 1 & 1, err, quit));
               if (!ok) break;
-              const float4* sc = reinterpret_cast<const float4*>(sm + S::scales) + (kst & 1) * (kTokens / 2);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
+            const auto look = [&](uint32_t (&x)[32], int c0) {
+              if constexpr (QUANT) {  // s (q.c) + z sum(q)
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                  const float4 z = sc[16 * k + c];
-                  const f2 y = fma2(f2_of(__uint_as_float(x[k][2 * c]), __uint_as_float(x[k][2 * c + 1])), f2_of(z.x, z.y),
+                  const float4 z = sc[c0 / 2 + c];
+                  const f2 y = fma2(f2_of(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), f2_of(z.x, z.y),
                                     rows::mul2(f2_of(z.z, z.w), qsum2));
                   float u, v;
                   f2_get(y, u, v);
-                  x[k][2 * c] = __float_as_uint(u);
-                  x[k][2 * c + 1] = __float_as_uint(v);
+                  x[2 * c] = __float_as_uint(u);
+                  x[2 * c + 1] = __float_as_uint(v);
                 }
-            }
-            const int tb = (t0 + i) * kTokens;
-            if (tb + kTokens - 1 > first_lim || (p.window && tb <= last_lim - p.window)) {
-              const int a0 = low - tb, a1 = lim - tb;  // columns a0 .. a1 are seen
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
+              }
+              if (masked) {
+                const int b0 = a0 - c0, b1 = a1 - c0;
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
-                  if (32 * k + c < a0 || 32 * k + c > a1) x[k][c] = 0xff800000u;
+                  if (c < b0 || c > b1) x[c] = 0xff800000u;
+              }
+              if (QUANT || masked) tmem_st32(tS + c0, x);
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
+                mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(x[c + 2])), __uint_as_float(x[c + 3]));
+              }
+            };
+            // (no load is under way across a branch: its registers might be moved before it is done)
+            uint32_t xa[32], xb[32];
+            if (QUANT || masked) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < kTokens; c0 += 64) {
+                tmem_ld32(tS + c0, xa);
+                tmem_ld32(tS + c0 + 32, xb);
+                tmem_ld_wait(xa);
+                tmem_ld_wait(xb);
+                look(xa, c0);
+                look(xb, c0 + 32);
+              }
+              tmem_st_wait();
+            } else {
+              tmem_ld32(tS, xa);
+#pragma unroll
+              for (int c0 = 0; c0 < kTokens; c0 += 64) {
+                tmem_ld_wait(xa);
+                tmem_ld32(tS + c0 + 32, xb);
+                look(xa, c0);
+                tmem_ld_wait(xb);
+                if (c0 == 0) tmem_ld32(tS + 64, xa);
+                look(xb, c0 + 32);
+              }
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 32; c += 2)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(x[k][c])), __uint_as_float(x[k][c + 1]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * alpha;
+            const float top = fmaxf(mx[0], mx[1]) * alpha;
             const bool need = top > m + kLazy;
             if (__any_sync(0xffffffffu, need)) {
               float f = 1.0f;
@@ -1337,25 +1329,32 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             const f2 nm2 = f2_of(nm, nm);
             f2 sum[2] = {f2_of(0.0f, 0.0f), f2_of(0.0f, 0.0f)};
             T* const type = nullptr;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            const auto weigh = [&](const uint32_t (&x)[32], int c0) {
               uint32_t w[16];
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 float u, v;
-                f2_get(fma2(f2_of(__uint_as_float(x[k][2 * c]), __uint_as_float(x[k][2 * c + 1])), alpha2, nm2), u, v);
+                f2_get(fma2(f2_of(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), alpha2, nm2), u, v);
                 u = ex2(u);
                 v = ex2(v);
                 sum[c & 1] = add2(sum[c & 1], f2_of(u, v));
                 w[c] = pack2(type, u, v);
               }
-              tmem_st16(tS + 16 * k, w);
-              if (k & 1) {
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_full[buf][k / 2]);
-              }
+              tmem_st16(tS + c0 / 2, w);
+            };
+            tmem_ld32(tS, xa);
+#pragma unroll
+            for (int c0 = 0; c0 < kTokens; c0 += 64) {
+              tmem_ld_wait(xa);
+              tmem_ld32(tS + c0 + 32, xb);
+              weigh(xa, c0);
+              tmem_ld_wait(xb);
+              if (c0 == 0) tmem_ld32(tS + 64, xa);
+              weigh(xb, c0 + 32);
+              tmem_st_wait();
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.p_full[buf][c0 / 64]);
             }
             float s0, s1, s2, s3;
             f2_get(sum[0], s0, s1);
