@@ -134,11 +134,11 @@ struct Shape {
   static constexpr int tile = H * half;
   static constexpr int softmax = NQ * 128;         // threads
   // Beside them: for codes four warps that unpack, for 16 bits one that looks
-  // through masked values; one that loads, and one that multiplies.
+  // through masked values; one that loads; one that multiplies for each query tile.
   static constexpr int helpers = QUANT ? 4 : 1;
   static constexpr int W0 = NQ * 4;                // first helper
-  static constexpr int WL = W0 + helpers;          // loads; WL + 1 multiplies
-  static constexpr int threads = (WL + 2) * 32;
+  static constexpr int WL = W0 + helpers;          // loads; from WL + 1 on: multiply
+  static constexpr int threads = (WL + 1 + NQ) * 32;
   static constexpr int NST = QUANT ? 4 : D == 128 ? (NQ == 2 ? 5 : 6) : 8;  // key and value tiles, in turn
   static constexpr int q = 0;
   static constexpr int ring = NQ * tile;           // (a query tile is as large as a key tile)
@@ -164,6 +164,7 @@ struct Ctl {
   // one for each query tile, or where there is one for each of its score tiles, of which a role may be a tile ahead of
   // another: a wait tells a phase from the one before only.
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2];
+  uint64_t turn[2];             // of a query tile's products
   uint64_t seg_full[kSlots], seg_empty[kSlots];
   uint64_t fin;
   uint32_t tmem;
@@ -733,8 +734,8 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&ctl.full[i], QUANT ? S::helpers : 1);
-      // the products have read it, and (16 bits) the warp that looks has passed it
-      mbar_init(&ctl.empty[i], QUANT ? 1 : 1 + S::helpers);
+      // the products of each query tile have read it, and (16 bits) the warp that looks has passed it
+      mbar_init(&ctl.empty[i], QUANT ? NQ : NQ + S::helpers);
       mbar_init(&ctl.looked[i], S::helpers);
     }
     if (QUANT)
@@ -748,12 +749,13 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
       mbar_init(&ctl.s_full[g], 1);
       mbar_init(&ctl.p_full[g], 4);
       mbar_init(&ctl.o_done[g], 1);
+      mbar_init(&ctl.turn[g], 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
-      mbar_init(&ctl.seg_empty[i], S::W0 + S::helpers + 1);
+      mbar_init(&ctl.seg_empty[i], S::W0 + S::helpers + NQ);
     }
-    mbar_init(&ctl.fin, 1);
+    mbar_init(&ctl.fin, NQ);
     ctl.quit = 0;
     fence_mbar_init();
   }
@@ -950,83 +952,97 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
       }
       __syncwarp();
     } else {
-      // ================= multiplies: scores into columns tS, weights times values into tO.  The whole warp
-      // waits and one lane, always the same, issues: addresses and descriptors then stay in uniform registers.
-      // With one lane in a branch of its own an issue took 44 clocks instead of 17, a wait that is already over
-      // 100 instead of 30 (beside the softmax warps 90 and 250: more than the products, 64 each).  The weights
-      // of a tile and the next scores, which take their columns, are issued in this order by one lane and done
-      // in it.  A warp for each of the two query tiles was slower: their products then alternate, both end
-      // together, and both softmax groups wait, and work, at the same time.
+      // ================= multiply, a warp a query tile: scores into columns tS, weights times values into
+      // tO.  The whole warp waits and one lane, always the same, issues: addresses and descriptors then stay in
+      // uniform registers.  With one lane in a branch of its own an issue took 44 clocks instead of 17, a wait
+      // that is already over 100 instead of 30.  The weights' product and the next scores, which take the
+      // weights' columns, are issued in this order by one lane and done in it.
+      // The two warps take turns, a product and the next scores each, so that one query tile's softmax works
+      // while the other's products run (in any order they would alternate, end together, and both groups would
+      // wait and work at the same time: 3,700 clocks for a tile of both).  Beside the softmax warps a wait takes
+      // 300 clocks even if it is over, so a warp waits for all it needs during the other's turn (one warp for
+      // both: 3,880 clocks), and gives the turn away four products (256 clocks) before its own are all issued.
       constexpr uint32_t f = Fmt<T>::code << 7 | Fmt<T>::code << 10;
       constexpr uint32_t idO = idesc_f16_f32(kM, D) | f | 1u << 16;  // values run along channels
       // -q for a scale below 0 (queries of codes have the sign already)
       const uint32_t idS = idesc_f16_f32(kM, kTokens) | f | (!QUANT && p.alpha < 0.0f ? 1u << 13 : 0u);
-      const uint32_t sq = smem_u32(sm + S::q), sr = smem_u32(sm + S::ring);
+      const int g = warp - S::WL - 1;
+      const uint32_t sq = smem_u32(sm + S::q) + g * S::tile, sr = smem_u32(sm + S::ring);
       Stage st = {0, 0}, slot = {0, 0};
-      uint32_t qph = 0, pph = 0, lookph = 0;
+      uint32_t qph = 0, pph = 0, lookph = 0, tph = g == 0;  // (the first turn is query tile 0's)
       bool ok = true;
       // (of the elected lane)
-      const auto scores = [&](int g, int buf, int stage, bool last) {
-        const uint64_t dq = smem_desc_sw128(sq + g * S::tile, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
+      const auto scores = [&](int buf, int stage, bool last) {
+        const uint64_t dq = smem_desc_sw128(sq, 16, 1024), dk = smem_desc_sw128(sr + stage * S::tile, 16, 1024);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
+          if (NQ > 1 && k == D / 16 - 4) mbar_arrive(&ctl.turn[g ^ 1]);
           const uint64_t off = ((k / 4) * S::half + (k % 4) * 32) >> 4;
           umma_f16(tm + S::tS + kTokens * buf, dq + off, dk + off, idS, k > 0);
         }
         umma_commit(&ctl.s_full[buf]);
+        umma_commit(&ctl.empty[stage]);
         if (last) umma_commit(&ctl.q_empty[g]);
       };
-      const auto outputs = [&](int g, int buf, int stage, bool first, bool done) {
+      const auto outputs = [&](int buf, int stage, bool first, bool done, bool hand_over) {
         const uint64_t dv = smem_desc_sw128(sr + stage * S::tile, S::half, 1024);
         const uint32_t pt = tm + S::tS + kTokens * buf;
 #pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k) umma_f16_ts(tm + S::tO + D * g, pt + 8 * k, dv + ((2048 * k) >> 4), idO, !first || k > 0);
+        for (int k = 0; k < kTokens / 16; ++k) {
+          if (NQ > 1 && k == kTokens / 16 - 4 && hand_over) mbar_arrive(&ctl.turn[g ^ 1]);
+          umma_f16_ts(tm + S::tO + D * g, pt + 8 * k, dv + ((2048 * k) >> 4), idO, !first || k > 0);
+        }
+        umma_commit(&ctl.empty[stage]);
         if (done) umma_commit(&ctl.o_done[buf]);
       };
       const auto ready = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase, err, quit)) != 0; };
+      const auto my_turn = [&]() {
+        if (NQ == 1) return true;
+        const bool r = ready(&ctl.turn[g], tph);
+        tph ^= 1;
+        return r;
+      };
       while (ok) {
         ok = ready(&ctl.seg_full[slot.i], slot.phase);
         if (!ok) break;
         const Seg& sg = ctl.seg[slot.i];
         if (sg.done) break;
-        const int t0 = sg.t0, nt = sg.t1 - t0, pos = sg.pos, last = sg.hi - 1;
-        const int ng0 = tiles_of(sg, 0), ng1 = NQ == 1 ? 0 : tiles_of(sg, 1);  // tiles of each query tile
+        const int t0 = sg.t0, nt = sg.t1 - t0, pos = sg.pos, last = sg.hi - 1, ng = tiles_of(sg, g);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.seg_empty[slot.i]);
         slot.next<kSlots>();
         Stage key = st;
         st.next<S::NST>();
         ok = ready(&ctl.full[key.i], key.phase);
-#pragma unroll 1
-        for (int g = 0; g < NQ; ++g) {
-          const int ng = g ? ng1 : ng0;
-          if (ng <= 0) continue;
-          ok = ok && ready(&ctl.q_full[g], qph >> g & 1);
-          qph ^= 1u << g;
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (elect_one()) scores(g, NQ == 1 ? 0 : g, key.i, ng == 1);
-          __syncwarp();
+        if (ng > 0) {
+          ok = ok && ready(&ctl.q_full[g], qph);
+          qph ^= 1;
         }
+        ok = ok && my_turn();
         if (!ok) break;
-        if (elect_one()) umma_commit(&ctl.empty[key.i]);
+        tc_fence_after_sync();
+        if (elect_one()) {
+          if (ng > 0) {
+            scores(NQ == 1 ? 0 : g, key.i, ng == 1);
+          } else {  // (a stage that only the other query tile has a use for)
+            mbar_arrive(&ctl.turn[g ^ 1]);
+            mbar_arrive(&ctl.empty[key.i]);
+          }
+        }
+        __syncwarp();
         for (int i = 0; i < nt && ok; ++i) {
           const Stage v = st;
           st.next<S::NST>();
           key = st;
           const bool next = i + 1 < nt;
-          if (next) st.next<S::NST>();
-          // What is there long since is waited for first: a wait takes its time even if it is over (beside the
-          // products, which take all of the shared memory's bandwidth, 200 clocks and more), and between the
-          // weights' arrival and their product and the next scores there is none.
-          if (next) ok = ready(&ctl.full[key.i], key.phase);
+          if (next) {
+            st.next<S::NST>();
+            ok = ready(&ctl.full[key.i], key.phase);
+          }
           if (NQ == 1 && next) {
             if (!ok) break;
             tc_fence_after_sync();
-            if (elect_one()) {
-              scores(0, (i + 1) & 1, key.i, i + 2 == nt);
-              umma_commit(&ctl.empty[key.i]);
-            }
+            if (elect_one()) scores((i + 1) & 1, key.i, i + 2 == nt);
             __syncwarp();
           }
           if (!QUANT && masked_tile(t0 + i, pos, last, p.window)) {
@@ -1035,25 +1051,24 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           } else {
             ok = ok && ready(&ctl.full[v.i], v.phase);
           }
-          if (!ok) break;
-#pragma unroll 1
-          for (int g = 0; g < NQ; ++g) {
-            const int ng = g ? ng1 : ng0, buf = NQ == 1 ? i & 1 : g;
-            if (i >= ng) continue;
-            ok = ready(&ctl.p_full[buf], pph >> buf & 1);
+          const int buf = NQ == 1 ? i & 1 : g;
+          ok = ok && my_turn();
+          if (i < ng) {
+            ok = ok && ready(&ctl.p_full[buf], pph >> buf & 1);
             pph ^= 1u << buf;
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (elect_one()) {
-              outputs(g, buf, v.i, i == 0, NQ == 1 || i + 1 == ng);
-              if (NQ > 1 && i + 1 < ng) scores(g, g, key.i, i + 2 == ng);
-            }
-            __syncwarp();
           }
           if (!ok) break;
+          tc_fence_after_sync();
           if (elect_one()) {
-            umma_commit(&ctl.empty[v.i]);
-            if (NQ > 1 && next) umma_commit(&ctl.empty[key.i]);
+            const bool more = NQ > 1 && i + 1 < ng;
+            if (i < ng) {
+              outputs(buf, v.i, i == 0, NQ == 1 || i + 1 == ng, !more);
+              if (more) scores(g, key.i, i + 2 == ng);
+            } else {
+              mbar_arrive(&ctl.turn[g ^ 1]);
+              mbar_arrive(&ctl.empty[v.i]);
+            }
+            if (NQ > 1 && next && !more) mbar_arrive(&ctl.empty[key.i]);
           }
           __syncwarp();
         }
