@@ -163,7 +163,7 @@ struct Ctl {
   uint64_t raw_full[kMostRaw], raw_empty[kMostRaw];
   // one for each query tile, or where there is one for each of its score tiles, of which a role may be a tile ahead of
   // another: a wait tells a phase from the one before only.
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2];  // (weights are ready in two halves)
   uint64_t turn[2];             // of a query tile's products
   uint64_t seg_full[kSlots], seg_empty[kSlots];
   uint64_t fin;
@@ -747,7 +747,8 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
       mbar_init(&ctl.q_full[g], q_tma ? 1 : S::helpers);
       mbar_init(&ctl.q_empty[g], QUANT ? 5 : 1);  // the products, and the warps that have the rows' factors
       mbar_init(&ctl.s_full[g], 1);
-      mbar_init(&ctl.p_full[g], 4);
+      mbar_init(&ctl.p_full[g][0], 4);
+      mbar_init(&ctl.p_full[g][1], 4);
       mbar_init(&ctl.o_done[g], 1);
       mbar_init(&ctl.turn[g], 1);
     }
@@ -984,16 +985,11 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
         umma_commit(&ctl.empty[stage]);
         if (last) umma_commit(&ctl.q_empty[g]);
       };
-      const auto outputs = [&](int buf, int stage, bool first, bool done, bool hand_over) {
-        const uint64_t dv = smem_desc_sw128(sr + stage * S::tile, S::half, 1024);
-        const uint32_t pt = tm + S::tS + kTokens * buf;
+      const auto outputs = [&](int buf, int stage, int part, bool first) {
+        const uint64_t dv = smem_desc_sw128(sr + stage * S::tile + part * (kTokens / 2) * 128, S::half, 1024);
+        const uint32_t pt = tm + S::tS + kTokens * buf + part * (kTokens / 4);
 #pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k) {
-          if (NQ > 1 && k == kTokens / 16 - 4 && hand_over) mbar_arrive(&ctl.turn[g ^ 1]);
-          umma_f16_ts(tm + S::tO + D * g, pt + 8 * k, dv + ((2048 * k) >> 4), idO, !first || k > 0);
-        }
-        umma_commit(&ctl.empty[stage]);
-        if (done) umma_commit(&ctl.o_done[buf]);
+        for (int k = 0; k < kTokens / 32; ++k) umma_f16_ts(tm + S::tO + D * g, pt + 8 * k, dv + ((2048 * k) >> 4), idO, !first || k > 0);
       };
       const auto ready = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase, err, quit)) != 0; };
       const auto my_turn = [&]() {
@@ -1054,7 +1050,12 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           const int buf = NQ == 1 ? i & 1 : g;
           ok = ok && my_turn();
           if (i < ng) {
-            ok = ok && ready(&ctl.p_full[buf], pph >> buf & 1);
+            ok = ok && ready(&ctl.p_full[buf][0], pph >> buf & 1);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (elect_one()) outputs(buf, v.i, 0, i == 0);
+            __syncwarp();
+            ok = ready(&ctl.p_full[buf][1], pph >> buf & 1);
             pph ^= 1u << buf;
           }
           if (!ok) break;
@@ -1062,7 +1063,10 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           if (elect_one()) {
             const bool more = NQ > 1 && i + 1 < ng;
             if (i < ng) {
-              outputs(buf, v.i, i == 0, NQ == 1 || i + 1 == ng, !more);
+              if (NQ > 1 && !more) mbar_arrive(&ctl.turn[g ^ 1]);
+              outputs(buf, v.i, 1, false);
+              umma_commit(&ctl.empty[v.i]);
+              if (NQ == 1 || i + 1 == ng) umma_commit(&ctl.o_done[buf]);
               if (more) scores(g, key.i, i + 2 == ng);
             } else {
               mbar_arrive(&ctl.turn[g ^ 1]);
@@ -1358,11 +1362,11 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               tmem_ld_wait(xb);
               if (c0 == 0) tmem_ld32(tS + 64, xa);
               weigh(xb, c0 + 32);
+              tmem_st_wait();
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.p_full[buf][c0 / 64]);
             }
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.p_full[buf]);
             float s0, s1, s2, s3;
             f2_get(sum[0], s0, s1);
             f2_get(sum[1], s2, s3);
