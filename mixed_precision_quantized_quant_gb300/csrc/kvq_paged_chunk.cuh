@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           const int pos = w.sp.pos0 + it.tok, hi = pos + it.tokens;
           const int lo = p.window && pos >= p.window ? pos - p.window + 1 : 0;
           const int32_t* table = PROMPT ? nullptr : p.batch.table + w.s * p.batch.table_stride;
-          Seg& sg = ctl.seg[slot.i];
+          Seg& sg = ctl.seg[slot.i];  // (stays until its readers are done with it)
           if (lane == 0) {
             sg.table = table;
             sg.done = 0;
@@ -829,19 +829,6 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             note.tokens = it.tokens;
             note.row = w.sp.row0 + it.tok;
             note.kvh = w.kvh;
-          }
-          if (q_tma) {
-            for (int g = 0; g < NQ; ++g) {
-              if (tiles_of(sg, g) <= 0) continue;
-              ok = ok && __all_sync(0xffffffffu, wait(&ctl.q_empty[g], (qph >> g & 1) ^ 1, err, quit));
-              qph ^= 1u << g;
-              if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&ctl.q_full[g], S::H * 128 * a.T * p.gqa);
-              __syncwarp();
-              if (lane < S::H)
-                tma4(sm + S::q + g * S::tile + lane * S::half, &a.qm, w.kvh * p.gqa, w.sp.row0 + it.tok + g * a.T, lane,
-                     &ctl.q_full[g]);
-            }
           }
           for (int t = it.t0 + from; t < it.t0 + to && ok; ++t) {
             // a lane's page (codes: stored tile; rows of two halves: of both), the same for keys and values
@@ -920,6 +907,20 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
                 }
                 st.next<S::NST>();
                 if (issued < S::NST) ++issued;
+              }
+            }
+            // queries after the first tile: theirs may have to wait for the segment before
+            if (q_tma && t == it.t0 + from) {
+              for (int g = 0; g < NQ; ++g) {
+                if (tiles_of(sg, g) <= 0) continue;
+                ok = ok && __all_sync(0xffffffffu, wait(&ctl.q_empty[g], (qph >> g & 1) ^ 1, err, quit));
+                qph ^= 1u << g;
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&ctl.q_full[g], S::H * 128 * a.T * p.gqa);
+                __syncwarp();
+                if (lane < S::H)
+                  tma4(sm + S::q + g * S::tile + lane * S::half, &a.qm, w.kvh * p.gqa, w.sp.row0 + it.tok + g * a.T, lane,
+                       &ctl.q_full[g]);
               }
             }
           }
@@ -1389,19 +1390,20 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
         if (QUANT) kst += sg.t1 - t0 - (nt > 0 ? nt : 0);
         // ---- the rows' results
         const int64_t at = (static_cast<int64_t>(sg.row) + g * a.T + my_tok) * p.hkv * p.gqa + sg.kvh * p.gqa + my_head;
+        const bool fine = !sg.dirty && !__any_sync(0xffffffffu, l == 0.0f);
         if (sg.whole) {
           const float inv = l != 0.0f ? __fdividef(1.0f, l) : 0.0f;
           uint8_t* dst = static_cast<uint8_t*>(p.out) + at * D * 2;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_ld_wait(o);
+          const auto write = [&](const uint32_t (&o)[32], int c) {
             float y[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = l != 0.0f ? __uint_as_float(o[k]) * inv : 0.0f;
+            for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
             to_channels<QUANT>(p.pool.vb, y);
-            if (sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
+            if (!fine) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = l != 0.0f ? y[k] : 0.0f;
+              if (sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
+            }
             uint32_t w[2][8];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -1415,6 +1417,16 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               store32(dst + 2 * c, wide_out, w[0]);
               store32(dst + 2 * c + 32, wide_out, w[1]);
             }
+          };
+#pragma unroll 1
+          for (int c = 0; c < D; c += 64) {
+            uint32_t o0[32], o1[32];
+            tmem_ld32(tO + c, o0);
+            tmem_ld32(tO + c + 32, o1);
+            tmem_ld_wait(o0);
+            tmem_ld_wait(o1);
+            write(o0, c);
+            write(o1, c + 32);
           }
           if (p.lse && live)
             p.lse[at] = l == 0.0f ? -INFINITY : ((m - Fmt<T>::room) + log2f(l)) * 0.69314718055994531f;
@@ -1437,7 +1449,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
 #pragma unroll
               for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]);
               to_channels<QUANT>(p.pool.vb, y);
-              if (sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
+              if (!fine && sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
               if (fits) {
                 float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows) + rr;
 #pragma unroll
