@@ -133,9 +133,9 @@ struct Shape {
   static constexpr int half = kTokens * 128;       // bytes of a tile's half
   static constexpr int tile = H * half;
   static constexpr int softmax = NQ * 128;         // threads
-  // Beside them: for codes four warps that unpack, for 16 bits one that looks
+  // Beside them: for codes four or eight warps that unpack, for 16 bits one that looks
   // through masked values; one that loads; one that multiplies for each query tile.
-  static constexpr int helpers = QUANT ? 4 : 1;
+  static constexpr int helpers = QUANT ? (NQ == 1 ? 8 : 4) : 1;
   static constexpr int W0 = NQ * 4;                // first helper
   static constexpr int WL = W0 + helpers;          // loads; from WL + 1 on: multiply
   static constexpr int threads = (WL + 1 + NQ) * 32;
@@ -497,111 +497,133 @@ __host__ __device__ constexpr int code_channel(int bits, int i) {
   return bits == 8 ? 4 * (j / 2) + j % 2 + 2 * k : bits == 4 ? 8 * (j / 4) + j % 4 + 4 * k : j + 8 * k;
 }
 
-// Stores the two 16-byte chunks of a run of 16 channels (run u of row `row`) at
-// their swizzled places; the order keeps a warp's lanes, eight runs of a row,
-// on different banks.
-template <int HALF>
-__device__ __forceinline__ void store_run(uint8_t* tile, int row, int u, const uint32_t (&h)[8]) {
-  uint8_t* at = tile + (u / 4) * HALF + row * 128;
-  const int c = 2 * (u % 4), x = row & 7, odd = u / 4;
-  const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-  *reinterpret_cast<uint4*>(at + (((c + odd) ^ x) << 4)) = odd ? b : a;
-  *reinterpret_cast<uint4*>(at + (((c + 1 - odd) ^ x) << 4)) = odd ? a : b;
-}
-
-// Four stored tiles of 16 tokens (tokens t16 .. of the 128-token tile, positions
-// pos ..) into the key and the value operand: keys as codes less their middle,
-// the scales and what they are to be added as fp32; values as numbers, rounded
-// to fp16 once.  Tokens outside lo .. hi, and in masked tiles those whose scale
-// or zero is no number, get values of 0.  All is read before anything is worked
-// on: one tile after another took 500 ns each, hardly any of them at work.
-template <int D, int KB, int VB>
-__device__ __forceinline__ void unpack_four(const uint8_t* raw, int tile_bytes, const int (&slots)[4], uint64_t* freed, uint8_t* kt,
-                                            uint8_t* vt, float4* scales, int t16, int pos, Seg& sg, bool masked, int nth, int tid) {
-  constexpr int U = D / 16, rk = D / 8 * KB, rv = D / 8 * VB, HALF = kTokens * 128;
-  constexpr float mid = KB == 8 ? 128.0f : KB == 4 ? 8.0f : 2.0f;
-  const int u = tid % U, i = tid / U % 16, r = tile_key_row(i);
-  // D = 64: half of the threads take keys, half values
-  const bool keys = D == 128 || tid < 16 * U, values = D == 128 || tid >= 16 * U;
-  const int k_at = r * rk + ((u * 2 * KB) ^ tile_key_xor(rk, r)), v_at = 16 * rk + i * rv + ((u * 2 * VB) ^ tile_val_xor(rv, i));
-  Codes<KB> kc[4];
-  Codes<VB> vc[4];
-  uint2 sz[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint8_t* t = raw + slots[c] * tile_bytes;
-    sz[c] = *reinterpret_cast<const uint2*>(t + 16 * (rk + rv) + r * 8);
-    if (keys) kc[c].load(t + k_at);
-    if (values) vc[c].load(t + v_at);
+// Where the two 16-byte chunks of a run of 16 channels (run u of row `row`) go
+// in a tile; the order keeps a warp's lanes, eight runs of a row, on different
+// banks: `odd` lanes store the second chunk first.
+struct RunPlace {
+  uint32_t first, second;
+  bool odd;
+  __device__ __forceinline__ RunPlace(int row, int u) {
+    const int c = 2 * (u % 4), x = row & 7;
+    const uint32_t at = (u / 4) * kTokens * 128 + row * 128;
+    odd = u >= 4;
+    first = at + (((c + odd) ^ x) << 4);
+    second = at + (((c + 1 - odd) ^ x) << 4);
   }
-  __syncwarp();
-  if ((tid & 31) == 0)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) mbar_arrive(freed + slots[c]);
-  const int lo = sg.lo, hi = sg.hi;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t h[8];
-    const int at = t16 + 16 * c + i;
-    if (keys) {
-      kc[c].unpack(mid, h);
-      store_run<HALF>(kt, at, u, h);
-      if (u == 0) {
-        const float2 f = __half22float2(u32_as_h2(sz[c].x));
-        float* to = reinterpret_cast<float*>(scales + at / 2) + (at & 1);
-        to[0] = f.x;
-        to[2] = fmaf(f.x, mid, f.y);
-      }
+  __device__ __forceinline__ void store(uint8_t* tile, const uint32_t (&h)[8]) const {
+    const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+    *reinterpret_cast<uint4*>(tile + first) = odd ? b : a;
+    *reinterpret_cast<uint4*>(tile + second) = odd ? a : b;
+  }
+};
+
+// 32 codes, an aligned run of channels, as they are stored.
+template <int BITS>
+struct Run32 {
+  Codes<BITS> c[2];
+  __device__ __forceinline__ void load(const uint8_t* src) {
+    if constexpr (BITS == 8) {
+      c[0].load(src);
+      c[1].load(src + 16);
+    } else if constexpr (BITS == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(src);
+      c[0].w[0] = x.x, c[0].w[1] = x.y, c[1].w[0] = x.z, c[1].w[1] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      c[0].w[0] = x.x, c[1].w[0] = x.y;
     }
-    if (values) {
-      const __half2 f = u32_as_h2(sz[c].y);
-      const bool in = pos + 16 * c + i >= lo && pos + 16 * c + i < hi;
-      const bool fine = (sz[c].y & 0x7c00u) != 0x7c00u && (sz[c].y & 0x7c000000u) != 0x7c000000u;
-      const bool none = !in || (masked && !fine);
-      vc[c].unpack(0.0f, h);
-      const __half2 s = __low2half2(f), z = __high2half2(f);
+  }
+};
+
+// The eight stored tiles of 16 tokens of a tile (positions pos ..) into the key
+// and the value operand: keys as codes less their middle, their scales and what
+// they are to be added as fp32; values as numbers, rounded to fp16 once.  In
+// masked tiles tokens outside lo .. hi, and those whose scale or zero is no
+// number, get values of 0.  A warp takes 8 tokens at a time (head_dim 64: 16),
+// a lane 32 channels of one; eight lanes that store together have eight tokens,
+// whose swizzles put them on different banks.
+template <int D, int KB, int VB, int WARPS>
+__device__ __forceinline__ bool unpack_tile(const uint8_t* raw, int tile_bytes, int raw_slots, int first, uint32_t phase, uint64_t* full,
+                                            uint64_t* freed, uint8_t* kt, uint8_t* vt, float4* scales, int pos, Seg& sg, bool masked,
+                                            int nth, int warp, int lane, int32_t* err, int* quit) {
+  constexpr int U = D / 32, TW = 32 / U, PER = 16 / TW;  // lanes of a token, tokens of a warp, warps of a stored tile
+  constexpr int rk = D / 8 * KB, rv = D / 8 * VB;
+  constexpr float mid = KB == 8 ? 128.0f : KB == 4 ? 8.0f : 2.0f;
+  const int u = lane / TW, i = warp % PER * TW + lane % TW, r = tile_key_row(i);
+  const int k_at = r * rk + ((u * 4 * KB) ^ tile_key_xor(rk, r)), v_at = 16 * rk + i * rv + ((u * 4 * VB) ^ tile_val_xor(rv, i));
+  const int sz_at = 16 * (rk + rv) + r * 8;
+  const uint32_t to = (u / 2) * kTokens * 128 + i * 128, x4 = ((4 * (u % 2)) ^ (i & 7)) << 4;  // chunk c of the run: x4 ^ 16 c
+#pragma unroll 1
+  for (int c = warp / PER; c < 8; c += WARPS / PER) {  // the stored tile
+    int n = first + c;
+    const int wraps = n / raw_slots;
+    n -= wraps * raw_slots;
+    if (!__all_sync(0xffffffffu, wait(full + n, (phase + wraps) & 1, err, quit))) return false;
+    const uint8_t* t = raw + n * tile_bytes;
+    const uint2 sz = *reinterpret_cast<const uint2*>(t + sz_at);
+    Run32<KB> k;
+    Run32<VB> v;
+    k.load(t + k_at);
+    v.load(t + v_at);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(freed + n);
+    uint8_t *kd = kt + c * 16 * 128 + to, *vd = vt + c * 16 * 128 + to;
+    uint32_t h[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = none ? 0u : h2_as_u32(__hfma2(u32_as_h2(h[j]), s, z));
-      // a last step past the greatest fp16 (a scale rounded up) stays finite
-      const float top = fabsf(__low2float(f)) * ((1 << VB) - 1) + fabsf(__high2float(f));
-      if (top > 65504.0f) {
+    for (int q = 0; q < 2; ++q) {
+      k.c[q].unpack(mid, h);
+      *reinterpret_cast<uint4*>(kd + (x4 ^ (32 * q))) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(kd + (x4 ^ (32 * q + 16))) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    const int token = 16 * c + i;
+    if (u == 0) {
+      const float2 f = __half22float2(u32_as_h2(sz.x));
+      float* sc = reinterpret_cast<float*>(scales + token / 2) + (token & 1);
+      sc[0] = f.x;
+      sc[2] = fmaf(f.x, mid, f.y);
+    }
+    uint32_t f = sz.y;
+    if (masked) {
+      const bool in = pos + token >= sg.lo && pos + token < sg.hi, fine = (f & 0x7c00u) != 0x7c00u && (f & 0x7c000000u) != 0x7c000000u;
+      if (in && !fine && u == 0) {
+        sg.dirty = 1;
+        if (nth < kMostBad) atomicOr(&sg.bad[nth][token / 32], 1u << (token % 32));
+      }
+      if (!in || !fine) f = 0;  // a scale and a zero of 0
+    }
+    const __half2 s = __low2half2(u32_as_h2(f)), z = __high2half2(u32_as_h2(f));
+    // a last step past the greatest fp16 (a scale rounded up) stays finite
+    const bool far = fmaf(__low2float(s), static_cast<float>((1 << VB) - 1), fabsf(__low2float(z))) > 65504.0f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      v.c[q].unpack(0.0f, h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hfma2(u32_as_h2(h[j]), s, z));
+      if (far) {
         const __half2 lim = __floats2half2_rn(65504.0f, 65504.0f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hmax2_nan(__hmin2_nan(u32_as_h2(h[j]), lim), __hneg2(lim)));
       }
-      if (in && none && u == 0) {
-        sg.dirty = 1;
-        if (nth < kMostBad) atomicOr(&sg.bad[nth][at / 32], 1u << (at % 32));
-      }
-      store_run<HALF>(vt, at, u, h);
+      *reinterpret_cast<uint4*>(vd + (x4 ^ (32 * q))) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(vd + (x4 ^ (32 * q + 16))) = make_uint4(h[4], h[5], h[6], h[7]);
     }
   }
+  return true;
 }
 
-template <int D>
-__device__ __forceinline__ void unpack_any(int kb, int vb, const uint8_t* raw, int tile_bytes, const int (&slots)[4], uint64_t* freed,
-                                           uint8_t* kt, uint8_t* vt, float4* scales, int t16, int pos, Seg& sg, bool masked, int nth,
-                                           int tid) {
-  const auto with = [&](auto k, auto v) {
-    unpack_four<D, decltype(k)::value, decltype(v)::value>(raw, tile_bytes, slots, freed, kt, vt, scales, t16, pos, sg, masked, nth, tid);
-  };
-  using two = std::integral_constant<int, 2>;
-  using four = std::integral_constant<int, 4>;
-  using eight = std::integral_constant<int, 8>;
-  const auto value = [&](auto k) {
-    if (vb == 8)
-      with(k, eight{});
-    else if (vb == 4)
-      with(k, four{});
-    else
-      with(k, two{});
-  };
-  if (kb == 8)
-    value(eight{});
-  else if (kb == 4)
-    value(four{});
-  else
-    value(two{});
+template <int D, int WARPS, typename... A>
+__device__ __forceinline__ bool unpack_any(int kb, int vb, A&&... args) {
+  switch (kb * 16 + vb) {
+    case 8 * 16 + 8: return unpack_tile<D, 8, 8, WARPS>(args...);
+    case 8 * 16 + 4: return unpack_tile<D, 8, 4, WARPS>(args...);
+    case 8 * 16 + 2: return unpack_tile<D, 8, 2, WARPS>(args...);
+    case 4 * 16 + 8: return unpack_tile<D, 4, 8, WARPS>(args...);
+    case 4 * 16 + 4: return unpack_tile<D, 4, 4, WARPS>(args...);
+    case 4 * 16 + 2: return unpack_tile<D, 4, 2, WARPS>(args...);
+    case 2 * 16 + 8: return unpack_tile<D, 2, 8, WARPS>(args...);
+    case 2 * 16 + 4: return unpack_tile<D, 2, 4, WARPS>(args...);
+    default: return unpack_tile<D, 2, 2, WARPS>(args...);
+  }
 }
 
 // Query rows of a group as operand rows, by `n` threads.  16 bits: as they are
@@ -612,7 +634,7 @@ template <typename T, int D, bool QUANT>
 __device__ __forceinline__ void stage_queries(const Launch& a, const Seg& sg, int g, int rows, uint8_t* qs, float2* factors,
                                               int me, int n) {
   const PagedChunkParams& p = a.p;
-  constexpr int U = D / 16, HALF = kTokens * 128;
+  constexpr int U = D / 16;
   const int u = me % U, per = n / U;
   if (QUANT)
     for (int r = rows + me; r < kM; r += n) factors[r] = make_float2(1.0f, 0.0f);
@@ -677,7 +699,7 @@ __device__ __forceinline__ void stage_queries(const Launch& a, const Seg& sg, in
       else
         order(std::integral_constant<int, 2>{});
     }
-    if (row < rows) store_run<HALF>(qs, row, u, h);
+    if (row < rows) RunPlace(row, u).store(qs, h);
     }
   }
 }
@@ -741,7 +763,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
     if (QUANT)
       for (int i = 0; i < kMostRaw; ++i) {
         mbar_init(&ctl.raw_full[i], 1);
-        mbar_init(&ctl.raw_empty[i], S::helpers);
+        mbar_init(&ctl.raw_empty[i], D / 64);  // warps of a stored tile
       }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&ctl.q_full[g], q_tma ? 1 : S::helpers);
@@ -1122,22 +1144,12 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           if (!ok) break;
           uint8_t *kt = sm + S::ring + k.i * S::tile, *vt = sm + S::ring + v.i * S::tile;
           float4* scales = reinterpret_cast<float4*>(sm + S::scales) + (k.i / 2) * (kTokens / 2);
-#pragma unroll 1
-          for (int c = 0; c < 8; c += 4) {
-            int slots[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              ok = ok && wait(&ctl.raw_full[rw.i], rw.phase, err, quit);
-              slots[k] = rw.i;
-              if (++rw.i == a.raw_slots) {
-                rw.i = 0;
-                rw.phase ^= 1;
-              }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            unpack_any<D>(p.pool.kb, p.pool.vb, sm + S::raw, p.pool.tile_bytes, slots, ctl.raw_empty, kt, vt, scales, c * 16,
-                          t * kTokens + c * 16, sg, masked, seen, me);
+          ok = unpack_any<D, S::helpers>(p.pool.kb, p.pool.vb, sm + S::raw, p.pool.tile_bytes, a.raw_slots, rw.i, rw.phase, ctl.raw_full,
+                                         ctl.raw_empty, kt, vt, scales, t * kTokens, sg, masked, seen, warp - S::W0, lane, err, quit);
+          rw.i += 8;
+          while (rw.i >= a.raw_slots) {
+            rw.i -= a.raw_slots;
+            rw.phase ^= 1;
           }
           if (!ok) break;
           if (masked) {
@@ -1259,6 +1271,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               if (!ok) break;
             }
             float mx[2] = {-INFINITY, -INFINITY};
+            // (a warp without rows of its own leaves what is there: no other row's result depends on it)
             const auto look = [&](uint32_t (&x)[32], int c0) {
               if constexpr (QUANT) {  // s (q.c) + z sum(q)
 #pragma unroll
