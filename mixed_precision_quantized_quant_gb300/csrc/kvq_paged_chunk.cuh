@@ -852,32 +852,40 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             note.row = w.sp.row0 + it.tok;
             note.kvh = w.kvh;
           }
+          // A lane's page (codes: stored tile; rows of two halves: of both), the same for keys and values; its
+          // number is asked for a tile ahead.
+          const int shift = QUANT ? 4 : p.pool.page_shift, in_tile = (lane / (QUANT ? 1 : S::H)) << shift;
+          const auto entry_of = [&](int t) {
+            const int at = t * kTokens + in_tile;
+            if (PROMPT || in_tile >= kTokens || t >= it.t0 + to || at >= hi || at + (1 << shift) <= lo) return -1;
+            const int32_t* entry = table + (at >> p.pool.page_shift);
+            return table_ok(p.batch, entry, err) ? *entry : -1;
+          };
+          const auto needed = [&](int t) {
+            const int at = t * kTokens + in_tile;
+            return !PROMPT && in_tile < kTokens && at < hi && at + (1 << shift) > lo;
+          };
+          int ahead = entry_of(it.t0 + from);
           for (int t = it.t0 + from; t < it.t0 + to && ok; ++t) {
-            // a lane's page (codes: stored tile; rows of two halves: of both), the same for keys and values
-            int page = -1;
-            const int shift = QUANT ? 4 : p.pool.page_shift;
-            const int at = t * kTokens + ((lane / (QUANT ? 1 : S::H)) << shift);
-            if (!PROMPT) {
-              if (lane < (kTokens >> shift) * (QUANT ? 1 : S::H) && at < hi && at + (1 << shift) > lo) {
-                const int32_t* entry = table + (at >> p.pool.page_shift);
-                if (table_ok(p.batch, entry, err)) {
-                  page = *entry;
-                  if (page < 0 || page >= p.pool.num_pages) {
-                    atomicExch(err, kErrBadPage);
-                    page = -1;
-                  } else if (!pool_ok(p.pool, p.pool.pages + page * p.pool.page_stride + w.kvh * p.pool.head_stride,
-                                      p.pool.head_stride)) {
-                    page = -1;
-                  }
-                }
+            const int at = t * kTokens + in_tile;
+            int page = ahead;
+            ahead = entry_of(t + 1);
+            if (needed(t)) {
+              if (page < 0 || page >= p.pool.num_pages) {
+                atomicExch(err, kErrBadPage);
+                page = -1;
+              } else if (!pool_ok(p.pool, p.pool.pages + page * p.pool.page_stride + w.kvh * p.pool.head_stride,
+                                  p.pool.head_stride)) {
+                page = -1;
               }
             }
             if constexpr (QUANT) {
-              // eight stored tiles, a lane each, four at a time: no lane waits for a slot that another of its
-              // four fills first
+              // eight stored tiles, a lane each, no more at a time than there are slots: no lane waits for a slot
+              // that another of them fills first
+              const int most = a.raw_slots >= 8 ? 8 : 4;
 #pragma unroll 1
-              for (int r = 0; r < 8; r += 4) {
-                if (lane >= r && lane < r + 4) {
+              for (int r = 0; r < 8; r += most) {
+                if (lane >= r && lane < r + most) {
                   const int n = rw.i + lane, wraps = n / a.raw_slots, slot_i = n - wraps * a.raw_slots;
                   ok = ok && wait(&ctl.raw_empty[slot_i], (rw.phase ^ (wraps & 1)) ^ 1, err, quit);
                   if (ok) {
