@@ -1306,17 +1306,15 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
                 mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(x[c + 2])), __uint_as_float(x[c + 3]));
               }
             };
+            constexpr bool ROLL = QUANT;
             // (no load is under way across a branch: its registers might be moved before it is done)
             uint32_t xa[32], xb[32];
             if (QUANT || masked) {
 #pragma unroll 1
-              for (int c0 = 0; c0 < kTokens; c0 += 64) {
+              for (int c0 = 0; c0 < kTokens; c0 += 32) {
                 tmem_ld32(tS + c0, xa);
-                tmem_ld32(tS + c0 + 32, xb);
                 tmem_ld_wait(xa);
-                tmem_ld_wait(xb);
                 look(xa, c0);
-                look(xb, c0 + 32);
               }
               tmem_st_wait();
             } else {
@@ -1375,6 +1373,21 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               }
               tmem_st16(tS + c0 / 2, w);
             };
+            if constexpr (ROLL) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < kTokens; c0 += 64) {
+#pragma unroll 1
+                for (int c1 = c0; c1 < c0 + 64; c1 += 32) {
+                  tmem_ld32(tS + c1, xa);
+                  tmem_ld_wait(xa);
+                  weigh(xa, c1);
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_full[buf][c0 / 64]);
+              }
+            } else {
             tmem_ld32(tS, xa);
 #pragma unroll
             for (int c0 = 0; c0 < kTokens; c0 += 64) {
@@ -1388,6 +1401,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               tc_fence_before_sync();
               __syncwarp();
               if (lane == 0) mbar_arrive(&ctl.p_full[buf][c0 / 64]);
+            }
             }
             float s0, s1, s2, s3;
             f2_get(sum[0], s0, s1);
