@@ -173,6 +173,18 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 2560, "control");
 
+__device__ __forceinline__ bool is_over(uint64_t* bar, uint32_t phase) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(phase)
+      : "memory");
+  return done != 0;
+}
+
 // A bounded wait that ends when another of the CTA's waits gave up.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, int32_t* err, volatile int* quit) {
   const uint32_t addr = smem_u32(bar);
@@ -1064,10 +1076,12 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           const bool next = i + 1 < nt;
           if (next) {
             st.next<S::NST>();
-            ok = ready(&ctl.full[key.i], key.phase);
+            if (NQ > 1) ok = ready(&ctl.full[key.i], key.phase);
           }
-          if (NQ == 1 && next) {
-            if (!ok) break;
+          // One query tile: the next scores run beside this tile's softmax, if their keys are there already; if
+          // not, this tile's product, which frees its stage, is not kept waiting for them.
+          const bool early = NQ == 1 && next && __all_sync(0xffffffffu, is_over(&ctl.full[key.i], key.phase));
+          if (early) {
             tc_fence_after_sync();
             if (elect_one()) scores((i + 1) & 1, key.i, i + 2 == nt);
             __syncwarp();
@@ -1106,6 +1120,13 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             if (NQ > 1 && next && !more) mbar_arrive(&ctl.empty[key.i]);
           }
           __syncwarp();
+          if (NQ == 1 && next && !early) {
+            ok = ready(&ctl.full[key.i], key.phase);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (elect_one()) scores((i + 1) & 1, key.i, i + 2 == nt);
+            __syncwarp();
+          }
         }
       }
       if (elect_one()) umma_commit(&ctl.fin);  // nothing is under way when the columns are given back
@@ -1243,7 +1264,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
       if (tokens > 0) {
         const int t0 = sg.t0, nt = tiles_of(sg, g);
         const int first_lim = sg.pos + g * a.T, last_lim = first_lim + tokens - 1;
-        const bool live = my_tok < tokens;
+        const bool live = my_tok < tokens, idle = !__any_sync(0xffffffffu, live);  // a row, a warp without rows
         const int lim = live ? first_lim + my_tok : last_lim;
         const int low = p.window ? lim - p.window + 1 : 0;
         float m = -INFINITY, l = 0.0f;
@@ -1267,6 +1288,12 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t tS = tm + S::tS + kTokens * buf + lanes;
+            if (idle) {  // (what its columns hold counts for its own rows only)
+              if (NQ == 1) oph ^= 1u << buf;
+              ++kst;
+              if (lane < 2) mbar_arrive(&ctl.p_full[buf][lane]);
+              continue;
+            }
             // The scores are read twice, 64 columns at a time, for their maximum and for the weights: held in
             // registers the loops would be unrolled over all 128, and the instructions of all roles no longer
             // fit the instruction cache (a quarter to a half of the time went into that).
@@ -1279,7 +1306,6 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               if (!ok) break;
             }
             float mx[2] = {-INFINITY, -INFINITY};
-            // (a warp without rows of its own leaves what is there: no other row's result depends on it)
             const auto look = [&](uint32_t (&x)[32], int c0) {
               if constexpr (QUANT) {  // s (q.c) + z sum(q)
 #pragma unroll
