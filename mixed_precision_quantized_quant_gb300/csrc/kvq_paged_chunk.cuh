@@ -139,7 +139,9 @@ struct Shape {
   static constexpr int W0 = NQ * 4;                // first helper
   static constexpr int WL = W0 + helpers;          // loads; from WL + 1 on: multiply
   static constexpr int threads = (WL + 1 + NQ) * 32;
-  static constexpr int NST = QUANT ? 4 : D == 128 ? (NQ == 2 ? 5 : 6) : 8;  // key and value tiles, in turn
+  // Key and value tiles, in turn.  (Three for codes where there is no room for more: values take the stage of the
+  // keys before them, which the scores free early.)
+  static constexpr int NST = QUANT ? (D == 128 && NQ == 2 ? 3 : 4) : D == 128 ? (NQ == 2 ? 5 : 6) : 8;
   static constexpr int q = 0;
   static constexpr int ring = NQ * tile;           // (a query tile is as large as a key tile)
   static constexpr int raw = ring + NST * tile;    // codes: tiles of 16 tokens as they are stored
@@ -151,7 +153,7 @@ struct Shape {
   static constexpr int ctl = raw + raw_bytes + extra;
   static constexpr int smem = ctl + 2560;
   static_assert(smem <= most && NST * tile >= kPlan * 8, "shared memory");
-  static_assert(!QUANT || raw_bytes >= 4 * paged_tile_bytes(D, 8, 8), "stored tiles");
+  static_assert(!QUANT || raw_bytes >= 8 * paged_tile_bytes(D, 8, 8), "a tile's stored tiles");
   static constexpr int tS = 0, tO = 2 * kTokens;   // columns: two score tiles, then the outputs
 };
 
@@ -164,6 +166,7 @@ struct Ctl {
   // one for each query tile, or where there is one for each of its score tiles, of which a role may be a tile ahead of
   // another: a wait tells a phase from the one before only.
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2];  // (weights are ready in two halves)
+  uint64_t scales_full[2], scales_empty[2];  // of even and odd tiles: written, read by all softmax warps
   uint64_t turn[2];             // of a query tile's products
   uint64_t seg_full[kSlots], seg_empty[kSlots];
   uint64_t fin;
@@ -547,57 +550,100 @@ struct Run32 {
   }
 };
 
-// The eight stored tiles of 16 tokens of a tile (positions pos ..) into the key
-// and the value operand: keys as codes less their middle, their scales and what
-// they are to be added as fp32; values as numbers, rounded to fp16 once.  In
-// masked tiles tokens outside lo .. hi, and those whose scale or zero is no
-// number, get values of 0.  A warp takes 8 tokens at a time (head_dim 64: 16),
-// a lane 32 channels of one; eight lanes that store together have eight tokens,
-// whose swizzles put them on different banks.
-template <int D, int KB, int VB, int WARPS>
-__device__ __forceinline__ bool unpack_tile(const uint8_t* raw, int tile_bytes, int raw_slots, int first, uint32_t phase, uint64_t* full,
-                                            uint64_t* freed, uint8_t* kt, uint8_t* vt, float4* scales, int pos, Seg& sg, bool masked,
-                                            int nth, int warp, int lane, int32_t* err, int* quit) {
-  constexpr int U = D / 32, TW = 32 / U, PER = 16 / TW;  // lanes of a token, tokens of a warp, warps of a stored tile
-  constexpr int rk = D / 8 * KB, rv = D / 8 * VB;
+// Where a lane reads and writes: a warp takes 8 tokens at a time (head_dim 64:
+// 16), a lane 32 channels of one; eight lanes that store together have eight
+// tokens, whose swizzles put them on different banks.
+template <int D>
+struct LanePlace {
+  static constexpr int U = D / 32, TW = 32 / U, PER = 16 / TW;  // lanes of a token, tokens of a warp, warps of a stored tile
+  int u, i;         // run of channels, token of the stored tile
+  uint32_t to, x4;  // the run's half and row; its chunk c is at x4 ^ 16 c
+  __device__ __forceinline__ LanePlace(int warp, int lane) : u(lane / TW), i(warp % PER * TW + lane % TW) {
+    to = (u / 2) * kTokens * 128 + i * 128;
+    x4 = ((4 * (u % 2)) ^ (i & 7)) << 4;
+  }
+  __device__ __forceinline__ void store(uint8_t* row, int q, const uint32_t (&h)[8]) const {
+    *reinterpret_cast<uint4*>(row + (x4 ^ (32 * q))) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(row + (x4 ^ (32 * q + 16))) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+};
+
+// Stored tiles under way, from the first of a tile on.
+struct RawRing {
+  const uint8_t* at;
+  int tile_bytes, slots, first;
+  uint32_t phase;
+  uint64_t *full, *freed;
+  int32_t* err;
+  int* quit;
+  // the slot of stored tile c, waited for
+  __device__ __forceinline__ bool wait_for(int c, int& n) const {
+    n = first + c;
+    uint32_t ph = phase;
+    if (n >= slots) {
+      n -= slots;
+      ph ^= 1;
+    }
+    return __all_sync(0xffffffffu, wait(full + n, ph, err, quit));
+  }
+};
+
+// The eight stored tiles of 16 tokens of a tile into the key operand: codes less
+// their middle, the tokens' scales and what they are to be added as fp32.
+template <int D, int KB, int WARPS>
+__device__ __forceinline__ bool unpack_keys(const RawRing& ring, uint8_t* kt, float4* scales, int warp, int lane) {
+  constexpr int rk = D / 8 * KB;
   constexpr float mid = KB == 8 ? 128.0f : KB == 4 ? 8.0f : 2.0f;
-  const int u = lane / TW, i = warp % PER * TW + lane % TW, r = tile_key_row(i);
-  const int k_at = r * rk + ((u * 4 * KB) ^ tile_key_xor(rk, r)), v_at = 16 * rk + i * rv + ((u * 4 * VB) ^ tile_val_xor(rv, i));
-  const int sz_at = 16 * (rk + rv) + r * 8;
-  const uint32_t to = (u / 2) * kTokens * 128 + i * 128, x4 = ((4 * (u % 2)) ^ (i & 7)) << 4;  // chunk c of the run: x4 ^ 16 c
+  const LanePlace<D> pl(warp, lane);
+  const int r = tile_key_row(pl.i), at = r * rk + ((pl.u * 4 * KB) ^ tile_key_xor(rk, r)), sz_at = ring.tile_bytes - 128 + r * 8;
 #pragma unroll 1
-  for (int c = warp / PER; c < 8; c += WARPS / PER) {  // the stored tile
-    int n = first + c;
-    const int wraps = n / raw_slots;
-    n -= wraps * raw_slots;
-    if (!__all_sync(0xffffffffu, wait(full + n, (phase + wraps) & 1, err, quit))) return false;
-    const uint8_t* t = raw + n * tile_bytes;
-    const uint2 sz = *reinterpret_cast<const uint2*>(t + sz_at);
+  for (int c = warp / pl.PER; c < 8; c += WARPS / pl.PER) {
+    int n;
+    if (!ring.wait_for(c, n)) return false;
+    const uint8_t* t = ring.at + n * ring.tile_bytes;
     Run32<KB> k;
-    Run32<VB> v;
-    k.load(t + k_at);
-    v.load(t + v_at);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(freed + n);
-    uint8_t *kd = kt + c * 16 * 128 + to, *vd = vt + c * 16 * 128 + to;
-    uint32_t h[8];
+    k.load(t + at);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(t + sz_at));
+    uint8_t* row = kt + c * 16 * 128 + pl.to;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
+      uint32_t h[8];
       k.c[q].unpack(mid, h);
-      *reinterpret_cast<uint4*>(kd + (x4 ^ (32 * q))) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(kd + (x4 ^ (32 * q + 16))) = make_uint4(h[4], h[5], h[6], h[7]);
+      pl.store(row, q, h);
     }
-    const int token = 16 * c + i;
-    if (u == 0) {
-      const float2 f = __half22float2(u32_as_h2(sz.x));
-      float* sc = reinterpret_cast<float*>(scales + token / 2) + (token & 1);
+    if (pl.u == 0) {
+      float* sc = reinterpret_cast<float*>(scales + 8 * c + pl.i / 2) + (pl.i & 1);
       sc[0] = f.x;
       sc[2] = fmaf(f.x, mid, f.y);
     }
-    uint32_t f = sz.y;
+  }
+  return true;
+}
+
+// The same (positions pos ..) into the value operand: numbers, rounded to fp16
+// once.  In masked tiles tokens outside lo .. hi, and those whose scale or zero is
+// no number, get values of 0.
+template <int D, int VB, int WARPS>
+__device__ __forceinline__ bool unpack_values(const RawRing& ring, int kb, uint8_t* vt, int pos, Seg& sg, bool masked, int nth, int warp,
+                                              int lane) {
+  constexpr int rv = D / 8 * VB;
+  const LanePlace<D> pl(warp, lane);
+  const int at = 2 * D * kb + pl.i * rv + ((pl.u * 4 * VB) ^ tile_val_xor(rv, pl.i)),
+            sz_at = ring.tile_bytes - 128 + tile_key_row(pl.i) * 8 + 4;
+#pragma unroll 1
+  for (int c = warp / pl.PER; c < 8; c += WARPS / pl.PER) {
+    int n;
+    if (!ring.wait_for(c, n)) return false;
+    const uint8_t* t = ring.at + n * ring.tile_bytes;
+    Run32<VB> v;
+    v.load(t + at);
+    uint32_t f = *reinterpret_cast<const uint32_t*>(t + sz_at);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ring.freed + n);
     if (masked) {
+      const int token = 16 * c + pl.i;
       const bool in = pos + token >= sg.lo && pos + token < sg.hi, fine = (f & 0x7c00u) != 0x7c00u && (f & 0x7c000000u) != 0x7c000000u;
-      if (in && !fine && u == 0) {
+      if (in && !fine && pl.u == 0) {
         sg.dirty = 1;
         if (nth < kMostBad) atomicOr(&sg.bad[nth][token / 32], 1u << (token % 32));
       }
@@ -606,8 +652,10 @@ __device__ __forceinline__ bool unpack_tile(const uint8_t* raw, int tile_bytes, 
     const __half2 s = __low2half2(u32_as_h2(f)), z = __high2half2(u32_as_h2(f));
     // a last step past the greatest fp16 (a scale rounded up) stays finite
     const bool far = fmaf(__low2float(s), static_cast<float>((1 << VB) - 1), fabsf(__low2float(z))) > 65504.0f;
+    uint8_t* row = vt + c * 16 * 128 + pl.to;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
+      uint32_t h[8];
       v.c[q].unpack(0.0f, h);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hfma2(u32_as_h2(h[j]), s, z));
@@ -616,26 +664,10 @@ __device__ __forceinline__ bool unpack_tile(const uint8_t* raw, int tile_bytes, 
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = h2_as_u32(__hmax2_nan(__hmin2_nan(u32_as_h2(h[j]), lim), __hneg2(lim)));
       }
-      *reinterpret_cast<uint4*>(vd + (x4 ^ (32 * q))) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(vd + (x4 ^ (32 * q + 16))) = make_uint4(h[4], h[5], h[6], h[7]);
+      pl.store(row, q, h);
     }
   }
   return true;
-}
-
-template <int D, int WARPS, typename... A>
-__device__ __forceinline__ bool unpack_any(int kb, int vb, A&&... args) {
-  switch (kb * 16 + vb) {
-    case 8 * 16 + 8: return unpack_tile<D, 8, 8, WARPS>(args...);
-    case 8 * 16 + 4: return unpack_tile<D, 8, 4, WARPS>(args...);
-    case 8 * 16 + 2: return unpack_tile<D, 8, 2, WARPS>(args...);
-    case 4 * 16 + 8: return unpack_tile<D, 4, 8, WARPS>(args...);
-    case 4 * 16 + 4: return unpack_tile<D, 4, 4, WARPS>(args...);
-    case 4 * 16 + 2: return unpack_tile<D, 4, 2, WARPS>(args...);
-    case 2 * 16 + 8: return unpack_tile<D, 2, 8, WARPS>(args...);
-    case 2 * 16 + 4: return unpack_tile<D, 2, 4, WARPS>(args...);
-    default: return unpack_tile<D, 2, 2, WARPS>(args...);
-  }
 }
 
 // Query rows of a group as operand rows, by `n` threads.  16 bits: as they are
@@ -785,6 +817,8 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
       mbar_init(&ctl.p_full[g][1], 4);
       mbar_init(&ctl.o_done[g], 1);
       mbar_init(&ctl.turn[g], 1);
+      mbar_init(&ctl.scales_full[g], S::helpers);
+      mbar_init(&ctl.scales_empty[g], S::W0);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
@@ -892,31 +926,27 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               }
             }
             if constexpr (QUANT) {
-              // eight stored tiles, a lane each, no more at a time than there are slots: no lane waits for a slot
-              // that another of them fills first
-              const int most = a.raw_slots >= 8 ? 8 : 4;
-#pragma unroll 1
-              for (int r = 0; r < 8; r += most) {
-                if (lane >= r && lane < r + most) {
-                  const int n = rw.i + lane, wraps = n / a.raw_slots, slot_i = n - wraps * a.raw_slots;
-                  ok = ok && wait(&ctl.raw_empty[slot_i], (rw.phase ^ (wraps & 1)) ^ 1, err, quit);
-                  if (ok) {
-                    uint64_t* bar = &ctl.raw_full[slot_i];
-                    if (page >= 0) {
-                      const int in = at & ((1 << p.pool.page_shift) - 1);
-                      const uint8_t* src = p.pool.pages + page * p.pool.page_stride + w.kvh * p.pool.head_stride +
-                                           static_cast<int64_t>(in / kTile) * p.pool.tile_bytes;
-                      mbar_arrive_expect_tx(bar, p.pool.tile_bytes);
-                      bulk_g2s(sm + S::raw + slot_i * p.pool.tile_bytes, src, p.pool.tile_bytes, bar);
-                    } else {
-                      mbar_arrive(bar);
-                    }
+              // eight stored tiles, a lane each (there are slots for as many: no lane waits for one that another
+              // of them fills first)
+              if (lane < 8) {
+                const int n = rw.i + lane, over = n >= a.raw_slots, slot_i = over ? n - a.raw_slots : n;
+                ok = wait(&ctl.raw_empty[slot_i], rw.phase ^ over ^ 1, err, quit);
+                if (ok) {
+                  uint64_t* bar = &ctl.raw_full[slot_i];
+                  if (page >= 0) {
+                    const int in = at & ((1 << p.pool.page_shift) - 1);
+                    const uint8_t* src = p.pool.pages + page * p.pool.page_stride + w.kvh * p.pool.head_stride +
+                                         static_cast<int64_t>(in / kTile) * p.pool.tile_bytes;
+                    mbar_arrive_expect_tx(bar, p.pool.tile_bytes);
+                    bulk_g2s(sm + S::raw + slot_i * p.pool.tile_bytes, src, p.pool.tile_bytes, bar);
+                  } else {
+                    mbar_arrive(bar);
                   }
                 }
-                ok = __all_sync(0xffffffffu, ok);
               }
+              ok = __all_sync(0xffffffffu, ok);
               rw.i += 8;
-              while (rw.i >= a.raw_slots) {
+              if (rw.i >= a.raw_slots) {
                 rw.i -= a.raw_slots;
                 rw.phase ^= 1;
               }
@@ -1138,7 +1168,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
     // through the values of masked tiles
     const int me = tid - S::W0 * 32;
     Stage st = {0, 0}, slot = {0, 0}, rw = {0, 0};
-    uint32_t qph = 0;
+    uint32_t qph = 0, tiles = 0;
     bool ok = true;
     while (ok) {
       ok = __all_sync(0xffffffffu, wait(&ctl.seg_full[slot.i], slot.phase, err, quit));
@@ -1163,20 +1193,36 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
       for (int t = sg.t0; t < sg.t1 && ok; ++t) {
         const bool masked = masked_tile(t, sg.pos, sg.hi - 1, p.window);
         if constexpr (QUANT) {
-          // both of the tile's stages
+          // keys first: the scores need them, while the values' stage may be in use for longer
           const Stage k = st;
           st.next<S::NST>();
           const Stage v = st;
           st.next<S::NST>();
-          ok = wait(&ctl.empty[k.i], k.phase ^ 1, err, quit);
-          ok = __all_sync(0xffffffffu, ok && wait(&ctl.empty[v.i], v.phase ^ 1, err, quit));
-          if (!ok) break;
+          const RawRing ring = {sm + S::raw, p.pool.tile_bytes, a.raw_slots, rw.i, rw.phase, ctl.raw_full, ctl.raw_empty, err, quit};
           uint8_t *kt = sm + S::ring + k.i * S::tile, *vt = sm + S::ring + v.i * S::tile;
-          float4* scales = reinterpret_cast<float4*>(sm + S::scales) + (k.i / 2) * (kTokens / 2);
-          ok = unpack_any<D, S::helpers>(p.pool.kb, p.pool.vb, sm + S::raw, p.pool.tile_bytes, a.raw_slots, rw.i, rw.phase, ctl.raw_full,
-                                         ctl.raw_empty, kt, vt, scales, t * kTokens, sg, masked, seen, warp - S::W0, lane, err, quit);
+          float4* scales = reinterpret_cast<float4*>(sm + S::scales) + (tiles & 1) * (kTokens / 2);
+          const int w = warp - S::W0;
+          ok = __all_sync(0xffffffffu, wait(&ctl.empty[k.i], k.phase ^ 1, err, quit));
+          ok = ok && __all_sync(0xffffffffu, wait(&ctl.scales_empty[tiles & 1], (tiles >> 1 & 1) ^ 1, err, quit));
+          if (!ok) break;
+          ok = p.pool.kb == 8   ? unpack_keys<D, 8, S::helpers>(ring, kt, scales, w, lane)
+               : p.pool.kb == 4 ? unpack_keys<D, 4, S::helpers>(ring, kt, scales, w, lane)
+                                : unpack_keys<D, 2, S::helpers>(ring, kt, scales, w, lane);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl.full[k.i]);
+            mbar_arrive(&ctl.scales_full[tiles & 1]);
+          }
+          ++tiles;
+          ok = __all_sync(0xffffffffu, wait(&ctl.empty[v.i], v.phase ^ 1, err, quit));
+          if (!ok) break;
+          ok = p.pool.vb == 8   ? unpack_values<D, 8, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane)
+               : p.pool.vb == 4 ? unpack_values<D, 4, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane)
+                                : unpack_values<D, 2, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane);
           rw.i += 8;
-          while (rw.i >= a.raw_slots) {
+          if (rw.i >= a.raw_slots) {
             rw.i -= a.raw_slots;
             rw.phase ^= 1;
           }
@@ -1190,10 +1236,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ctl.full[k.i]);
-            mbar_arrive(&ctl.full[v.i]);
-          }
+          if (lane == 0) mbar_arrive(&ctl.full[v.i]);
         } else {
           // every stage in turn, so that none is mistaken for its last use
           ok = __all_sync(0xffffffffu, wait(&ctl.full[st.i], st.phase, err, quit));
@@ -1255,6 +1298,14 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
     Stage slot = {0, 0};
     uint32_t sph = 0, oph = 0, qph = 0, kst = 0;  // phases; tiles so far: the key scales' stage
     bool ok = true;
+    // gives back the scales of tiles that it has no use for, each once they are written
+    const auto pass_tiles = [&](int n) {
+      for (; n > 0; --n, ++kst) {
+        if (!__all_sync(0xffffffffu, wait(&ctl.scales_full[kst & 1], kst >> 1 & 1, err, quit))) return false;
+        if (lane == 0) mbar_arrive(&ctl.scales_empty[kst & 1]);
+      }
+      return true;
+    };
     while (ok) {
       ok = __all_sync(0xffffffffu, wait(&ctl.seg_full[slot.i], slot.phase, err, quit));
       if (!ok) break;
@@ -1290,6 +1341,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             const uint32_t tS = tm + S::tS + kTokens * buf + lanes;
             if (idle) {  // (what its columns hold counts for its own rows only)
               if (NQ == 1) oph ^= 1u << buf;
+              if (QUANT && lane == 2) mbar_arrive(&ctl.scales_empty[kst & 1]);
               ++kst;
               if (lane < 2) mbar_arrive(&ctl.p_full[buf][lane]);
               continue;
@@ -1302,7 +1354,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             const int a0 = low - tb, a1 = lim - tb;  // columns a0 .. a1 are seen
             const float4* sc = reinterpret_cast<const float4*>(sm + S::scales) + (kst & 1) * (kTokens / 2);
             if (QUANT) {  // (complete since before the scores; it makes the scales visible here)
-              ok = __all_sync(0xffffffffu, wait(&ctl.full[2 * (kst & 1)], kst >> 1 & 1, err, quit));
+              ok = __all_sync(0xffffffffu, wait(&ctl.scales_full[kst & 1], kst >> 1 & 1, err, quit));
               if (!ok) break;
             }
             float mx[2] = {-INFINITY, -INFINITY};
@@ -1343,6 +1395,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
                 look(xa, c0);
               }
               tmem_st_wait();
+              if (QUANT && lane == 0) mbar_arrive(&ctl.scales_empty[kst & 1]);
             } else {
               tmem_ld32(tS, xa);
 #pragma unroll
@@ -1447,8 +1500,9 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           if (!ok) break;
           tc_fence_after_sync();
         }
-        // tiles that only the other query tile saw
-        if (QUANT) kst += sg.t1 - t0 - (nt > 0 ? nt : 0);
+        // tiles that only the other query tile sees
+        if (QUANT) ok = pass_tiles(sg.t1 - t0 - (nt > 0 ? nt : 0));
+        if (!ok) break;
         // ---- the rows' results
         const int64_t at = (static_cast<int64_t>(sg.row) + g * a.T + my_tok) * p.hkv * p.gqa + sg.kvh * p.gqa + my_head;
         const bool fine = !sg.dirty && !__any_sync(0xffffffffu, l == 0.0f);
@@ -1522,7 +1576,8 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
         }
         tc_fence_before_sync();
       } else if (QUANT) {
-        kst += sg.t1 - sg.t0;
+        ok = pass_tiles(sg.t1 - sg.t0);
+        if (!ok) break;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.seg_empty[slot.i]);
