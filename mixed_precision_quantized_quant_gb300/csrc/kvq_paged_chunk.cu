@@ -56,7 +56,8 @@ cudaError_t launch_as(Launch& a, bool bf16, int sms, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, fn, a);
   if (e != cudaSuccess) return e;
-  if (a.grid == 1) return cudaSuccess;
+  // an item shorter than two uncut ends stays whole (see cut_at, walk_start)
+  if (a.grid == 1 || longest / chunk::kTokens + 1 + chunk::kStart < 2 * (chunk::kStart + 1) + 2) return cudaSuccess;
   return rows::launch_pdl(bf16 ? chunk::paged_chunk_join_kernel<true, D> : chunk::paged_chunk_join_kernel<false, D>, a,
                           dim3(static_cast<unsigned>(a.grid), static_cast<unsigned>(a.slot_rows / 32)), 256, s);
 }

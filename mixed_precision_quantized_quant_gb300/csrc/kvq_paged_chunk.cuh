@@ -568,39 +568,24 @@ struct LanePlace {
   }
 };
 
-// Stored tiles under way, from the first of a tile on.
+// A tile's eight stored tiles, from slot `first` of the ring on.
 struct RawRing {
   const uint8_t* at;
   int tile_bytes, slots, first;
-  uint32_t phase;
-  uint64_t *full, *freed;
-  int32_t* err;
-  int* quit;
-  // the slot of stored tile c, waited for
-  __device__ __forceinline__ bool wait_for(int c, int& n) const {
-    n = first + c;
-    uint32_t ph = phase;
-    if (n >= slots) {
-      n -= slots;
-      ph ^= 1;
-    }
-    return __all_sync(0xffffffffu, wait(full + n, ph, err, quit));
-  }
+  __device__ __forceinline__ int slot(int c) const { return first + c < slots ? first + c : first + c - slots; }
 };
 
 // The eight stored tiles of 16 tokens of a tile into the key operand: codes less
 // their middle, the tokens' scales and what they are to be added as fp32.
 template <int D, int KB, int WARPS>
-__device__ __forceinline__ bool unpack_keys(const RawRing& ring, uint8_t* kt, float4* scales, int warp, int lane) {
+__device__ __forceinline__ void unpack_keys(const RawRing& ring, uint8_t* kt, float4* scales, int warp, int lane) {
   constexpr int rk = D / 8 * KB;
   constexpr float mid = KB == 8 ? 128.0f : KB == 4 ? 8.0f : 2.0f;
   const LanePlace<D> pl(warp, lane);
   const int r = tile_key_row(pl.i), at = r * rk + ((pl.u * 4 * KB) ^ tile_key_xor(rk, r)), sz_at = ring.tile_bytes - 128 + r * 8;
 #pragma unroll 1
   for (int c = warp / pl.PER; c < 8; c += WARPS / pl.PER) {
-    int n;
-    if (!ring.wait_for(c, n)) return false;
-    const uint8_t* t = ring.at + n * ring.tile_bytes;
+    const uint8_t* t = ring.at + ring.slot(c) * ring.tile_bytes;
     Run32<KB> k;
     k.load(t + at);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(t + sz_at));
@@ -617,14 +602,13 @@ __device__ __forceinline__ bool unpack_keys(const RawRing& ring, uint8_t* kt, fl
       sc[2] = fmaf(f.x, mid, f.y);
     }
   }
-  return true;
 }
 
 // The same (positions pos ..) into the value operand: numbers, rounded to fp16
 // once.  In masked tiles tokens outside lo .. hi, and those whose scale or zero is
 // no number, get values of 0.
 template <int D, int VB, int WARPS>
-__device__ __forceinline__ bool unpack_values(const RawRing& ring, int kb, uint8_t* vt, int pos, Seg& sg, bool masked, int nth, int warp,
+__device__ __forceinline__ void unpack_values(const RawRing& ring, int kb, uint8_t* vt, int pos, Seg& sg, bool masked, int nth, int warp,
                                               int lane) {
   constexpr int rv = D / 8 * VB;
   const LanePlace<D> pl(warp, lane);
@@ -632,14 +616,10 @@ __device__ __forceinline__ bool unpack_values(const RawRing& ring, int kb, uint8
             sz_at = ring.tile_bytes - 128 + tile_key_row(pl.i) * 8 + 4;
 #pragma unroll 1
   for (int c = warp / pl.PER; c < 8; c += WARPS / pl.PER) {
-    int n;
-    if (!ring.wait_for(c, n)) return false;
-    const uint8_t* t = ring.at + n * ring.tile_bytes;
+    const uint8_t* t = ring.at + ring.slot(c) * ring.tile_bytes;
     Run32<VB> v;
     v.load(t + at);
     uint32_t f = *reinterpret_cast<const uint32_t*>(t + sz_at);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(ring.freed + n);
     if (masked) {
       const int token = 16 * c + pl.i;
       const bool in = pos + token >= sg.lo && pos + token < sg.hi, fine = (f & 0x7c00u) != 0x7c00u && (f & 0x7c000000u) != 0x7c000000u;
@@ -667,7 +647,6 @@ __device__ __forceinline__ bool unpack_values(const RawRing& ring, int kb, uint8
       pl.store(row, q, h);
     }
   }
-  return true;
 }
 
 // Query rows of a group as operand rows, by `n` threads.  16 bits: as they are
@@ -807,7 +786,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
     if (QUANT)
       for (int i = 0; i < kMostRaw; ++i) {
         mbar_init(&ctl.raw_full[i], 1);
-        mbar_init(&ctl.raw_empty[i], D / 64);  // warps of a stored tile
+        mbar_init(&ctl.raw_empty[i], S::helpers);
       }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&ctl.q_full[g], q_tma ? 1 : S::helpers);
@@ -1198,17 +1177,22 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           st.next<S::NST>();
           const Stage v = st;
           st.next<S::NST>();
-          const RawRing ring = {sm + S::raw, p.pool.tile_bytes, a.raw_slots, rw.i, rw.phase, ctl.raw_full, ctl.raw_empty, err, quit};
+          const RawRing ring = {sm + S::raw, p.pool.tile_bytes, a.raw_slots, rw.i};
           uint8_t *kt = sm + S::ring + k.i * S::tile, *vt = sm + S::ring + v.i * S::tile;
           float4* scales = reinterpret_cast<float4*>(sm + S::scales) + (tiles & 1) * (kTokens / 2);
           const int w = warp - S::W0;
           ok = __all_sync(0xffffffffu, wait(&ctl.empty[k.i], k.phase ^ 1, err, quit));
           ok = ok && __all_sync(0xffffffffu, wait(&ctl.scales_empty[tiles & 1], (tiles >> 1 & 1) ^ 1, err, quit));
+          // the stored tiles, a lane each: one wait for all of them
+          if (ok && lane < 8) ok = wait(&ctl.raw_full[ring.slot(lane)], rw.phase ^ (rw.i + lane >= a.raw_slots), err, quit);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          ok = p.pool.kb == 8   ? unpack_keys<D, 8, S::helpers>(ring, kt, scales, w, lane)
-               : p.pool.kb == 4 ? unpack_keys<D, 4, S::helpers>(ring, kt, scales, w, lane)
-                                : unpack_keys<D, 2, S::helpers>(ring, kt, scales, w, lane);
-          if (!ok) break;
+          if (p.pool.kb == 8)
+            unpack_keys<D, 8, S::helpers>(ring, kt, scales, w, lane);
+          else if (p.pool.kb == 4)
+            unpack_keys<D, 4, S::helpers>(ring, kt, scales, w, lane);
+          else
+            unpack_keys<D, 2, S::helpers>(ring, kt, scales, w, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -1218,15 +1202,21 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           ++tiles;
           ok = __all_sync(0xffffffffu, wait(&ctl.empty[v.i], v.phase ^ 1, err, quit));
           if (!ok) break;
-          ok = p.pool.vb == 8   ? unpack_values<D, 8, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane)
-               : p.pool.vb == 4 ? unpack_values<D, 4, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane)
-                                : unpack_values<D, 2, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane);
+          if (p.pool.vb == 8)
+            unpack_values<D, 8, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane);
+          else if (p.pool.vb == 4)
+            unpack_values<D, 4, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane);
+          else
+            unpack_values<D, 2, S::helpers>(ring, p.pool.kb, vt, t * kTokens, sg, masked, seen, w, lane);
+          // (every warp gives back every stored tile: it has waited for them all, and none may be filled anew before
+          // it has)
+          __syncwarp();
+          if (lane < 8) mbar_arrive(&ctl.raw_empty[ring.slot(lane)]);
           rw.i += 8;
           if (rw.i >= a.raw_slots) {
             rw.i -= a.raw_slots;
             rw.phase ^= 1;
           }
-          if (!ok) break;
           if (masked) {
             if (me == 0 && seen < kMostBad) {
               sg.bad_tile[seen] = t;
