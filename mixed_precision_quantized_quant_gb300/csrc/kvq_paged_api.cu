@@ -198,7 +198,7 @@ kvq_status attend(kvq_paged* h, int layer, const kvq_paged_batch* batch, const k
   kvq::PagedChunkParams p = {};
   kvq_status st = open_call(h, layer, batch, &p.batch, &p.pool);
   if (st != KVQ_OK) return st;
-  if (n_tokens < 0 || n_tokens > INT_MAX - 31 || (!batch->cu_tokens && n_tokens != batch->num_seqs)) return KVQ_ERR_ARG;
+  if (n_tokens < 0 || n_tokens > INT_MAX - 255 || (!batch->cu_tokens && n_tokens != batch->num_seqs)) return KVQ_ERR_ARG;
   if (window < 0 || !std::isfinite(scale)) return KVQ_ERR_ARG;
   const int hq = h->cfg.num_q_heads, hkv = h->cfg.num_kv_heads, d = h->cfg.head_dim;
   const double sc = scale == 0.0f ? 1.0 / std::sqrt(static_cast<double>(d)) : scale;

@@ -682,47 +682,47 @@ __device__ __forceinline__ void stage_queries(const Launch& a, const Seg& sg, in
     }
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
-    const int row = r1 + k * per + me / U;
-    const uint4* x = xs[k];
-    uint32_t h[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-    if constexpr (QUANT) {
-      float f[16];
+      const int row = r1 + k * per + me / U;
+      const uint4* x = xs[k];
+      uint32_t h[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+      if constexpr (QUANT) {
+        float f[16];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 v = a.bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h[j])) : __half22float2(u32_as_h2(h[j]));
-        f[2 * j] = v.x;
-        f[2 * j + 1] = v.y;
+        for (int j = 0; j < 8; ++j) {
+          const float2 v = a.bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h[j])) : __half22float2(u32_as_h2(h[j]));
+          f[2 * j] = v.x;
+          f[2 * j + 1] = v.y;
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(f[j]));
+#pragma unroll
+        for (int o = 1; o < U; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        int e = top > 0.0f && top < INFINITY ? 14 - ilogbf(top) : 0;
+        e = e > 126 ? 126 : e;
+        const float up = __int_as_float((127 + e) << 23) * (p.alpha < 0.0f ? -1.0f : 1.0f);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          f[j] = __half2float(__float2half_rn(f[j] * up));
+          sum += f[j];
+        }
+#pragma unroll
+        for (int o = 1; o < U; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (u == 0 && row < rows) factors[row] = make_float2(__int_as_float((127 - e) << 23), sum);
+        const auto order = [&](auto bits) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            h[j] = h2_as_u32(__floats2half2_rn(f[code_channel(decltype(bits)::value, 2 * j)], f[code_channel(decltype(bits)::value, 2 * j + 1)]));
+        };
+        if (p.pool.kb == 8)
+          order(std::integral_constant<int, 8>{});
+        else if (p.pool.kb == 4)
+          order(std::integral_constant<int, 4>{});
+        else
+          order(std::integral_constant<int, 2>{});
       }
-      float top = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(f[j]));
-#pragma unroll
-      for (int o = 1; o < U; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      int e = top > 0.0f && top < INFINITY ? 14 - ilogbf(top) : 0;
-      e = e > 126 ? 126 : e;
-      const float up = __int_as_float((127 + e) << 23) * (p.alpha < 0.0f ? -1.0f : 1.0f);
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        f[j] = __half2float(__float2half_rn(f[j] * up));
-        sum += f[j];
-      }
-#pragma unroll
-      for (int o = 1; o < U; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (u == 0 && row < rows) factors[row] = make_float2(__int_as_float((127 - e) << 23), sum);
-      const auto order = [&](auto bits) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          h[j] = h2_as_u32(__floats2half2_rn(f[code_channel(decltype(bits)::value, 2 * j)], f[code_channel(decltype(bits)::value, 2 * j + 1)]));
-      };
-      if (p.pool.kb == 8)
-        order(std::integral_constant<int, 8>{});
-      else if (p.pool.kb == 4)
-        order(std::integral_constant<int, 4>{});
-      else
-        order(std::integral_constant<int, 2>{});
-    }
-    if (row < rows) RunPlace(row, u).store(qs, h);
+      if (row < rows) RunPlace(row, u).store(qs, h);
     }
   }
 }

@@ -35,7 +35,7 @@ def attend(q, k, v, first, last, dtype, scale=0.0, quant=False, parts=None, v_sc
     kk, vv = (x.repeat_interleave(hq // hkv, 0) for x in (k, v))
     ka = kk.abs() if parts is None else parts.repeat_interleave(hq // hkv, 0)
     qq = q.double().transpose(0, 1)
-    at = torch.arange(n)
+    at = torch.arange(n, device=q.device)
     seen = (at >= first[:, None]) & (at <= last[:, None])
     t = (qq @ kk.transpose(1, 2) * sc).masked_fill(~seen, -math.inf)
     top = t.amax(-1, keepdim=True)
@@ -64,7 +64,7 @@ def attend(q, k, v, first, last, dtype, scale=0.0, quant=False, parts=None, v_sc
 def close(got, lse, exp):
     """Every element within its tolerance; infinities and zeros of empty rows exactly."""
     out, l64, tol, ltol = exp
-    got, lse = got.double().cpu(), lse.double().cpu()
+    got, lse = got.double().to(out.device), lse.double().to(out.device)
     err = (got - out).abs()
     bad = ~(err <= tol)
     assert not bool(bad.any()), (int(bad.sum()), float((err / tol)[bad].max()), torch.nonzero(bad)[:4].tolist())
@@ -75,3 +75,38 @@ def close(got, lse, exp):
     lerr = (lse - l64).abs()
     bad = ~((lerr <= ltol) | empty)
     assert not bool(bad.any()), (float((lerr / ltol)[bad].max()), torch.nonzero(bad)[:4].tolist())
+
+
+def dense(cache, layer, table_row, n, is_value):
+    """Rows [hkv, n, d] of a sequence's positions 0 .. n - 1 from the cache's bytes, in 64 bits, and the sizes
+    |scale code| + |zero| that they are made of, all on the GPU."""
+    v = cache.view(layer)
+    kb, vb, P, d, tile = v["k_bits"], v["v_bits"], v["page_size"], v["head_dim"], v["tile_bytes"]
+    off = v["pages"] - cache.buf.data_ptr()
+    data = cache.buf[off:off + cache.num_pages * v["page_stride"]].view(cache.num_pages, cache.Hkv, P // 16, tile)
+    pages = torch.as_tensor(table_row[:-(-n // P)], dtype=torch.int64, device=data.device)
+    t = data[pages].transpose(0, 1).reshape(cache.Hkv, -1, tile)  # [hkv, tiles, bytes]
+    dev = data.device
+    i = torch.arange(16, device=dev)
+    if kb == 16:
+        rows = t.view(cache.dtype).view(cache.Hkv, -1, 2, 16, d)[:, :, int(is_value)]
+        c = torch.arange(d, device=dev)
+        at = (((c // 8)[None] ^ (i & 7)[:, None]) * 8 + c % 8).expand(rows.shape)
+        x = torch.gather(rows, -1, at).reshape(cache.Hkv, -1, d)[:, :n].double()
+        return x, x.abs()
+    row = 2 * (i & 3) + (i >> 2 & 1) + (i & 8)
+    rk, rv = d * kb // 8, d * vb // 8
+    bits, rb, start, place = (vb, rv, 16 * rk, i) if is_value else (kb, rk, 0, row)
+    raw = t[..., start:start + 16 * rb].reshape(cache.Hkv, -1, 16, rb)[:, :, place]
+    b = torch.arange(rb, device=dev)
+    if is_value:
+        xor = (i & 3) * 32 if rb == 128 else (i >> 1 & 1) * 32 if rb == 64 else i * 0
+    else:
+        xor = (row & 1) * 64 if rb == 128 else row * 0
+    raw = torch.gather(raw, -1, (b[None] ^ xor[:, None]).expand(raw.shape))
+    sh = torch.arange(8 // bits, device=dev) * bits
+    code = ((raw.int()[..., None] >> sh) & ((1 << bits) - 1)).reshape(cache.Hkv, -1, 16, d).double()
+    sz = t[..., 16 * (rk + rv):].contiguous().view(torch.float16).view(cache.Hkv, -1, 16, 4)[:, :, row].double()
+    s, z = (sz[..., 2 * int(is_value) + k:2 * int(is_value) + k + 1] for k in (0, 1))
+    x, size = code * s + z, (code * s).abs() + z.abs()
+    return x.reshape(cache.Hkv, -1, d)[:, :n], size.reshape(cache.Hkv, -1, d)[:, :n]
