@@ -1,5 +1,60 @@
 // Paged cache: causal attention of runs of new tokens, over the pages or over
 // rows of their own (prompts).
+//
+// Mathematics.  For a row at position p and the positions t that it sees, with
+// x_t = scale log2(e) q.k_t, a running maximum m, l = sum 2^(x_t - m) and o = sum
+// 2^(x_t - m) v_t, the output is o / l, the log-sum-exp (m + log2 l) ln 2.
+// Quantized keys k = s c + z, of codes c less the middle of their range, give
+// q.k = s (q.c) + z sum(q): the codes go into the tensor cores as exact fp16
+// numbers, s and z are one multiply-add a score.  Values are dequantized to fp16.
+//
+// Roundings to 16 bits, beside the inputs' and the output's: the weights, to the
+// type that the values are multiplied in (bf16; fp16, where they are held 2^7
+// above 1: see kRoom16), and quantized values, to fp16.  Scores, maxima, sums and
+// outputs are held in fp32.  Measured against 64 bits (relative, 2-norm): bf16
+// 2.1e-3 where the output's own rounding alone makes 1.7e-3; fp16 2.7e-4 (2.1e-4);
+// fp16 over K8V4 3.3e-4; log-sum-exp below 1e-6.
+//
+// Bound.  Every byte of the cache is read once for up to 256 rows (token, query
+// head) of a kv head, 4 D operations each: with many new tokens the tensor rate is
+// the bound, with few the copy rate.
+//
+// Work split.  An item is one or two query tiles of kM / gqa tokens of one
+// (sequence, kv head), all its query heads together.  The tiles of keys of all
+// items in a row, and kStart more for each item, are cut into equal ranges, one
+// a CTA of one wave; a cut near an item's end moves there (see cut_at).  An item
+// that a cut divides leaves partial results, which a second kernel joins in a
+// fixed order.  Every CTA works its range out from the lengths by itself, so
+// that nothing is counted across CTAs and the workspace needs no clearing.
+//
+// A CTA holds one SM: 128 softmax threads a query tile (a thread a row); a warp
+// that plans and loads; a warp a query tile that multiplies (tcgen05, scores and
+// outputs in tensor memory, weights written over their scores); helpers.  16-bit
+// rows come by tensor maps, 128 tokens of keys and of values at a time in a ring;
+// the pages' swizzle is the one that the products take.  Codes come as they are
+// stored into a ring of their own, and four or eight warps unpack them into the
+// products' operands.  A segment (an item, or its part in the CTA's range) is
+// handed to all by a descriptor in shared memory.
+//
+// Masks.  Scores that a row may not see are -infinity before their maximum is
+// taken.  Their weights are 0, but 0 times an infinite value or NaN is NaN: in tiles
+// where some row is masked such values are set to 0 before the product (a warp looks
+// through them, or finds them unpacking), and added afterwards for the rows that
+// see them (add_bad).  So nothing that a row does not see reaches it, and what
+// memory holds behind a sequence's end does not matter.
+//
+// Measured (GB300, one call after another; peaks 6695 GB/s, 1920 TFLOP/s bf16):
+// 2,048 rows over 10,240 tokens, 32/8 heads, bf16 232 us, 1.33 PFLOP/s (69%); a
+// prompt of 8,192, 64/8, fp16 853 us, 1.29 PFLOP/s; 12 prompts of up to 2,047, 32/8,
+// bf16 280 us (46%); 5 rows of each of 16 sequences of up to 4,096 tokens, bf16 54
+// us (58% of the copy rate).  A tile of 128 tokens for two query tiles takes
+// about 3,150 clocks, 2,048 of them products: the rest is the way round (scores,
+// their softmax, 1,300 clocks, and five waits of 200 to 300, which is what one
+// costs beside products that take the shared memory's whole bandwidth).
+// Codes: 4 x 1,023 rows over 5,119 tokens, 32/8, K8V4 308 us, 0.65 PFLOP/s; 8 rows
+// of each of 8 sequences of up to 32,768, 64/8, K4V2 198 us.  They are bound by
+// the same chain with more in it: the scales, which every row reads from shared
+// memory for every score, and the unpacking.
 #pragma once
 
 #include <cuda.h>
@@ -20,7 +75,9 @@ using rows::fma2;
 
 constexpr int kTokens = 128;  // tokens of a key or value tile
 constexpr int kM = 128;       // rows of a query tile: the (token, query head) pairs of kM / gqa tokens of one kv head
-constexpr int kStart = 2;     // what starting an item counts, in tiles
+// What starting an item counts when the work is cut, in tiles (2 the best of 2, 3 and 5 for pieces, checks and prompts,
+// by 2 to 4%).
+constexpr int kStart = 2;
 constexpr int kPlan = 1024;   // entries of the plan in shared memory
 constexpr int kMostBad = 8;   // masked tiles of a segment (see masked_tile)
 constexpr int kSlots = 2;     // segments under way
@@ -270,9 +327,9 @@ struct Launch {
 
 // ---------------------------------------------------------------- planning
 
-// Weight (tiles, and kStart an item) of a sequence's items of one kv head, by a warp.
 __device__ __forceinline__ int items_of(int m, int T) { return m ? (m - 1) / T + 1 : 0; }
 
+// Weight (tiles, and kStart an item) of a sequence's items of one kv head, by a warp.
 __device__ __forceinline__ int64_t span_weight(const Span& s, int T, int window, int lane) {
   const int q = items_of(s.m, T);
   int64_t w = 0;
@@ -339,6 +396,7 @@ __device__ __forceinline__ void walk_start(const PagedChunkParams& p, int T, con
   const int64_t total = __shfl_sync(0xffffffffu, end, 31);
   int64_t quota = (total + grid - 1) / grid;
   if (quota < 3 * kStart) quota = 3 * kStart;
+  // within a sixteenth of a CTA's work (an eighth: pieces 5% slower; a thirty-second: prompts 3%)
   w.tol = static_cast<int>(quota / 16 < kStart + 1 ? kStart + 1 : quota / 16 > 64 ? 64 : quota / 16);
   w.b0 = quota * cta;
   w.b1 = w.b0 + quota < total ? w.b0 + quota : total;
@@ -1043,6 +1101,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
 #pragma unroll
         for (int k = 0; k < kTokens / 32; ++k) umma_f16_ts(tm + S::tO + D * g, pt + 8 * k, dv + ((2048 * k) >> 4), idO, !first || k > 0);
       };
+      // (by all lanes: with one lane of a barrier each, several at once, all forms were 5 to 65% slower)
       const auto ready = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase, err, quit)) != 0; };
       const auto my_turn = [&]() {
         if (NQ == 1) return true;
@@ -1316,7 +1375,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             qph ^= 1;
             if (!ok) break;
             const float2 fq = reinterpret_cast<const float2*>(sm + S::factors)[g * kM + r];
-            alpha *= fq.x;
+            alpha = fmaxf(alpha * fq.x, 1.17549435e-38f);  // (times -infinity it stays that)
             qsum = fq.y;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.q_empty[g]);
@@ -1336,9 +1395,10 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               if (lane < 2) mbar_arrive(&ctl.p_full[buf][lane]);
               continue;
             }
-            // The scores are read twice, 64 columns at a time, for their maximum and for the weights: held in
-            // registers the loops would be unrolled over all 128, and the instructions of all roles no longer
-            // fit the instruction cache (a quarter to a half of the time went into that).
+            // The scores are read twice, 32 columns at a time, for their maximum and for the weights.  Held in
+            // registers, every loop over them would be unrolled over all 128, and the code of all roles no longer
+            // fits the instruction cache: with codes half of the time went into that (8 warps' worth of 16-bit
+            // prompts 359 -> 300 us, K8V4 pieces 674 -> 431 us).
             const int tb = (t0 + i) * kTokens;
             const bool masked = tb + kTokens - 1 > first_lim || (p.window && tb <= last_lim - p.window);
             const int a0 = low - tb, a1 = lim - tb;  // columns a0 .. a1 are seen
@@ -1374,7 +1434,6 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
                 mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(x[c + 2])), __uint_as_float(x[c + 3]));
               }
             };
-            constexpr bool ROLL = QUANT;
             // (no load is under way across a branch: its registers might be moved before it is done)
             uint32_t xa[32], xb[32];
             if (QUANT || masked) {
@@ -1442,35 +1501,32 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               }
               tmem_st16(tS + c0 / 2, w);
             };
-            if constexpr (ROLL) {
-#pragma unroll 1
-              for (int c0 = 0; c0 < kTokens; c0 += 64) {
-#pragma unroll 1
-                for (int c1 = c0; c1 < c0 + 64; c1 += 32) {
-                  tmem_ld32(tS + c1, xa);
-                  tmem_ld_wait(xa);
-                  weigh(xa, c1);
-                }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_full[buf][c0 / 64]);
-              }
-            } else {
-            tmem_ld32(tS, xa);
-#pragma unroll
-            for (int c0 = 0; c0 < kTokens; c0 += 64) {
-              tmem_ld_wait(xa);
-              tmem_ld32(tS + c0 + 32, xb);
-              weigh(xa, c0);
-              tmem_ld_wait(xb);
-              if (c0 == 0) tmem_ld32(tS + 64, xa);
-              weigh(xb, c0 + 32);
+            const auto ready = [&](int part) {  // half of the weights are there
               tmem_st_wait();
               tc_fence_before_sync();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl.p_full[buf][c0 / 64]);
-            }
+              if (lane == 0) mbar_arrive(&ctl.p_full[buf][part]);
+            };
+            if constexpr (QUANT) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < kTokens; c0 += 32) {
+                tmem_ld32(tS + c0, xa);
+                tmem_ld_wait(xa);
+                weigh(xa, c0);
+                if (c0 % 64) ready(c0 / 64);
+              }
+            } else {
+              tmem_ld32(tS, xa);
+#pragma unroll
+              for (int c0 = 0; c0 < kTokens; c0 += 64) {
+                tmem_ld_wait(xa);
+                tmem_ld32(tS + c0 + 32, xb);
+                weigh(xa, c0);
+                tmem_ld_wait(xb);
+                if (c0 == 0) tmem_ld32(tS + 64, xa);
+                weigh(xb, c0 + 32);
+                ready(c0 / 64);
+              }
             }
             float s0, s1, s2, s3;
             f2_get(sum[0], s0, s1);

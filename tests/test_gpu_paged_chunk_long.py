@@ -174,3 +174,56 @@ def test_lengths_that_change_under_a_call(kb, vb):
     b.batch._keep[1].copy_(good)
     cu.copy_(ends)
     assert torch.equal(b.run()[0], want)
+
+
+def test_layers_of_one_cache():
+    # every layer has its own widths and its own place in the buffer
+    layers = [(16, 16), (4, 2), (16, 16), (8, 8)]
+    c = K.KVQPagedCache(layers, 8, 2, 128, 32, 12, dtype=torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    batch = K.PagedBatch(torch.randperm(12, generator=g, device="cuda").int().view(2, 6), _i32([150, 190]), _i32([0, 150, 340]))
+    rows = [[torch.randn(340, h, 128, generator=g, device="cuda").bfloat16() for h in (8, 2, 2)] for _ in layers]
+    for layer, (q, k, v) in enumerate(rows):
+        c.append(layer, batch, k, v)
+    for layer, (q, k, v) in enumerate(rows):
+        got, lse = c.chunk_attn(layer, batch, q, return_lse=True)
+        for b, (a, n) in enumerate(((0, 150), (150, 190))):
+            kk, size = C.dense(c, layer, batch._keep[0][b], n, False)
+            vv, _ = C.dense(c, layer, batch._keep[0][b], n, True)
+            last = torch.arange(n, device="cuda")
+            C.close(got[a:a + n], lse[a:a + n], C.attend(q[a:a + n], kk, vv, 0 * last, last, c.dtype, 0.0, layers[layer][0] != 16, size))
+    assert c.device_error() == 0
+
+
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 8)])
+def test_pages_past_four_gibibytes(kb, vb):
+    pages = 20_000 if kb != 16 else 10_000  # of 8 heads: 0.26 and 0.5 MiB each
+    c = K.KVQPagedCache([(kb, vb)], 8, 8, 128, 128, pages, dtype=torch.float16)
+    assert c.nbytes > 4 << 30
+    g = torch.Generator(device="cuda").manual_seed(0)
+    batch = K.PagedBatch(_i32([[pages - 1, 0, pages - 2, pages // 2]]), _i32([450]), _i32([0, 450]))
+    q, k, v = (torch.randn(450, 8, 128, generator=g, device="cuda").half() for _ in range(3))
+    c.append(0, batch, k, v)
+    got, lse = c.chunk_attn(0, batch, q, return_lse=True)
+    few = K.KVQPagedCache([(kb, vb)], 8, 8, 128, 128, 4, dtype=torch.float16)
+    near = K.PagedBatch(_i32([[0, 1, 2, 3]]), _i32([450]), _i32([0, 450]))
+    few.append(0, near, k, v)
+    e, le = few.chunk_attn(0, near, q, return_lse=True)
+    assert torch.equal(got, e) and torch.equal(lse, le) and c.device_error() == 0
+
+
+def test_calls_side_by_side():
+    # one cache, calls on three streams at once: each as by itself
+    big = [Big([2500, 700], [300, 9], 8, 4, 8, 2, 128, 32, "fp16", seed=1), Big([3000, 64, 900], [4, 2, 1], 16, 16, 8, 2, 128, 32, "fp16", seed=2)]
+    alone = [b.run() for b in big]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append([b.cache.chunk_attn(0, b.batch, b.q, return_lse=True) for b in big])
+    torch.cuda.synchronize()
+    for pair in got:
+        for (o, l), (e, le) in zip(pair, alone):
+            assert torch.equal(o, e) and torch.equal(l, le)
