@@ -1552,7 +1552,9 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
         // ---- the rows' results
         const int64_t at = (static_cast<int64_t>(sg.row) + g * a.T + my_tok) * p.hkv * p.gqa + sg.kvh * p.gqa + my_head;
         const bool fine = !sg.dirty && !__any_sync(0xffffffffu, l == 0.0f);
-        if (sg.whole) {
+        if (idle) {
+          // nothing of its own
+        } else if (sg.whole) {
           const float inv = l != 0.0f ? __fdividef(1.0f, l) : 0.0f;
           uint8_t* dst = static_cast<uint8_t*>(p.out) + at * D * 2;
           const auto write = [&](const uint32_t (&o)[32], int c) {
@@ -1595,7 +1597,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
           // m, l of every row, then the outputs, four channels of all rows together
           float* part = reinterpret_cast<float*>(p.ws + a.partials) + static_cast<int64_t>(sg.slot) * a.slot_rows * (D + 2);
           const int rr = kM * g + r;
-          const bool fits = rr < a.slot_rows && in_range(part, a.slot_rows * (D + 2) * 4, p.ws, p.ws_hi, err);
+          const bool fits = live && rr < a.slot_rows && in_range(part, a.slot_rows * (D + 2) * 4, p.ws, p.ws_hi, err);
           if (fits) {
             part[rr] = m;
             part[a.slot_rows + rr] = l;
