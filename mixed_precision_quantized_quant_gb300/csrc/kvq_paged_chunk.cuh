@@ -40,19 +40,19 @@
 // taken.  Their weights are 0, but 0 times an infinite value or NaN is NaN: in tiles
 // where some row is masked such values are set to 0 before the product (a warp looks
 // through them, or finds them unpacking), and added afterwards for the rows that
-// see them (add_bad).  So nothing that a row does not see reaches it, and what
+// see them (bad_sum).  So nothing that a row does not see reaches it, and what
 // memory holds behind a sequence's end does not matter.
 //
 // Measured (GB300, one call after another; peaks 6695 GB/s, 1920 TFLOP/s bf16):
-// 2,048 rows over 10,240 tokens, 32/8 heads, bf16 232 us, 1.33 PFLOP/s (69%); a
-// prompt of 8,192, 64/8, fp16 853 us, 1.29 PFLOP/s; 12 prompts of up to 2,047, 32/8,
-// bf16 280 us (46%); 5 rows of each of 16 sequences of up to 4,096 tokens, bf16 54
-// us (58% of the copy rate).  A tile of 128 tokens for two query tiles takes
+// 2,048 rows over 10,240 tokens, 32/8 heads, bf16 230 us, 1.34 PFLOP/s (70%); a
+// prompt of 8,192, 64/8, fp16 851 us, 1.29 PFLOP/s; 12 prompts of up to 2,047, 32/8,
+// bf16 280 us (46%); 5 rows of each of 16 sequences of up to 4,096 tokens, bf16 52
+// us (60% of the copy rate).  A tile of 128 tokens for two query tiles takes
 // about 3,150 clocks, 2,048 of them products: the rest is the way round (scores,
 // their softmax, 1,300 clocks, and five waits of 200 to 300, which is what one
 // costs beside products that take the shared memory's whole bandwidth).
-// Codes: 4 x 1,023 rows over 5,119 tokens, 32/8, K8V4 308 us, 0.65 PFLOP/s; 8 rows
-// of each of 8 sequences of up to 32,768, 64/8, K4V2 198 us.  They are bound by
+// Codes: 4 x 1,023 rows over 5,119 tokens, 32/8, K8V4 305 us, 0.65 PFLOP/s; 8 rows
+// of each of 8 sequences of up to 32,768, 64/8, K4V2 197 us.  They are bound by
 // the same chain with more in it: the scales, which every row reads from shared
 // memory for every score, and the unpacking.
 #pragma once
@@ -221,7 +221,7 @@ struct Ctl {
   uint64_t looked[8];           // masked values of the stage have been looked through
   uint64_t raw_full[kMostRaw], raw_empty[kMostRaw];
   // one for each query tile, or where there is one for each of its score tiles, of which a role may be a tile ahead of
-  // another: a wait tells a phase from the one before only.
+  // another (a wait can only tell a phase from the one before).
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2];  // (weights are ready in two halves)
   uint64_t scales_full[2], scales_empty[2];  // of even and odd tiles: written, read by all softmax warps
   uint64_t turn[2];             // of a query tile's products
@@ -479,11 +479,15 @@ __device__ __forceinline__ const uint8_t* value_at(const PagedChunkParams& p, co
 }
 
 // The masked tiles' values that are not finite were left out of the products
-// (times a weight of 0 they would be NaN); the rows that see them get them here.
-// A quantized row whose scale or zero is no number is none in all channels.
+// (times a weight of 0 they would be NaN); their sum in channel ch over the
+// positions first .. last that a row sees, 0 where there are none.  A quantized
+// row whose scale or zero is no number is none in all channels.
 template <typename T, int D, bool PROMPT, bool QUANT>
-__device__ __forceinline__ void add_bad(const PagedChunkParams& p, const Seg& sg, int first, int last, int c0, float (&o)[32]) {
+__device__ __forceinline__ float bad_sum(const PagedChunkParams& p, const Seg& sg, int first, int last, int ch) {
+  float sum = 0.0f;
+#pragma unroll 1
   for (int i = 0; i < sg.bad_tiles && i < kMostBad; ++i)
+#pragma unroll 1
     for (int b = 0; b < kTokens; ++b) {
       if (!sg.bad[i][b / 32]) {
         b |= 31;
@@ -491,22 +495,16 @@ __device__ __forceinline__ void add_bad(const PagedChunkParams& p, const Seg& sg
       }
       const int t = sg.bad_tile[i] * kTokens + b;
       if (!(sg.bad[i][b / 32] >> (b % 32) & 1) || t < first || t > last) continue;
-      const uint8_t* v = QUANT ? nullptr : value_at<PROMPT>(p, sg, t);
-      if (!QUANT && !v) continue;
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const int ch = c0 + c;
-        if (QUANT) {
-          o[c] = __int_as_float(0x7fffffff);
-          continue;
-        }
-        const T* x = PROMPT ? reinterpret_cast<const T*>(v) + ch
-                            : reinterpret_cast<const T*>(v + 32 * D + (t % kTile) * 2 * D +
-                                                         16 * tile_chunk16(ch / 8, t % kTile) + ch % 8 * 2);
-        const float f = Num<T>::to(*x);
-        if (!isfinite(f)) o[c] += f;
-      }
+      if (QUANT) return __int_as_float(0x7fffffff);
+      const uint8_t* v = value_at<PROMPT>(p, sg, t);
+      if (!v) continue;
+      const T* x = PROMPT ? reinterpret_cast<const T*>(v) + ch
+                          : reinterpret_cast<const T*>(v + 32 * D + (t % kTile) * 2 * D +
+                                                       16 * tile_chunk16(ch / 8, t % kTile) + ch % 8 * 2);
+      const float f = Num<T>::to(*x);
+      if (!isfinite(f)) sum += f;
     }
+  return sum;
 }
 
 // ---------------------------------------------------------------- codes
@@ -1397,8 +1395,8 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             }
             // The scores are read twice, 32 columns at a time, for their maximum and for the weights.  Held in
             // registers, every loop over them would be unrolled over all 128, and the code of all roles no longer
-            // fits the instruction cache: with codes half of the time went into that (8 warps' worth of 16-bit
-            // prompts 359 -> 300 us, K8V4 pieces 674 -> 431 us).
+            // fits the instruction cache: with codes half of the time went into that (12 prompts of
+            // up to 2,047 tokens, bf16, 359 -> 300 us; K8V4 pieces 674 -> 431 us).
             const int tb = (t0 + i) * kTokens;
             const bool masked = tb + kTokens - 1 > first_lim || (p.window && tb <= last_lim - p.window);
             const int a0 = low - tb, a1 = lim - tb;  // columns a0 .. a1 are seen
@@ -1551,22 +1549,21 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
         if (!ok) break;
         // ---- the rows' results
         const int64_t at = (static_cast<int64_t>(sg.row) + g * a.T + my_tok) * p.hkv * p.gqa + sg.kvh * p.gqa + my_head;
-        const bool fine = !sg.dirty && !__any_sync(0xffffffffu, l == 0.0f);
+        const bool spoilt = sg.dirty && live && l != 0.0f;
         if (idle) {
           // nothing of its own
         } else if (sg.whole) {
           const float inv = l != 0.0f ? __fdividef(1.0f, l) : 0.0f;
           uint8_t* dst = static_cast<uint8_t*>(p.out) + at * D * 2;
-          const auto write = [&](const uint32_t (&o)[32], int c) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_ld_wait(o);
             float y[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
+            for (int k = 0; k < 32; ++k) y[k] = l != 0.0f ? __uint_as_float(o[k]) * inv : 0.0f;
             to_channels<QUANT>(p.pool.vb, y);
-            if (!fine) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = l != 0.0f ? y[k] : 0.0f;
-              if (sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
-            }
             uint32_t w[2][8];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -1580,17 +1577,21 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               store32(dst + 2 * c, wide_out, w[0]);
               store32(dst + 2 * c + 32, wide_out, w[1]);
             }
-          };
-#pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            uint32_t o0[32], o1[32];
-            tmem_ld32(tO + c, o0);
-            tmem_ld32(tO + c + 32, o1);
-            tmem_ld_wait(o0);
-            tmem_ld_wait(o1);
-            write(o0, c);
-            write(o1, c + 32);
           }
+          if (spoilt)
+#pragma unroll 1
+            for (int c = 0; c < D; ++c) {
+              const float f = bad_sum<T, D, PROMPT, QUANT>(p, sg, low, lim, c);
+              uint16_t* x = reinterpret_cast<uint16_t*>(dst) + c;
+              if (f != 0.0f) {
+                if (QUANT && a.bf16) {
+                  *x = 0x7fff;  // (NaN)
+                } else {
+                  T* y = reinterpret_cast<T*>(x);
+                  *y = Num<T>::from(Num<T>::to(*y) + f);
+                }
+              }
+            }
           if (p.lse && live)
             p.lse[at] = l == 0.0f ? -INFINITY : ((m - Fmt<T>::room) + log2f(l)) * 0.69314718055994531f;
         } else {
@@ -1602,6 +1603,7 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             part[rr] = m;
             part[a.slot_rows + rr] = l;
           }
+          float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows) + rr;
           if (nt > 0) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -1612,14 +1614,18 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
 #pragma unroll
               for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]);
               to_channels<QUANT>(p.pool.vb, y);
-              if (!fine && sg.dirty && l != 0.0f) add_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, c, y);
               if (fits) {
-                float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows) + rr;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                   dst[(c / 4 + k) * a.slot_rows] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
               }
             }
+            if (spoilt && fits)
+#pragma unroll 1
+              for (int c = 0; c < D; ++c) {
+                const float f = bad_sum<T, D, PROMPT, QUANT>(p, sg, low, lim, c);
+                if (f != 0.0f) reinterpret_cast<float*>(dst + c / 4 * a.slot_rows)[c % 4] += f;
+              }
           }
         }
         tc_fence_before_sync();
