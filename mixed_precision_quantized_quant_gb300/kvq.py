@@ -603,8 +603,11 @@ class HeadNorm:
             if ptr[i] % 16 or stride[i] % 8:
                 raise ValueError(f"{name}'s heads must be 16-byte aligned")
         self.args = HeadNormArgs(ptr[0], ptr[1], stride[0], stride[1], eps)
+        self._fits = None  # the last caches' device, dtype and heads that the weights were found to fit
 
     def _check(self, device, dtype, hq: int, hkv: int, d: int) -> None:
+        if self._fits == (device, dtype, hq, hkv, d):
+            return
         for w, name, heads in zip(self.weights, ("q_weight", "k_weight"), (hq, hkv)):
             if w is None:
                 continue
@@ -612,6 +615,7 @@ class HeadNorm:
                 raise ValueError(f"{name} must be {dtype} on {device}, got {w.dtype} on {w.device}")
             if tuple(w.shape) not in ((d,), (heads, d)):
                 raise ValueError(f"{name} has shape {tuple(w.shape)}, expected {(d,)} or {(heads, d)}")
+        self._fits = device, dtype, hq, hkv, d
 
 
 def rotation_table(rows: int, dim: int, base: float = 10000.0, device="cuda"):

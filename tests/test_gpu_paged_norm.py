@@ -180,6 +180,18 @@ def test_norm_refusals():
     assert np.array_equal(c.download(), before) and c.cache.device_error() == 0
 
 
+def test_norm_of_one_cache_is_refused_by_another_that_it_does_not_fit():
+    one = Case([20, 5], kb=4, vb=4, d=64, hq=4, hkv=2)
+    norm = K.HeadNorm(_w(one, 4), _w(one, 2))
+    for _ in range(2):  # fitting calls in between change nothing
+        one.cache.append(0, one.batch, one.rows(2, 2), one.rows(2, 2), norm=norm)
+        for kw in (dict(hq=4, hkv=4), dict(hq=8, hkv=2)):
+            two = Case([20, 5], kb=4, vb=4, d=64, **kw)
+            with pytest.raises(ValueError):
+                two.cache.append(0, two.batch, two.rows(2, two.hkv), two.rows(2, two.hkv), norm=norm)
+    assert one.cache.device_error() == 0
+
+
 @pytest.mark.parametrize("kb,vb", [(16, 16), (8, 4)])
 def test_prompt_then_chunk_then_decode(kb, vb):
     # as a server runs them: prompts admitted, pieces appended and attended, then single tokens; the attention of every
