@@ -40,7 +40,7 @@
 // taken.  Their weights are 0, but 0 times an infinite value or NaN is NaN: in tiles
 // where some row is masked such values are set to 0 before the product (a warp looks
 // through them, or finds them unpacking), and added afterwards for the rows that
-// see them (bad_sum).  So nothing that a row does not see reaches it, and what
+// see them (for_bad).  So nothing that a row does not see reaches it, and what
 // memory holds behind a sequence's end does not matter.
 //
 // Measured (GB300, one call after another; peaks 6695 GB/s, 1920 TFLOP/s bf16):
@@ -479,12 +479,12 @@ __device__ __forceinline__ const uint8_t* value_at(const PagedChunkParams& p, co
 }
 
 // The masked tiles' values that are not finite were left out of the products
-// (times a weight of 0 they would be NaN); their sum in channel ch over the
-// positions first .. last that a row sees, 0 where there are none.  A quantized
-// row whose scale or zero is no number is none in all channels.
-template <typename T, int D, bool PROMPT, bool QUANT>
-__device__ __forceinline__ float bad_sum(const PagedChunkParams& p, const Seg& sg, int first, int last, int ch) {
-  float sum = 0.0f;
+// (times a weight of 0 they would be NaN): add(channel, value) for each at the
+// positions first .. last that a row sees.  A quantized row whose scale or zero
+// is no number is none in all channels.  Tokens outside, channels inside: what
+// only other rows see, or none, costs a row a test a token.
+template <typename T, int D, bool PROMPT, bool QUANT, typename Add>
+__device__ __forceinline__ void for_bad(const PagedChunkParams& p, const Seg& sg, int first, int last, Add add) {
 #pragma unroll 1
   for (int i = 0; i < sg.bad_tiles && i < kMostBad; ++i)
 #pragma unroll 1
@@ -495,16 +495,22 @@ __device__ __forceinline__ float bad_sum(const PagedChunkParams& p, const Seg& s
       }
       const int t = sg.bad_tile[i] * kTokens + b;
       if (!(sg.bad[i][b / 32] >> (b % 32) & 1) || t < first || t > last) continue;
-      if (QUANT) return __int_as_float(0x7fffffff);
-      const uint8_t* v = value_at<PROMPT>(p, sg, t);
-      if (!v) continue;
-      const T* x = PROMPT ? reinterpret_cast<const T*>(v) + ch
-                          : reinterpret_cast<const T*>(v + 32 * D + (t % kTile) * 2 * D +
-                                                       16 * tile_chunk16(ch / 8, t % kTile) + ch % 8 * 2);
-      const float f = Num<T>::to(*x);
-      if (!isfinite(f)) sum += f;
+      const uint8_t* v = QUANT ? nullptr : value_at<PROMPT>(p, sg, t);
+      if (!QUANT && !v) continue;
+#pragma unroll 1
+      for (int ch = 0; ch < D; ++ch) {
+        if (QUANT) {
+          add(ch, __int_as_float(0x7fffffff));
+          continue;
+        }
+        const T* x = PROMPT ? reinterpret_cast<const T*>(v) + ch
+                            : reinterpret_cast<const T*>(v + 32 * D + (t % kTile) * 2 * D +
+                                                         16 * tile_chunk16(ch / 8, t % kTile) + ch % 8 * 2);
+        const float f = Num<T>::to(*x);
+        if (!isfinite(f)) add(ch, f);
+      }
+      if (QUANT) return;
     }
-  return sum;
 }
 
 // ---------------------------------------------------------------- codes
@@ -1579,19 +1585,15 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
             }
           }
           if (spoilt)
-#pragma unroll 1
-            for (int c = 0; c < D; ++c) {
-              const float f = bad_sum<T, D, PROMPT, QUANT>(p, sg, low, lim, c);
+            for_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, [&](int c, float f) {
               uint16_t* x = reinterpret_cast<uint16_t*>(dst) + c;
-              if (f != 0.0f) {
-                if (QUANT && a.bf16) {
-                  *x = 0x7fff;  // (NaN)
-                } else {
-                  T* y = reinterpret_cast<T*>(x);
-                  *y = Num<T>::from(Num<T>::to(*y) + f);
-                }
+              if (QUANT && a.bf16) {
+                *x = 0x7fff;  // (NaN)
+              } else {  // (no rounding: the sum is not finite)
+                T* y = reinterpret_cast<T*>(x);
+                *y = Num<T>::from(Num<T>::to(*y) + f);
               }
-            }
+            });
           if (p.lse && live)
             p.lse[at] = l == 0.0f ? -INFINITY : ((m - Fmt<T>::room) + log2f(l)) * 0.69314718055994531f;
         } else {
@@ -1621,11 +1623,9 @@ __global__ void __launch_bounds__(Shape<D, NQ, QUANT>::threads, 1) paged_chunk_k
               }
             }
             if (spoilt && fits)
-#pragma unroll 1
-              for (int c = 0; c < D; ++c) {
-                const float f = bad_sum<T, D, PROMPT, QUANT>(p, sg, low, lim, c);
-                if (f != 0.0f) reinterpret_cast<float*>(dst + c / 4 * a.slot_rows)[c % 4] += f;
-              }
+              for_bad<T, D, PROMPT, QUANT>(p, sg, low, lim, [&](int c, float f) {
+                reinterpret_cast<float*>(dst + c / 4 * a.slot_rows)[c % 4] += f;
+              });
           }
         }
         tc_fence_before_sync();
